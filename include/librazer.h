@@ -299,6 +299,107 @@ razer_status razer_weight_offset_sse(const void* w, razer_dtype w_dt, int64_t ro
  * workspace is optional there. */
 size_t razer_workspace_bytes(int op, int64_t m, int64_t n, int64_t k);
 
+/* ---- microscaled 4-bit tensors (MXFP4) ----------------------------------------
+ *
+ * THE FORMAT (Open Compute Project, "Microscaling Formats (MX) Specification
+ * v1.0", MXFP4).  X[rows, cols], row-major, cols % 32 == 0, is cut into
+ * 32-element blocks along each row, each with one E8M0 scale byte:
+ *
+ *   byte   = floor(log2(amax_block)) - 2 + 127, at least 0 (a zero block: 0);
+ *            its value is 2^(byte - 127)
+ *   code_j = FP4-E2M1 of x_j / 2^(byte - 127): sign bit 3 (a zero keeps its
+ *            sign), magnitude index 0..7 of {0, 0.5, 1, 1.5, 2, 3, 4, 6},
+ *            nearest-even, saturating at 6
+ *
+ * A block with an infinity or NaN gets byte 255 (NaN) and codes 0: all its
+ * values, and every product they enter, are NaN.  Unlike the RaZeR formats there
+ * is no tensor scale and no special value: the matrix units read codes and
+ * scales as they are stored, and both operands of a product are in 4 bits. */
+typedef struct razer_mx {
+  int64_t rows;    /* >= 0 */
+  int64_t cols;    /* >= 0, multiple of 32 */
+  uint8_t* codes;  /* device, rows*cols/2 bytes, 16-byte aligned, even column in the low half */
+  uint8_t* scales; /* device, rows*cols/32 bytes, row-major */
+} razer_mx;
+
+/* Encode x[out->rows, out->cols] (F32, F16 or BF16; x_stride elements from row
+ * to row, a multiple of 16 bytes).  No workspace.  At most 2^34 elements
+ * (RAZER_E_UNSUPPORTED above). */
+razer_status razer_mx_quantize(const void* x, razer_dtype x_dt, int64_t x_stride, const razer_mx* out,
+                               void* stream);
+
+/* Encode silu(g) * u = g * u / (1 + exp(-g)), the input of an MLP's down
+ * projection: gu is [out->rows, 2 * out->cols], g its first out->cols columns
+ * and u the others (the output of one product with the gate and up weights
+ * stacked).  The fp32 product is packed directly. */
+razer_status razer_mx_quantize_gated(const void* gu, razer_dtype gu_dt, int64_t gu_stride, const razer_mx* out,
+                                     void* stream);
+
+/* Decode to out[rows, cols]: value(code) * 2^(byte - 127), exact in fp32; F16
+ * and BF16 round it to nearest even. */
+razer_status razer_mx_dequant(const razer_mx* t, void* out, razer_dtype out_dt, void* stream);
+
+/* y[M, N] = x[M, K] * w[N, K]^T of two MXFP4 tensors, M from one token up; fp32
+ * accumulation, one rounding to y_dt.  K == 0 is RAZER_E_UNSUPPORTED.  ws: at
+ * least razer_mx_workspace_bytes(M, N, K, 0) bytes, 16-byte aligned (may be 0
+ * -> NULL). */
+razer_status razer_mx_gemm(const razer_mx* x, const razer_mx* w, void* y, razer_dtype y_dt, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Largest expert count of razer_mx_gemm_grouped. */
+#define RAZER_MX_MAX_EXPERTS 4096
+
+/* The products of a mixture of experts: w stacks `experts` weights [N, K], N =
+ * w->rows / experts, and y[M, N] takes rows offsets[e] .. offsets[e + 1] - 1
+ * through weight e:
+ *
+ *   y[r] = x[x_rows[r]] * w_e^T        (x[r] where x_rows is NULL: M = x->rows)
+ *
+ * offsets: device, experts + 1 ascending row numbers; x_rows: device, M row
+ * numbers of x.  Neither is read on the host, so a router's output can be used
+ * without waiting for it and the call can be captured.  Runs of no rows are
+ * allowed; rows of y outside every run are left as they were; a row number
+ * outside x (such as -1, padding) makes its row of y zero.  Offsets outside
+ * [0, M] are clamped.  ws: razer_mx_workspace_bytes(M, N, K, experts) bytes,
+ * 16-byte aligned. */
+razer_status razer_mx_gemm_grouped(const razer_mx* x, const razer_mx* w, const int32_t* offsets,
+                                   int64_t experts, const int32_t* x_rows, int64_t m, void* y,
+                                   razer_dtype y_dt, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of a product (experts = 0) or of a grouped one (n: columns of
+ * one expert).  Depends on the current device's compute-unit count. */
+size_t razer_mx_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts);
+
+/* The step between two blocks of a transformer, in one pass:
+ *
+ *   h_out = h + residual_scale * gate . N(y; post_weight)
+ *   x_out = N(h_out; pre_weight)            N(v; w) = w * v / sqrt(mean(v^2) + eps)
+ *
+ * with fp32 arithmetic; h_out, x_out and the packed x are each rounded once from
+ * fp32 (x from the unrounded h_out).  Optional parts are NULL. */
+enum { RAZER_NORM_POST = 1u /* y is normalised; without it h_out = h + residual_scale * gate . post_weight . y */ };
+typedef struct razer_norm {
+  int64_t rows;
+  int64_t cols;           /* multiple of 32, at most 32768 */
+  int32_t dtype;          /* razer_dtype of y, h, the weights, gate, h_out and x_out */
+  uint32_t flags;         /* RAZER_NORM_POST */
+  const void* y;          /* device [rows, cols], the block's output; NULL: h_out = h */
+  const void* h;          /* device [rows, cols], the residual stream */
+  int64_t y_stride;       /* elements from row to row, a multiple of 16 bytes */
+  int64_t h_stride;
+  const void* post_weight; /* device [cols]; NULL: ones */
+  const void* pre_weight;  /* device [cols]; NULL: ones */
+  const void* gate;        /* device [gate_rows, cols]; NULL: ones.  Row r takes gate row
+                              r / (rows / gate_rows): one gate for all, one a sequence, one a row */
+  int64_t gate_rows;       /* divides rows */
+  float residual_scale;
+  float eps;
+  void* h_out;             /* device [rows, cols]; may be NULL, may be h (if its rows are contiguous) */
+  void* x_out;             /* device [rows, cols]; may be NULL */
+  const razer_mx* packed;  /* x as MXFP4; may be NULL */
+} razer_norm;
+razer_status razer_block_norm(const razer_norm* a, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* razer_status_string(razer_status s);
 

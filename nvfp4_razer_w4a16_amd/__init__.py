@@ -8,7 +8,9 @@ no fallback path.
 
 Functions carry the C names: ``razer_quantize_weight``, ``razer_quantize_act``,
 ``razer_dequant``, ``razer_gemv``, ``razer_gemm``, ``razer_gemm_w4a4``, ``razer_weight_offset_sse``,
-``razer_workspace_bytes``, ``razer_status_string``.
+``razer_workspace_bytes``, ``razer_status_string``; the microscaled 4-bit (MXFP4)
+operators and the block norm, ``razer_mx_*`` and ``razer_block_norm``, are in ``mx``
+and re-exported here.
 """
 from __future__ import annotations
 
@@ -32,7 +34,8 @@ SECOND_PAIR_OFFSETS = tuple(range(-7, 8))  # entry i of razer_weight_offset_sse 
 
 EXPORTED = ("razer_quantize_weight", "razer_quantize_act", "razer_quantize_act_noalloc", "razer_dequant", "razer_gemv",
             "razer_gemv_group", "razer_gemm", "razer_gemm_w4a4", "razer_weight_offset_sse", "razer_workspace_bytes",
-            "razer_status_string")
+            "razer_status_string", "razer_mx_quantize", "razer_mx_quantize_gated", "razer_mx_dequant", "razer_mx_gemm",
+            "razer_mx_gemm_grouped", "razer_mx_workspace_bytes", "razer_block_norm")
 
 DEFAULT_WEIGHT_OFFSETS = (-2, 4)  # special values +/-5 and +/-8
 DEFAULT_ACT_OFFSETS = (-2,)       # special values +/-5
@@ -83,6 +86,7 @@ def lib() -> ctypes.CDLL:
         L.razer_workspace_bytes.restype = sz
         L.razer_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.razer_status_string.restype, L.razer_status_string.argtypes = ctypes.c_char_p, [i32]
+        mx.bind(L)
         _lib = L
     return _lib
 
@@ -446,3 +450,9 @@ def razer_gemm_w4a4(x: PackedTensor, w: PackedTensor, out_dtype: torch.dtype = t
                                  ctypes.c_void_p(workspace.data_ptr() if workspace is not None else 0), wsb,
                                  ctypes.c_void_p(_stream(stream))), "razer_gemm_w4a4")
     return out
+
+
+from . import mx  # noqa: E402  (binds to the names above)
+from .mx import (MX_BLOCK, RAZER_MX_MAX_EXPERTS, RAZER_NORM_POST, MxTensor, razer_block_norm,  # noqa: E402
+                 razer_mx_dequant, razer_mx_gemm, razer_mx_gemm_grouped, razer_mx_quantize,
+                 razer_mx_quantize_gated, razer_mx_workspace_bytes)

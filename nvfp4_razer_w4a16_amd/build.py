@@ -36,6 +36,10 @@ SOURCES = {
     # MFMA results in VGPRs: the epilogue of every block reads them with VALU
     "rz_bdiag.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "rz_w4a4.hip": [],
+    "rz_mx_encode.hip": [],
+    "rz_mx_gemm.hip": [],
+    "rz_block_norm.hip": [],
+    "rz_mx_api.cpp": [],
     "rz_api.cpp": [],
 }
 

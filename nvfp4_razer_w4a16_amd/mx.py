@@ -1,0 +1,326 @@
+"""Microscaled 4-bit tensors (MXFP4) and the block norm: binding of the
+``razer_mx_*`` calls and ``razer_block_norm`` of ``include/librazer.h``.
+
+An ``MxTensor`` holds 32-element blocks of FP4-E2M1 codes with one power-of-two
+scale byte each.  Both operands of a product are MxTensors::
+
+    h, x = razer_block_norm(y, h, post_weight=p, pre_weight=q, packed=True)
+    gu   = razer_mx_gemm(x, gate_up)                  # [M, 2 * I]
+    y    = razer_mx_gemm(razer_mx_quantize_gated(gu), down)
+
+The package re-exports every name here.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _DT, RAZER_OK, RazerError, _check_buffer, lib
+
+RAZER_NORM_POST = 1
+RAZER_MX_MAX_EXPERTS = 4096
+MX_BLOCK = 32
+
+
+class razer_mx(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+class razer_norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("y", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("y_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64), ("post_weight", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("h_out", ctypes.c_void_p),
+                ("x_out", ctypes.c_void_p), ("packed", ctypes.POINTER(razer_mx))]
+
+
+def bind(L: ctypes.CDLL):
+    """Argument types of the calls bound here."""
+    vp, sz, i32, i64, P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, ctypes.POINTER(razer_mx)
+    for name, args in (("razer_mx_quantize", [vp, i32, i64, P, vp]),
+                       ("razer_mx_quantize_gated", [vp, i32, i64, P, vp]),
+                       ("razer_mx_dequant", [P, vp, i32, vp]),
+                       ("razer_mx_gemm", [P, P, vp, i32, vp, sz, vp]),
+                       ("razer_mx_gemm_grouped", [P, P, vp, i64, vp, i64, vp, i32, vp, sz, vp]),
+                       ("razer_block_norm", [ctypes.POINTER(razer_norm), vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = i32, args
+    L.razer_mx_workspace_bytes.restype, L.razer_mx_workspace_bytes.argtypes = sz, [i64] * 4
+
+
+def _check(status: int, what: str):
+    if status != RAZER_OK:
+        raise RazerError(status, what)
+
+
+def _stream(stream, device: torch.device) -> int:
+    """The caller's stream, or the current one of the tensors' device, which has
+    to be the current device: launches go to that one."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _dtype(dt: torch.dtype) -> int:
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return code
+
+
+def _on_gpu(t, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, not {t.device}")
+    return t.device
+
+
+class MxTensor:
+    """An MXFP4 tensor in device memory.
+
+    codes: uint8 [rows, cols // 2], the even column in the low half of a byte;
+    scales: uint8 [rows, cols // 32]."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, rows: int, cols: int, device):
+        if rows < 0 or cols < 0 or cols % MX_BLOCK:
+            raise ValueError(f"cols must be a multiple of {MX_BLOCK}")
+        self.rows, self.cols = rows, cols
+        self.codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((rows, cols // MX_BLOCK), dtype=torch.uint8, device=device)
+
+    @classmethod
+    def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "MxTensor":
+        """The tensor that these buffers hold (shared, not copied); leading
+        dimensions, such as a stack of experts, are rows."""
+        t = cls.__new__(cls)
+        t.codes = codes if codes.dim() == 2 else codes.view(-1, codes.shape[-1])
+        t.scales = scales if scales.dim() == 2 else scales.view(-1, scales.shape[-1])
+        t.rows, t.cols = t.codes.shape[0], 2 * t.codes.shape[1]
+        t.check()
+        return t
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def check(self, name: str = "MxTensor") -> torch.device:
+        """Its buffers match its shape (they are plain attributes a caller can
+        replace); returns their device."""
+        c, s, rows, cols = self.codes, self.scales, self.rows, self.cols
+        if not (c.dtype == s.dtype == torch.uint8 and c.is_contiguous() and s.is_contiguous()
+                and cols % MX_BLOCK == 0 and c.shape == (rows, cols // 2) and s.shape == (rows, cols // MX_BLOCK)
+                and c.device == s.device):
+            raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
+                             f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
+        return c.device
+
+    def struct(self) -> razer_mx:
+        return razer_mx(self.rows, self.cols, self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def _operand(t, name: str) -> torch.device:
+    if not isinstance(t, MxTensor):
+        raise TypeError(f"{name} must be an MxTensor")
+    dev = t.check(name)
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU, not {dev}")
+    return dev
+
+
+def _rows_of(x: torch.Tensor) -> torch.Tensor:
+    """x [rows, cols] as the calls take it: contiguous 16-byte rows at any stride
+    of whole 16 bytes; copied where it is not."""
+    if x.stride(1) == 1 and x.stride(0) >= x.shape[1] and not (x.stride(0) * x.element_size() | x.data_ptr()) % 16:
+        return x
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
+def _same(dev: torch.device, want: torch.device, name: str):
+    if dev != want:
+        raise ValueError(f"{name} must be on {want}, not {dev}")
+
+
+def _packed_out(out, rows: int, cols: int, device) -> MxTensor:
+    if out is None:
+        return MxTensor(rows, cols, device)
+    _same(_operand(out, "out"), device, "out")
+    if out.shape != (rows, cols):
+        raise ValueError(f"out is {out.rows}x{out.cols}, expected {rows}x{cols}")
+    return out
+
+
+def _encode(call, x, parts: int, out, stream) -> MxTensor:
+    dev = _on_gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("expected a 2-D tensor")
+    dt = _dtype(x.dtype)
+    if x.shape[1] % (parts * MX_BLOCK):
+        raise ValueError(f"columns must be a multiple of {parts * MX_BLOCK}")
+    out = _packed_out(out, x.shape[0], x.shape[1] // parts, dev)
+    x = _rows_of(x)
+    s = out.struct()
+    _check(call(x.data_ptr(), dt, x.stride(0), ctypes.byref(s), _stream(stream, dev)), call.__name__)
+    return out
+
+
+def razer_mx_quantize(x: torch.Tensor, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """MXFP4 encoding of x [rows, cols] (f32, f16 or bf16; cols % 32 == 0)."""
+    return _encode(lib().razer_mx_quantize, x, 1, out, stream)
+
+
+def razer_mx_quantize_gated(gu: torch.Tensor, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """MXFP4 encoding of silu(g) * u for gu [rows, 2 * cols] = [g | u]."""
+    return _encode(lib().razer_mx_quantize_gated, gu, 2, out, stream)
+
+
+def razer_mx_dequant(t: MxTensor, dtype: torch.dtype = torch.float32, out=None, stream=None) -> torch.Tensor:
+    """The values of t [rows, cols] (exact in f32, rounded once to f16 / bf16)."""
+    dev = _operand(t, "t")
+    if out is None:
+        out = torch.empty((t.rows, t.cols), dtype=dtype, device=dev)
+    else:
+        _check_buffer(out, (t.rows, t.cols), dev, "out")
+    s = t.struct()
+    _check(lib().razer_mx_dequant(ctypes.byref(s), out.data_ptr(), _dtype(out.dtype), _stream(stream, dev)),
+           "razer_mx_dequant")
+    return out
+
+
+def razer_mx_workspace_bytes(m: int, n: int, k: int, experts: int = 0) -> int:
+    return int(lib().razer_mx_workspace_bytes(m, n, k, experts))
+
+
+def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    else:
+        _check_buffer(out, (m, n), dev, "out")
+    if workspace is None:
+        need = lib().razer_mx_workspace_bytes(m, n, k, experts)
+        if not need:
+            return out, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_buffer(workspace, None, dev, "workspace")
+    return out, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
+                  stream=None) -> torch.Tensor:
+    """y[M, N] = x[M, K] . w[N, K]^T."""
+    dev = _operand(x, "x")
+    _same(_operand(w, "w"), dev, "w")
+    if x.cols != w.cols:
+        raise ValueError(f"x has {x.cols} columns, w {w.cols}")
+    out, ws, wsb = _product_buffers(x.rows, w.rows, x.cols, 0, dev, out_dtype, out, workspace)
+    sx, sw = x.struct(), w.struct()
+    _check(lib().razer_mx_gemm(ctypes.byref(sx), ctypes.byref(sw), out.data_ptr(), _dtype(out.dtype), ws, wsb,
+                               _stream(stream, dev)), "razer_mx_gemm")
+    return out
+
+
+def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_rows: torch.Tensor | None = None,
+                          out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
+                          stream=None) -> torch.Tensor:
+    """The products of a mixture of experts: w stacks E = offsets.numel() - 1
+    weights [N, K]; rows offsets[e] .. offsets[e + 1] - 1 of the result are
+    x[x_rows[r]] . w_e^T (x[r] without x_rows).  offsets (int32 [E + 1]) and
+    x_rows (int32 [M]) stay on the GPU.  Rows outside every run are not written;
+    a row number outside x makes its row zero."""
+    dev = _operand(x, "x")
+    _same(_operand(w, "w"), dev, "w")
+    if x.cols != w.cols:
+        raise ValueError(f"x has {x.cols} columns, w {w.cols}")
+    if offsets.dim() != 1:
+        raise ValueError("offsets must be 1-D")
+    _check_buffer(offsets, tuple(offsets.shape), dev, "offsets", torch.int32)
+    experts, m = offsets.numel() - 1, x.rows
+    if experts < 1 or w.rows % experts:
+        raise ValueError(f"w has {w.rows} rows for {experts} experts")
+    rows = None
+    if x_rows is not None:
+        if x_rows.dim() != 1:
+            raise ValueError("x_rows must be 1-D")
+        _check_buffer(x_rows, tuple(x_rows.shape), dev, "x_rows", torch.int32)
+        m, rows = x_rows.numel(), x_rows.data_ptr()
+    n = w.rows // experts
+    out, ws, wsb = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
+    sx, sw = x.struct(), w.struct()
+    _check(lib().razer_mx_gemm_grouped(ctypes.byref(sx), ctypes.byref(sw), offsets.data_ptr(), experts, rows, m,
+                                       out.data_ptr(), _dtype(out.dtype), ws, wsb, _stream(stream, dev)),
+           "razer_mx_gemm_grouped")
+    return out
+
+
+def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=None, post_norm: bool | None = None,
+                     gate=None, residual_scale: float = 1.0, pre_weight=None, eps: float = 1e-5,
+                     packed: bool = False, h_out=None, x_out=None, stream=None):
+    """(h', x) of h' = h + residual_scale * gate . N(y; post_weight) and
+    x = N(h'; pre_weight), N(v; w) = w * v / sqrt(mean(v^2) + eps).
+
+    y, h: [rows, cols]; y None: h' = h.  The norm of y is taken where post_norm is
+    true (by default, where post_weight is given).  gate: [cols] or
+    [gate_rows, cols], gate_rows a divisor of rows.  packed: x is an MxTensor, else
+    a tensor of h's dtype.  h_out (h itself, if contiguous) and x_out take the
+    results."""
+    dev = _on_gpu(h, "h")
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D")
+    rows, cols = h.shape
+    if cols % MX_BLOCK:
+        raise ValueError(f"columns must be a multiple of {MX_BLOCK}")
+    dt = _dtype(h.dtype)
+    a = razer_norm(rows=rows, cols=cols, dtype=dt, residual_scale=residual_scale, eps=eps)
+    h = _rows_of(h)
+    a.h, a.h_stride = h.data_ptr(), h.stride(0)
+    if y is not None:
+        if _on_gpu(y, "y") != dev or y.shape != h.shape or y.dtype != h.dtype:
+            raise ValueError(f"y must be {rows}x{cols} of {h.dtype} on {dev}")
+        y = _rows_of(y)
+        a.y, a.y_stride = y.data_ptr(), y.stride(0)
+        if post_norm if post_norm is not None else post_weight is not None:
+            a.flags = RAZER_NORM_POST
+    elif post_weight is not None or gate is not None or post_norm:
+        raise ValueError("post_weight, post_norm and gate belong to y")
+    if post_weight is not None:
+        _check_buffer(post_weight, (cols,), dev, "post_weight", h.dtype)
+        a.post_weight = post_weight.data_ptr()
+    if pre_weight is not None:
+        _check_buffer(pre_weight, (cols,), dev, "pre_weight", h.dtype)
+        a.pre_weight = pre_weight.data_ptr()
+    if gate is not None:
+        a.gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
+        _check_buffer(gate, (cols,) if gate.dim() == 1 else (a.gate_rows, cols), dev, "gate", h.dtype)
+        a.gate = gate.data_ptr()
+    if h_out is None:
+        h_out = torch.empty((rows, cols), dtype=h.dtype, device=dev)
+    else:
+        _check_buffer(h_out, (rows, cols), dev, "h_out", h.dtype)
+    a.h_out = h_out.data_ptr()
+    if packed:
+        x = _packed_out(x_out, rows, cols, dev)
+        s = x.struct()
+        a.packed = ctypes.pointer(s)
+    else:
+        x = torch.empty((rows, cols), dtype=h.dtype, device=dev) if x_out is None else x_out
+        if x_out is not None:
+            _check_buffer(x, (rows, cols), dev, "x_out", h.dtype)
+        a.x_out = x.data_ptr()
+    _check(lib().razer_block_norm(ctypes.byref(a), _stream(stream, dev)), "razer_block_norm")
+    return h_out, x
