@@ -220,6 +220,242 @@ template <typename OT> __global__ __launch_bounds__(256) void mx_tile_kernel(Arg
   }
 }
 
+// ---- stream kernel -------------------------------------------------------------
+// For few rows of X the product is a read of W.  A workgroup owns 16 W rows at a
+// time (a "row tile") and all of K; each of its up to eight waves takes U units
+// of 512 elements of K and keeps its share of up to 16 MT rows of X in registers
+// for all the row tiles that the workgroup walks through, so that nothing but W
+// is read in the loop.
+//
+// A unit (16 rows x 256 bytes) is loaded with four instructions that each cover
+// 256 contiguous bytes of four rows, four units ahead of their use, and turned
+// through a wave's own LDS stage into the operand's layout (chunk c of row r at
+// place c ^ r: no bank conflicts either way).  Group g = lane / 16 takes block
+// 4g + s of a unit at MFMA s, so its scale bytes are one dword.  The scale bytes
+// of a row tile are one contiguous piece of memory; the workgroup loads it a
+// tile ahead and hands it round in LDS.  The waves' partial sums meet in LDS,
+// one barrier a row tile (both areas are double-buffered).
+//
+// Reads past the last W row return zero (the buffer descriptor ends there), so
+// the loop has no branch around a load.
+constexpr int kSRows = 16, kSUnit = 512, kSAhead = 4, kSMaxWaves = 8;
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+}
+
+template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
+}
+
+template <int U, int MT>
+__global__ __launch_bounds__(64 * kSMaxWaves, U * MT == 1 ? 4 : 2) void mx_stream_kernel(Args a, int y_dtype, int waves) {
+  constexpr int kPart = kSRows * 16 * MT;  // fp32 sums of one wave
+  constexpr int kChunks = U / 4 + 1;       // 16-byte chunks of a tile's scale bytes a thread carries: nb + 1 <= 16 U waves + 1
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const Tile t = find_tile(a, 16 * MT, blockIdx.y);
+  if (t.expert < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
+  const int g = lane >> 4, l16 = lane & 15;
+  uint8_t* stage = smem + wave * (kSRows * 256);
+  float* part = (float*)(smem + waves * (kSRows * 256));            // [2][waves][kPart]
+  uint8_t* sc = (uint8_t*)(part + 2 * waves * kPart);                // [2][sc_bytes]
+  const int sc_bytes = (kSRows * nb + 4 + 15 + 4) & ~15;             // a tile's scale bytes, dword-aligned start
+  const int unit0 = wave * U;
+  const uint8_t* wc = a.wc + (int64_t)t.expert * a.n * kb;
+  const uint8_t* wsc = a.ws + (int64_t)t.expert * a.n * nb;
+  const int tiles = (int)((a.n + kSRows - 1) / kSRows);
+
+  // this wave's share of X
+  u32x4_t fx[MT][U][4];
+  uint32_t dx[MT][U];
+  const int64_t last = t.m1 - 1;
+#pragma unroll
+  for (int j = 0; j < MT; j++) {
+    int64_t row = min(t.m0 + 16 * j + l16, last);
+    if (a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
+    const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int b = (unit0 + u) * 16 + 4 * g;
+#pragma unroll
+      for (int s = 0; s < 4; s++) fx[j][u][s] = *(const u32x4_t*)(pc + min(b + s, nb - 1) * 16);
+      dx[j][u] = scales4(ps, b, nb);
+    }
+  }
+
+  // W units: slot i of a round is unit i % U of row tile i / U of the round
+  constexpr int kRound = U > kSAhead ? U : kSAhead, kTilesRound = kRound / U;
+  u32x4_t fw[kSAhead][4];
+  int voff[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) voff[i] = (4 * i + g) * kb + l16 * 16;
+  const int step = (int)gridDim.x;
+  auto load_unit = [&](int tile, int u, u32x4_t (&v)[4]) {
+    const int n0 = tile * kSRows, col = (unit0 + u) * 256;
+    const int rows = min(max((int)a.n - n0, 0), kSRows);
+    const Rsrc r = rsrc_of(wc + (int64_t)n0 * kb + col, max(rows * kb - col, 0));
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 0);
+  };
+  // A row tile's scale bytes, from the dword that holds its first one; thread i
+  // carries 16 bytes of every 16 * (threads).  Dwords that hold none of the bytes
+  // read zero.
+  struct Scales {
+    u32x4_t v[kChunks];
+  };
+  auto load_scales = [&](int tile) {
+    const int n0 = tile * kSRows, rows = min(max((int)a.n - n0, 0), kSRows);
+    const uint8_t* p = wsc + (int64_t)n0 * nb;
+    const int skew = (int)((uintptr_t)p & 3);
+    const Rsrc r = rsrc_of(p - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
+    Scales s;
+#pragma unroll
+    for (int i = 0; i < kChunks; i++)
+      s.v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (i * 64 * waves + tid) * 16, 0, 0);
+    return s;
+  };
+  auto keep_scales = [&](const Scales& s, int buf) {
+#pragma unroll
+    for (int i = 0; i < kChunks; i++) {
+      const int at = (i * 64 * waves + tid) * 16;
+      if (at < sc_bytes) *(u32x4_t*)(sc + buf * sc_bytes + at) = s.v[i];
+    }
+  };
+  auto skew_of = [&](int tile) { return (int)((uintptr_t)(wsc + (int64_t)tile * kSRows * nb) & 3); };
+
+  int tile = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < kSAhead; i++) load_unit(tile + i / U * step, i % U, fw[i]);
+  keep_scales(load_scales(tile), 0);
+  __syncthreads();
+
+  f32x4_t acc[MT];
+  int buf = 0;
+  // row tile RT of a round
+  auto row_tile = [&](auto which) {
+      constexpr int rt = decltype(which)::value;
+      const Scales next_sc = load_scales(tile + step);
+      const int skew = skew_of(tile);
+#pragma unroll
+      for (int j = 0; j < MT; j++) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        constexpr int kA = kSAhead;
+        const int slot = (rt * U + u) % kA;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          *(u32x4_t*)(stage + (4 * i + g) * 256 + ((l16 ^ (4 * i + g)) * 16)) = fw[slot][i];
+        const int ahead = u + kA;  // the unit that takes this slot
+        load_unit(tile + ahead / U * step, ahead % U, fw[slot]);
+        // scale bytes of blocks b .. b + 3 of row l16, 0 past K
+        const int b = (unit0 + u) * 16 + 4 * g, at = skew + l16 * nb + b;
+        const uint32_t* q = (const uint32_t*)(sc + buf * sc_bytes) + (min(at, sc_bytes - 8) >> 2);
+        uint32_t dw = __builtin_amdgcn_alignbyte(q[1], q[0], (uint32_t)at & 3u);
+        const int have = nb - b;
+        dw = have >= 4 ? dw : have <= 0 ? 0u : dw & ((1u << (8 * have)) - 1u);
+        wave_lds_sync();
+        u32x4_t f[4];
+#pragma unroll
+        for (int s = 0; s < 4; s++) f[s] = *(const u32x4_t*)(stage + l16 * 256 + (((4 * g + s) ^ l16) * 16));
+#pragma unroll
+        for (int j = 0; j < MT; j++) {
+          acc[j] = mma16<0>(f[0], fx[j][u][0], acc[j], dw, dx[j][u]);
+          acc[j] = mma16<1>(f[1], fx[j][u][1], acc[j], dw, dx[j][u]);
+          acc[j] = mma16<2>(f[2], fx[j][u][2], acc[j], dw, dx[j][u]);
+          acc[j] = mma16<3>(f[3], fx[j][u][3], acc[j], dw, dx[j][u]);
+        }
+        // the products stay here: moved down, all units' fragments would wait in registers
+#pragma unroll
+        for (int j = 0; j < MT; j++) asm volatile("" : "+v"(acc[j]));
+        wave_lds_sync();
+      }
+      float* mine = part + (buf * waves + wave) * kPart;
+#pragma unroll
+      for (int j = 0; j < MT; j++) *(f32x4_t*)(mine + j * 256 + lane * 4) = acc[j];
+      keep_scales(next_sc, buf ^ 1);
+      __syncthreads();
+      for (int o = tid; o < kPart; o += 64 * waves) {
+        const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
+        const float* p = part + buf * waves * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+        float v = 0.0f;
+        for (int w = 0; w < waves; w++) v += p[w * kPart];
+        const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
+        if (row < t.m1 && col < a.n) {
+          if (a.x_rows) {
+            const int64_t r = a.x_rows[row];
+            if (r < 0 || r >= a.x_rows_total) v = 0.0f;
+          }
+          const int64_t at = row * a.n + col;
+          if (y_dtype == kF32) ((float*)a.y)[at] = v;
+          else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(v);
+          else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(v);
+        }
+      }
+      buf ^= 1;
+      tile += step;
+      return tile < tiles;
+  };
+  if (tile >= tiles) return;
+  while (true) {
+    if (!row_tile(std::integral_constant<int, 0>{})) return;
+    if constexpr (kTilesRound > 1)
+      if (!row_tile(std::integral_constant<int, 1>{})) return;
+    if constexpr (kTilesRound > 2) {
+      if (!row_tile(std::integral_constant<int, 2>{})) return;
+      if (!row_tile(std::integral_constant<int, 3>{})) return;
+    }
+  }
+}
+
+// The stream kernel's shape for a product: U units a wave, waves, MT.
+struct StreamPlan {
+  int u, waves, mt;  // u = 0: not covered
+};
+StreamPlan stream_plan(int64_t rows, int64_t k) {
+  const int64_t units = (k + kSUnit - 1) / kSUnit;
+  const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  int u = 1;
+  while ((int64_t)u * kSMaxWaves < units) u *= 2;
+  if (u * mt > 8) return {0, 0, 0};  // X would not fit the registers
+  return {u, (int)((units + u - 1) / u), mt};
+}
+
+template <int U, int MT> hipError_t go_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t stream) {
+  const int nb = (int)(a.k / kMxBlock);
+  const int sc_bytes = (kSRows * nb + 4 + 15 + 4) & ~15;
+  const size_t lds = (size_t)p.waves * (kSRows * 256 + 2 * 4 * kSRows * 16 * MT) + 2 * sc_bytes;
+  const int64_t tiles = (a.n + kSRows - 1) / kSRows;
+  const int64_t jobs = a.offsets ? min((a.m + 16 * MT - 1) / (16 * MT) + a.experts, a.m) : (a.m + 16 * MT - 1) / (16 * MT);
+  const int64_t slots = (int64_t)device_cu_count() * 2;
+  int64_t per = (tiles * jobs + slots - 1) / slots;  // row tiles a workgroup
+  if (a.offsets) per = min(per, (int64_t)4);         // many of the jobs may be empty
+  const int64_t gx = (tiles + per - 1) / per;
+  auto kern = mx_stream_kernel<U, MT>;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)gx, (unsigned)jobs), dim3(64 * p.waves), lds, stream, a, y_dtype, p.waves);
+  return hipGetLastError();
+}
+
+hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t s) {
+  switch (p.mt * 16 + p.u) {
+    case 17: return go_stream<1, 1>(a, y_dtype, p, s);
+    case 18: return go_stream<2, 1>(a, y_dtype, p, s);
+    case 20: return go_stream<4, 1>(a, y_dtype, p, s);
+    case 24: return go_stream<8, 1>(a, y_dtype, p, s);
+    case 33: return go_stream<1, 2>(a, y_dtype, p, s);
+    case 34: return go_stream<2, 2>(a, y_dtype, p, s);
+    case 36: return go_stream<4, 2>(a, y_dtype, p, s);
+    case 65: return go_stream<1, 4>(a, y_dtype, p, s);
+    default: return go_stream<2, 4>(a, y_dtype, p, s);
+  }
+}
+
 template <typename OT> hipError_t run(const Args& a, hipStream_t stream) {
   const int64_t gx = (a.n + kT - 1) / kT;
   const int64_t gy = (a.m + kT - 1) / kT + (a.offsets ? min((int64_t)a.experts, a.m) : 0);
@@ -235,6 +471,12 @@ hipError_t launch_mx_gemm(const MxGemm& g, void*, size_t, hipStream_t stream) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
   const Args a = {g.x.codes, g.x.scales, g.w.codes, g.w.scales, g.m, g.n, g.k, g.x.rows, g.y, g.offsets, g.x_rows,
                   g.experts};
+  // rows of one product: of one expert, on average
+  const int64_t rows = g.offsets ? (g.m + g.experts - 1) / g.experts : g.m;
+  if (rows <= 64) {
+    const StreamPlan p = stream_plan(rows, g.k);
+    if (p.u) return run_stream(a, g.y_dtype, p, stream);
+  }
   if (g.y_dtype == kF32) return run<float>(a, stream);
   if (g.y_dtype == kF16) return run<_Float16>(a, stream);
   return run<__bf16>(a, stream);
