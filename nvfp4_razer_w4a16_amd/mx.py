@@ -87,50 +87,78 @@ class MxTensor:
     codes: uint8 [rows, cols // 2], the even column in the low half of a byte;
     scales: uint8 [rows, cols // 32]."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("rows", "cols", "device", "_buf", "_codes", "_scales", "_valid")
 
     def __init__(self, rows: int, cols: int, device):
         if rows < 0 or cols < 0 or cols % MX_BLOCK:
             raise ValueError(f"cols must be a multiple of {MX_BLOCK}")
         self.rows, self.cols = rows, cols
-        self.codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
-        self.scales = torch.empty((rows, cols // MX_BLOCK), dtype=torch.uint8, device=device)
+        # one buffer for both: codes, then scales; their views are made when asked for
+        self._buf = torch.empty(rows * cols // 32 * 17, dtype=torch.uint8, device=device)
+        self.device = self._buf.device
+        self._codes = self._scales = None
+        self._valid = True
 
     @classmethod
     def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "MxTensor":
         """The tensor that these buffers hold (shared, not copied); leading
         dimensions, such as a stack of experts, are rows."""
         t = cls.__new__(cls)
-        t.codes = codes if codes.dim() == 2 else codes.view(-1, codes.shape[-1])
-        t.scales = scales if scales.dim() == 2 else scales.view(-1, scales.shape[-1])
-        t.rows, t.cols = t.codes.shape[0], 2 * t.codes.shape[1]
+        shape = codes.shape
+        if len(shape) != 2:
+            codes, scales = codes.view(-1, shape[-1]), scales.view(-1, scales.shape[-1])
+            shape = codes.shape
+        t.rows, t.cols = shape[0], 2 * shape[1]
+        t._buf, t._codes, t._scales, t._valid = None, codes, scales, False
         t.check()
         return t
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * self.cols // 2].view(self.rows, self.cols // 2)
+        return self._codes
+
+    @codes.setter
+    def codes(self, t: torch.Tensor):
+        self._scales, self._codes, self._valid, self._buf = self.scales, t, False, None
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._buf[self.rows * self.cols // 2:].view(self.rows, self.cols // MX_BLOCK)
+        return self._scales
+
+    @scales.setter
+    def scales(self, t: torch.Tensor):
+        self._codes, self._scales, self._valid, self._buf = self.codes, t, False, None
 
     @property
     def shape(self):
         return (self.rows, self.cols)
 
-    @property
-    def device(self) -> torch.device:
-        return self.codes.device
-
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        return self.rows * self.cols // 32 * 17
 
     def check(self, name: str = "MxTensor") -> torch.device:
-        """Its buffers match its shape (they are plain attributes a caller can
-        replace); returns their device."""
-        c, s, rows, cols = self.codes, self.scales, self.rows, self.cols
-        if not (c.dtype == s.dtype == torch.uint8 and c.is_contiguous() and s.is_contiguous()
-                and cols % MX_BLOCK == 0 and c.shape == (rows, cols // 2) and s.shape == (rows, cols // MX_BLOCK)
-                and c.device == s.device):
-            raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
-                             f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
-        return c.device
+        """Its buffers match its shape (buffers it was given are looked at once);
+        returns their device."""
+        if not self._valid:
+            c, s, rows, cols = self._codes, self._scales, self.rows, self.cols
+            if not (c.dtype == s.dtype == torch.uint8 and c.is_contiguous() and s.is_contiguous()
+                    and cols % MX_BLOCK == 0 and c.shape == (rows, cols // 2) and s.shape == (rows, cols // MX_BLOCK)
+                    and c.device == s.device):
+                raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
+                                 f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
+            self.device = c.device
+            self._valid = True
+        return self.device
 
     def struct(self) -> razer_mx:
-        return razer_mx(self.rows, self.cols, self.codes.data_ptr(), self.scales.data_ptr())
+        if self._buf is not None:
+            p = self._buf.data_ptr()
+            return razer_mx(self.rows, self.cols, p, p + self.rows * self.cols // 2)
+        return razer_mx(self.rows, self.cols, self._codes.data_ptr(), self._scales.data_ptr())
 
 
 def _operand(t, name: str) -> torch.device:
@@ -145,7 +173,7 @@ def _operand(t, name: str) -> torch.device:
 def _rows_of(x: torch.Tensor) -> torch.Tensor:
     """x [rows, cols] as the calls take it: contiguous 16-byte rows at any stride
     of whole 16 bytes; copied where it is not."""
-    if x.stride(1) == 1 and x.stride(0) >= x.shape[1] and not (x.stride(0) * x.element_size() | x.data_ptr()) % 16:
+    if x.stride(1) == 1 and not (x.stride(0) * x.element_size() | x.data_ptr()) % 16 and x.stride(0) >= x.shape[1]:
         return x
     x = x.contiguous()
     return x if x.data_ptr() % 16 == 0 else x.clone()
@@ -170,12 +198,12 @@ def _encode(call, x, parts: int, out, stream) -> MxTensor:
     if x.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     dt = _dtype(x.dtype)
-    if x.shape[1] % (parts * MX_BLOCK):
+    rows, cols = x.shape
+    if cols % (parts * MX_BLOCK):
         raise ValueError(f"columns must be a multiple of {parts * MX_BLOCK}")
-    out = _packed_out(out, x.shape[0], x.shape[1] // parts, dev)
+    out = _packed_out(out, rows, cols // parts, dev)
     x = _rows_of(x)
-    s = out.struct()
-    _check(call(x.data_ptr(), dt, x.stride(0), ctypes.byref(s), _stream(stream, dev)), call.__name__)
+    _check(call(x.data_ptr(), dt, x.stride(0), out.struct(), _stream(stream, dev)), call.__name__)
     return out
 
 
@@ -196,8 +224,7 @@ def razer_mx_dequant(t: MxTensor, dtype: torch.dtype = torch.float32, out=None, 
         out = torch.empty((t.rows, t.cols), dtype=dtype, device=dev)
     else:
         _check_buffer(out, (t.rows, t.cols), dev, "out")
-    s = t.struct()
-    _check(lib().razer_mx_dequant(ctypes.byref(s), out.data_ptr(), _dtype(out.dtype), _stream(stream, dev)),
+    _check(lib().razer_mx_dequant(t.struct(), out.data_ptr(), _dtype(out.dtype), _stream(stream, dev)),
            "razer_mx_dequant")
     return out
 
@@ -229,8 +256,7 @@ def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloa
     if x.cols != w.cols:
         raise ValueError(f"x has {x.cols} columns, w {w.cols}")
     out, ws, wsb = _product_buffers(x.rows, w.rows, x.cols, 0, dev, out_dtype, out, workspace)
-    sx, sw = x.struct(), w.struct()
-    _check(lib().razer_mx_gemm(ctypes.byref(sx), ctypes.byref(sw), out.data_ptr(), _dtype(out.dtype), ws, wsb,
+    _check(lib().razer_mx_gemm(x.struct(), w.struct(), out.data_ptr(), _dtype(out.dtype), ws, wsb,
                                _stream(stream, dev)), "razer_mx_gemm")
     return out
 
@@ -261,8 +287,7 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
         m, rows = x_rows.numel(), x_rows.data_ptr()
     n = w.rows // experts
     out, ws, wsb = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
-    sx, sw = x.struct(), w.struct()
-    _check(lib().razer_mx_gemm_grouped(ctypes.byref(sx), ctypes.byref(sw), offsets.data_ptr(), experts, rows, m,
+    _check(lib().razer_mx_gemm_grouped(x.struct(), w.struct(), offsets.data_ptr(), experts, rows, m,
                                        out.data_ptr(), _dtype(out.dtype), ws, wsb, _stream(stream, dev)),
            "razer_mx_gemm_grouped")
     return out
@@ -282,45 +307,48 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     dev = _on_gpu(h, "h")
     if h.dim() != 2:
         raise ValueError("h must be 2-D")
-    rows, cols = h.shape
+    rows, cols = shape = h.shape
     if cols % MX_BLOCK:
         raise ValueError(f"columns must be a multiple of {MX_BLOCK}")
-    dt = _dtype(h.dtype)
-    a = razer_norm(rows=rows, cols=cols, dtype=dt, residual_scale=residual_scale, eps=eps)
+    kind = h.dtype
+    dt = _dtype(kind)
     h = _rows_of(h)
-    a.h, a.h_stride = h.data_ptr(), h.stride(0)
+    flags, y_ptr, y_stride, post, pre, gates, gate_rows = 0, None, 0, None, None, None, 0
     if y is not None:
-        if _on_gpu(y, "y") != dev or y.shape != h.shape or y.dtype != h.dtype:
-            raise ValueError(f"y must be {rows}x{cols} of {h.dtype} on {dev}")
+        if _on_gpu(y, "y") != dev or y.shape != shape or y.dtype != kind:
+            raise ValueError(f"y must be {rows}x{cols} of {kind} on {dev}")
         y = _rows_of(y)
-        a.y, a.y_stride = y.data_ptr(), y.stride(0)
+        y_ptr, y_stride = y.data_ptr(), y.stride(0)
         if post_norm if post_norm is not None else post_weight is not None:
-            a.flags = RAZER_NORM_POST
+            flags = RAZER_NORM_POST
     elif post_weight is not None or gate is not None or post_norm:
         raise ValueError("post_weight, post_norm and gate belong to y")
     if post_weight is not None:
-        _check_buffer(post_weight, (cols,), dev, "post_weight", h.dtype)
-        a.post_weight = post_weight.data_ptr()
+        _check_buffer(post_weight, (cols,), dev, "post_weight", kind)
+        post = post_weight.data_ptr()
     if pre_weight is not None:
-        _check_buffer(pre_weight, (cols,), dev, "pre_weight", h.dtype)
-        a.pre_weight = pre_weight.data_ptr()
+        _check_buffer(pre_weight, (cols,), dev, "pre_weight", kind)
+        pre = pre_weight.data_ptr()
     if gate is not None:
-        a.gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
-        _check_buffer(gate, (cols,) if gate.dim() == 1 else (a.gate_rows, cols), dev, "gate", h.dtype)
-        a.gate = gate.data_ptr()
+        gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
+        _check_buffer(gate, (cols,) if gate.dim() == 1 else (gate_rows, cols), dev, "gate", kind)
+        gates = gate.data_ptr()
     if h_out is None:
-        h_out = torch.empty((rows, cols), dtype=h.dtype, device=dev)
+        h_out = h.new_empty(shape)
     else:
-        _check_buffer(h_out, (rows, cols), dev, "h_out", h.dtype)
-    a.h_out = h_out.data_ptr()
+        _check_buffer(h_out, shape, dev, "h_out", kind)
+    x_ptr = p_ptr = None
     if packed:
         x = _packed_out(x_out, rows, cols, dev)
-        s = x.struct()
-        a.packed = ctypes.pointer(s)
+        p_ptr = ctypes.pointer(x.struct())
+    elif x_out is None:
+        x = h.new_empty(shape)
+        x_ptr = x.data_ptr()
     else:
-        x = torch.empty((rows, cols), dtype=h.dtype, device=dev) if x_out is None else x_out
-        if x_out is not None:
-            _check_buffer(x, (rows, cols), dev, "x_out", h.dtype)
-        a.x_out = x.data_ptr()
-    _check(lib().razer_block_norm(ctypes.byref(a), _stream(stream, dev)), "razer_block_norm")
+        x = x_out
+        _check_buffer(x, shape, dev, "x_out", kind)
+        x_ptr = x.data_ptr()
+    a = razer_norm(rows, cols, dt, flags, y_ptr, h.data_ptr(), y_stride, h.stride(0), post, pre, gates, gate_rows,
+                   residual_scale, eps, h_out.data_ptr(), x_ptr, p_ptr)
+    _check(lib().razer_block_norm(a, _stream(stream, dev)), "razer_block_norm")
     return h_out, x
