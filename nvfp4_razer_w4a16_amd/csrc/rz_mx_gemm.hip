@@ -113,93 +113,195 @@ __device__ __forceinline__ void store4(OT* y, int64_t row, int64_t n, int64_t nn
 }
 
 // ---- tile kernel -------------------------------------------------------------
-// A 128x128 tile of y per workgroup of four waves (2x2), 256 elements of K a
-// step through LDS.  A tile row is 128 bytes of codes, eight 16-byte chunks;
-// chunk c of row r lies at place c ^ (r & 7), so the lanes of a fragment read
-// (one chunk of 32 rows) spread over the banks.
-constexpr int kT = 128, kStep = 256, kRowB = kStep / 2;
+// A BN x BM tile of y (BN rows of W, BM of X) per workgroup of four waves (2x2),
+// each wave (BN/2) x (BM/2) in 32x32 accumulators, 256 elements of K a step.
+//
+// LDS: two buffers of a step's codes, filled by direct-to-LDS loads of whole
+// 128-byte row pieces.  A piece is eight 16-byte chunks; chunk c of row r lies at
+// place c ^ (r & 7), so the lanes of a fragment read (one chunk of 32 rows)
+// spread over the banks.  Direct loads write lane-linear, so the loading lane
+// picks its chunk by the same rule.  Scale bytes come through registers, 16
+// bytes a row (two steps, a "window"), into one LDS area.
+//
+// Schedule of a step (four sub-steps of 64 elements): the fragments of the next
+// sub-step are read while the products of this one run.  The barrier sits before
+// the last sub-step, whose fragments are then in registers: behind it the next
+// step's buffer is complete and this step's is free, so the loads of the step
+// after next and the first fragments of the next step go out under its products.
+constexpr int kStep = 256, kRowB = kStep / 2;
 
-template <typename OT> __global__ __launch_bounds__(256) void mx_tile_kernel(Args a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lw[kT * kRowB], lx[kT * kRowB];
-  const Tile t = find_tile(a, kT, blockIdx.y);
+typedef __attribute__((address_space(1))) const void* GlobalPtr;
+typedef __attribute__((address_space(3))) void* LdsPtr;
+__device__ __forceinline__ void load_lds16(const uint8_t* g, uint8_t* l) {
+  __builtin_amdgcn_global_load_lds((GlobalPtr)g, (LdsPtr)l, 16, 0, 0);
+}
+
+// Number of the tile that workgroup b computes: consecutive workgroups go to the
+// eight XCDs in turn, so each XCD gets a contiguous run of tiles (and its L2 the
+// W rows that the run shares).
+__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t tiles) {
+  const int64_t per = tiles / 8, extra = tiles % 8, x = b % 8, i = b / 8;
+  return x * per + min(x, extra) + i;
+}
+
+template <int BN, int BM, typename OT>
+__global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kernel(Args a, int64_t m_tiles) {
+  constexpr int NI = BN / 64, MI = BM / 64;  // 32-row fragments of a wave
+  __shared__ __attribute__((aligned(16))) uint8_t w0[BN * kRowB], x0[BM * kRowB], w1[BN * kRowB], x1[BM * kRowB];
+  __shared__ __attribute__((aligned(16))) uint8_t scw[BN * 16], scx[BM * 16];
+  __shared__ int64_t x_at[BM];
+  const int64_t id = xcd_tile(blockIdx.x, gridDim.x);
+  const Tile t = find_tile(a, BM, id % m_tiles);
   if (t.expert < 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * kT;
+  const int64_t n0 = id / m_tiles * BN;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock);
-  const int64_t kb = a.k / 2;  // code bytes of a row
+  const int64_t kb = a.k / 2;
+  const int steps = (nb + 7) / 8;
   auto w_row = [&](int r) { return (int64_t)t.expert * a.n + min(n0 + r, a.n - 1); };
   auto x_row = [&](int r) -> int64_t {
     const int64_t row = min(t.m0 + r, t.m1 - 1);
     return a.x_rows ? min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1) : row;
   };
-  // this thread's four chunks of either tile
-  const uint8_t *pw[4], *px[4];
-  int place[4];
+  // direct loads: instruction i of a wave fills rows (4 i + wave) * 8 ..+7; W rows
+  // lie within 32 bits of the tile's first, X rows anywhere
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const uint8_t* wc = a.wc + ((int64_t)t.expert * a.n + n0) * kb;
+  uint32_t ow[BN / 32];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int r = i * 32 + (tid >> 3);
-    pw[i] = a.wc + w_row(r) * kb;
-    px[i] = a.xc + x_row(r) * kb;
-    place[i] = r * kRowB + (((tid & 7) ^ (r & 7)) * 16);
-  }
-  const int wn = (wave & 1) * 64, wm = (wave >> 1) * 64;
+  for (int i = 0; i < BN / 32; i++) ow[i] = (uint32_t)(min((int64_t)((4 * i + wave) * 8 + (lane >> 3)), a.n - 1 - n0) * kb);
+  for (int r = tid; r < BM; r += 256) x_at[r] = x_row(r) * kb;
+  auto load_step = [&](int s, uint8_t* lw, uint8_t* lx) {
+    const uint32_t col = (uint32_t)min(s * 8 + chunk, nb - 1) * 16;
+#pragma unroll
+    for (int i = 0; i < BN / 32; i++) load_lds16(wc + (uint64_t)(ow[i] + col), lw + (4 * i + wave) * 1024);
+#pragma unroll
+    for (int i = 0; i < BM / 32; i++)
+      load_lds16(a.xc + x_at[(4 * i + wave) * 8 + (lane >> 3)] + col, lx + (4 * i + wave) * 1024);
+  };
+  // scale bytes: thread i carries row i of either tile, 16 blocks (a window) at a time
+  const uint8_t* psw = a.ws + w_row(tid % BN) * nb;
+  const uint8_t* psx = a.xs + x_row(tid % BM) * nb;
+  struct Window {
+    u32x4_t w, x;
+  };
+  auto load_window = [&](int b) {
+    Window v = {};
+    if (b + 16 <= nb) {
+      __builtin_memcpy(&v.w, psw + b, 16);
+      __builtin_memcpy(&v.x, psx + b, 16);
+    }
+    return v;
+  };
+  auto keep_window = [&](int b, const Window& v) {
+    if (b + 16 <= nb) {
+      if (tid < BN) *(u32x4_t*)(scw + tid * 16) = v.w;
+      if (tid < BM) *(u32x4_t*)(scx + tid * 16) = v.x;
+    } else {  // the last window of a K that ends inside it: zeros from there on
+#pragma unroll 1
+      for (int i = 0; i < 16; i++) {
+        const int c = min(b + i, nb - 1);
+        if (tid < BN) scw[tid * 16 + i] = b + i < nb ? psw[c] : 0;
+        if (tid < BM) scx[tid * 16 + i] = b + i < nb ? psx[c] : 0;
+      }
+    }
+  };
+
+  const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
   const int half = lane >> 5, l32 = lane & 31;
-  const uint8_t *sw[2], *sx[2];
+  struct Frags {
+    u32x4_t w[NI], x[MI];
+  };
+  struct Dwords {
+    uint32_t w[NI], x[MI];
+  };
+  auto read_frags = [&](const uint8_t* lw, const uint8_t* lx, int kk) {
+    Frags f;
+    const int place = ((half * 4 + kk) ^ (l32 & 7)) * 16;
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
-    sw[i] = a.ws + w_row(wn + i * 32 + l32) * nb;
-    sx[i] = a.xs + x_row(wm + i * 32 + l32) * nb;
-  }
-  f32x16_t acc[2][2];
+    for (int i = 0; i < NI; i++) f.w[i] = *(const u32x4_t*)(lw + (wn + i * 32 + l32) * kRowB + place);
 #pragma unroll
-  for (int i = 0; i < 2; i++)
+    for (int i = 0; i < MI; i++) f.x[i] = *(const u32x4_t*)(lx + (wm + i * 32 + l32) * kRowB + place);
+    return f;
+  };
+  auto read_scales = [&](int step) {  // of the window
+    Dwords d;
 #pragma unroll
-    for (int j = 0; j < 2; j++)
+    for (int i = 0; i < NI; i++) d.w[i] = *(const uint32_t*)(scw + (wn + i * 32 + l32) * 16 + step * 8 + half * 4);
+#pragma unroll
+    for (int i = 0; i < MI; i++) d.x[i] = *(const uint32_t*)(scx + (wm + i * 32 + l32) * 16 + step * 8 + half * 4);
+    return d;
+  };
+  f32x16_t acc[NI][MI];
+#pragma unroll
+  for (int i = 0; i < NI; i++)
+#pragma unroll
+    for (int j = 0; j < MI; j++)
 #pragma unroll
       for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
-  const int steps = (nb + 7) / 8;
-  for (int s = 0; s < steps; s++) {
-    const int c = min(s * 8 + (tid & 7), nb - 1);
-    u32x4_t vw[4], vx[4];
+  auto products = [&](auto kk, const Frags& f, const Dwords& d) {
+    constexpr int I = decltype(kk)::value;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      vw[i] = *(const u32x4_t*)(pw[i] + c * 16);
-      vx[i] = *(const u32x4_t*)(px[i] + c * 16);
-    }
-    uint32_t dw[2], dx[2];
+    for (int i = 0; i < NI; i++)
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      dw[i] = scales4(sw[i], s * 8 + half * 4, nb);
-      dx[i] = scales4(sx[i], s * 8 + half * 4, nb);
-    }
+      for (int j = 0; j < MI; j++) acc[i][j] = mma<I>(f.w[i], f.x[j], acc[i][j], d.w[i], d.x[j]);
+  };
+  // Keeps the products before it from moving past the branches behind them, where
+  // their operands would have to wait in registers.
+  auto pin = [&]() {
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+      for (int j = 0; j < MI; j++) asm volatile("" : "+a"(acc[i][j]));
+  };
+  typedef std::integral_constant<int, 0> K0;
+  typedef std::integral_constant<int, 1> K1;
+  typedef std::integral_constant<int, 2> K2;
+  typedef std::integral_constant<int, 3> K3;
+  // One step from buffer (lw, lx), f its first fragments; `behind` runs after the
+  // barrier and returns the next step's first fragments.
+  auto step = [&](const uint8_t* lw, const uint8_t* lx, Frags f, const Dwords& d, auto behind) {
+    Frags g = read_frags(lw, lx, 1);
+    products(K0{}, f, d);
+    f = read_frags(lw, lx, 2);
+    products(K1{}, g, d);
+    g = read_frags(lw, lx, 3);
+    products(K2{}, f, d);
+    pin();
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      *(u32x4_t*)(lw + place[i]) = vw[i];
-      *(u32x4_t*)(lx + place[i]) = vx[i];
-    }
-    __syncthreads();
-    auto sub = [&](auto kk) {
-      constexpr int I = decltype(kk)::value;
-      u32x4_t fw[2], fx[2];
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int rw = wn + i * 32 + l32, rx = wm + i * 32 + l32;
-        fw[i] = *(const u32x4_t*)(lw + rw * kRowB + (((half * 4 + I) ^ (rw & 7)) * 16));
-        fx[i] = *(const u32x4_t*)(lx + rx * kRowB + (((half * 4 + I) ^ (rx & 7)) * 16));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int j = 0; j < 2; j++) acc[i][j] = mma<I>(fw[i], fx[j], acc[i][j], dw[i], dx[j]);
-    };
-    sub(std::integral_constant<int, 0>{});
-    sub(std::integral_constant<int, 1>{});
-    sub(std::integral_constant<int, 2>{});
-    sub(std::integral_constant<int, 3>{});
+    f = behind();
+    products(K3{}, g, d);
+    pin();
+    return f;
+  };
+
+  __syncthreads();  // x_at
+  load_step(0, w0, x0);
+  if (steps > 1) load_step(1, w1, x1);
+  keep_window(0, load_window(0));
+  __syncthreads();
+  Frags f = read_frags(w0, x0, 0);
+  Dwords da = read_scales(0), db = read_scales(1);
+  int s = 0;
+  for (; s + 1 < steps; s += 2) {
+    const int b = s * 8 + 16;
+    const Window v = load_window(b);
+    f = step(w0, x0, f, da, [&]() {
+      if (s + 2 < steps) load_step(s + 2, w0, x0);
+      const Frags n = read_frags(w1, x1, 0);
+      keep_window(b, v);
+      return n;
+    });
+    f = step(w1, x1, f, db, [&]() {
+      if (s + 3 < steps) load_step(s + 3, w1, x1);
+      da = read_scales(0);
+      return read_frags(w0, x0, 0);
+    });
+    db = read_scales(1);
   }
+  if (s < steps) step(w0, x0, f, da, [&]() { return Frags{}; });
 #pragma unroll
-  for (int j = 0; j < 2; j++) {
+  for (int j = 0; j < MI; j++) {
     const int64_t row = t.m0 + wm + j * 32 + l32;
     if (row >= t.m1) continue;
     bool none = false;
@@ -208,7 +310,7 @@ template <typename OT> __global__ __launch_bounds__(256) void mx_tile_kernel(Arg
       none = r < 0 || r >= a.x_rows_total;
     }
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < NI; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         const int64_t n = n0 + wn + i * 32 + q * 8 + half * 4;
@@ -456,11 +558,15 @@ hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream
   }
 }
 
-template <typename OT> hipError_t run(const Args& a, hipStream_t stream) {
-  const int64_t gx = (a.n + kT - 1) / kT;
-  const int64_t gy = (a.m + kT - 1) / kT + (a.offsets ? min((int64_t)a.experts, a.m) : 0);
-  hipLaunchKernelGGL(mx_tile_kernel<OT>, dim3((unsigned)gx, (unsigned)gy), dim3(256), 0, stream, a);
+template <int BN, int BM, typename OT> hipError_t go_tile(const Args& a, hipStream_t stream) {
+  const int64_t nt = (a.n + BN - 1) / BN;
+  const int64_t mt = (a.m + BM - 1) / BM + (a.offsets ? min((int64_t)a.experts, a.m) : 0);
+  hipLaunchKernelGGL((mx_tile_kernel<BN, BM, OT>), dim3((unsigned)(nt * mt)), dim3(256), 0, stream, a, mt);
   return hipGetLastError();
+}
+
+template <typename OT> hipError_t run(const Args& a, hipStream_t stream) {
+  return go_tile<256, 256, OT>(a, stream);
 }
 
 }  // namespace
