@@ -20,6 +20,7 @@ int64_t dtype_size(int dt) { return dt == RAZER_F32 ? 4 : 2; }
 
 constexpr int64_t kMaxElems = (int64_t)1 << 34;   // 8 elements a thread, 2^32 threads of a launch
 constexpr int64_t kMaxGemmRows = (int64_t)1 << 30;
+constexpr int64_t kMaxGemmK = (int64_t)1 << 23;   // the rows of a tile within 32 bits
 constexpr int64_t kMaxNormCols = 32768;           // 1024 threads of at most four 8-element chunks
 
 razer_status check_mx(const razer_mx* t) {
@@ -57,7 +58,7 @@ razer_status check_gemm(const razer_mx* x, const razer_mx* w, int64_t m, razer_d
   s = check_mx(w);
   if (s != RAZER_OK) return s;
   if (!dtype_ok(y_dt) || x->cols != w->cols || m < 0) return RAZER_E_INVALID;
-  if (x->cols == 0 || x->cols > INT32_MAX || m > kMaxGemmRows || w->rows > kMaxGemmRows) return RAZER_E_UNSUPPORTED;
+  if (x->cols == 0 || x->cols > kMaxGemmK || m > kMaxGemmRows || w->rows > kMaxGemmRows) return RAZER_E_UNSUPPORTED;
   return RAZER_OK;
 }
 
@@ -106,7 +107,7 @@ razer_status razer_mx_gemm_grouped(const razer_mx* x, const razer_mx* w, const i
   if (m == 0 || w->rows == 0) return RAZER_OK;
   if (!x_rows && m != x->rows) return RAZER_E_INVALID;
   if (x->rows == 0 || !offsets || !aligned(offsets, 4) || !aligned(x_rows, 4)) return RAZER_E_INVALID;
-  if (x->rows > kMaxGemmRows) return RAZER_E_UNSUPPORTED;
+  if (x->rows > kMaxGemmRows || (x_rows && x->rows * x->cols / 2 > UINT32_MAX)) return RAZER_E_UNSUPPORTED;
   if (!y || !aligned(y, 16)) return RAZER_E_INVALID;
   const size_t need = rz::mx_gemm_ws_bytes(m, w->rows / experts, x->cols, experts);
   if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return RAZER_E_INVALID;

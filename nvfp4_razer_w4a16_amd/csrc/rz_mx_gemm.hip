@@ -149,7 +149,6 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
   constexpr int NI = BN / 64, MI = BM / 64;  // 32-row fragments of a wave
   __shared__ __attribute__((aligned(16))) uint8_t w0[BN * kRowB], x0[BM * kRowB], w1[BN * kRowB], x1[BM * kRowB];
   __shared__ __attribute__((aligned(16))) uint8_t scw[BN * 16], scx[BM * 16];
-  __shared__ int64_t x_at[BM];
   const int64_t id = xcd_tile(blockIdx.x, gridDim.x);
   const Tile t = find_tile(a, BM, id % m_tiles);
   if (t.expert < 0) return;
@@ -163,21 +162,22 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
     const int64_t row = min(t.m0 + r, t.m1 - 1);
     return a.x_rows ? min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1) : row;
   };
-  // direct loads: instruction i of a wave fills rows (4 i + wave) * 8 ..+7; W rows
-  // lie within 32 bits of the tile's first, X rows anywhere
+  // direct loads: instruction i of a wave fills rows (4 i + wave) * 8 ..+7
   const int chunk = (lane & 7) ^ (lane >> 3);
   const uint8_t* wc = a.wc + ((int64_t)t.expert * a.n + n0) * kb;
-  uint32_t ow[BN / 32];
+  const int64_t x_first = a.x_rows ? 0 : t.m0;
+  const uint8_t* xc = a.xc + x_first * kb;
+  uint32_t ow[BN / 32], ox[BM / 32];  // the rows' bytes, from the tile's first row (gathered ones from X's)
 #pragma unroll
   for (int i = 0; i < BN / 32; i++) ow[i] = (uint32_t)(min((int64_t)((4 * i + wave) * 8 + (lane >> 3)), a.n - 1 - n0) * kb);
-  for (int r = tid; r < BM; r += 256) x_at[r] = x_row(r) * kb;
+#pragma unroll
+  for (int i = 0; i < BM / 32; i++) ox[i] = (uint32_t)((x_row((4 * i + wave) * 8 + (lane >> 3)) - x_first) * kb);
   auto load_step = [&](int s, uint8_t* lw, uint8_t* lx) {
     const uint32_t col = (uint32_t)min(s * 8 + chunk, nb - 1) * 16;
 #pragma unroll
     for (int i = 0; i < BN / 32; i++) load_lds16(wc + (uint64_t)(ow[i] + col), lw + (4 * i + wave) * 1024);
 #pragma unroll
-    for (int i = 0; i < BM / 32; i++)
-      load_lds16(a.xc + x_at[(4 * i + wave) * 8 + (lane >> 3)] + col, lx + (4 * i + wave) * 1024);
+    for (int i = 0; i < BM / 32; i++) load_lds16(xc + (uint64_t)(ox[i] + col), lx + (4 * i + wave) * 1024);
   };
   // scale bytes: thread i carries row i of either tile, 16 blocks (a window) at a time
   const uint8_t* psw = a.ws + w_row(tid % BN) * nb;
@@ -186,24 +186,21 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
     u32x4_t w, x;
   };
   auto load_window = [&](int b) {
-    Window v = {};
-    if (b + 16 <= nb) {
-      __builtin_memcpy(&v.w, psw + b, 16);
-      __builtin_memcpy(&v.x, psx + b, 16);
-    }
+    Window v;
+    __builtin_memcpy(&v.w, psw + b, 16);
+    __builtin_memcpy(&v.x, psx + b, 16);
     return v;
   };
-  auto keep_window = [&](int b, const Window& v) {
-    if (b + 16 <= nb) {
-      if (tid < BN) *(u32x4_t*)(scw + tid * 16) = v.w;
-      if (tid < BM) *(u32x4_t*)(scx + tid * 16) = v.x;
-    } else {  // the last window of a K that ends inside it: zeros from there on
+  auto store_window = [&](const Window& v) {
+    if (BN == 256 || tid < BN) *(u32x4_t*)(scw + tid * 16) = v.w;
+    if (BM == 256 || tid < BM) *(u32x4_t*)(scx + tid * 16) = v.x;
+  };
+  auto tail_window = [&](int b) {  // zeros from the end of K on
 #pragma unroll 1
-      for (int i = 0; i < 16; i++) {
-        const int c = min(b + i, nb - 1);
-        if (tid < BN) scw[tid * 16 + i] = b + i < nb ? psw[c] : 0;
-        if (tid < BM) scx[tid * 16 + i] = b + i < nb ? psx[c] : 0;
-      }
+    for (int i = 0; i < 16; i++) {
+      const int c = min(b + i, nb - 1);
+      if (tid < BN) scw[tid * 16 + i] = b + i < nb ? psw[c] : 0;
+      if (tid < BM) scx[tid * 16 + i] = b + i < nb ? psx[c] : 0;
     }
   };
 
@@ -260,38 +257,71 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
   typedef std::integral_constant<int, 3> K3;
   // One step from buffer (lw, lx), f its first fragments; `behind` runs after the
   // barrier and returns the next step's first fragments.
+  // The instruction order asked for: a sub-step's LDS reads, then the direct loads,
+  // one at a time between its products.
+  auto spread = [&](int reads, int loads) {
+#pragma unroll
+    for (int i = 0; i < NI * MI; i++) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto step = [&](const uint8_t* lw, const uint8_t* lx, Frags f, const Dwords& d, auto behind) {
     Frags g = read_frags(lw, lx, 1);
     products(K0{}, f, d);
+    spread(NI + MI, 2);
     f = read_frags(lw, lx, 2);
     products(K1{}, g, d);
+    spread(NI + MI, 0);
     g = read_frags(lw, lx, 3);
     products(K2{}, f, d);
+    spread(NI + MI, 0);
     pin();
     __syncthreads();
     f = behind();
     products(K3{}, g, d);
+    spread(NI * MI, (BN + BM) / 32);
     pin();
     return f;
   };
 
-  __syncthreads();  // x_at
   load_step(0, w0, x0);
   if (steps > 1) load_step(1, w1, x1);
-  keep_window(0, load_window(0));
+  if (nb >= 16)
+    store_window(load_window(0));
+  else
+    tail_window(0);
   __syncthreads();
   Frags f = read_frags(w0, x0, 0);
   Dwords da = read_scales(0), db = read_scales(1);
   int s = 0;
-  for (; s + 1 < steps; s += 2) {
-    const int b = s * 8 + 16;
-    const Window v = load_window(b);
+  // Two steps (a window) a round.  While the next window lies within K there is
+  // nothing to ask on the way, and the loads spread between the products.
+  for (; s * 8 + 32 <= nb; s += 2) {
+    const Window v = load_window(s * 8 + 16);
+    f = step(w0, x0, f, da, [&]() {
+      store_window(v);  // ahead of the loads, which the compiler would have it wait for
+      __builtin_amdgcn_sched_barrier(0);
+      load_step(s + 2, w0, x0);
+      return read_frags(w1, x1, 0);
+    });
+    f = step(w1, x1, f, db, [&]() {
+      load_step(s + 3, w1, x1);
+      da = read_scales(0);
+      return read_frags(w0, x0, 0);
+    });
+    db = read_scales(1);
+  }
+  // the last ones, where K may end
+  for (; s < steps; s += 2) {
     f = step(w0, x0, f, da, [&]() {
       if (s + 2 < steps) load_step(s + 2, w0, x0);
-      const Frags n = read_frags(w1, x1, 0);
-      keep_window(b, v);
-      return n;
+      tail_window(s * 8 + 16);
+      return read_frags(w1, x1, 0);
     });
+    if (s + 1 == steps) break;
     f = step(w1, x1, f, db, [&]() {
       if (s + 3 < steps) load_step(s + 3, w1, x1);
       da = read_scales(0);
@@ -299,7 +329,6 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
     });
     db = read_scales(1);
   }
-  if (s < steps) step(w0, x0, f, da, [&]() { return Frags{}; });
 #pragma unroll
   for (int j = 0; j < MI; j++) {
     const int64_t row = t.m0 + wm + j * 32 + l32;
