@@ -66,14 +66,27 @@ __device__ __forceinline__ Tile find_tile(const Args& a, int rows, int64_t t) {
     const uint64_t hit = __ballot(sum > t);
     if (hit) {
       const int src = __builtin_ctzll(hit);
-      const int first = __shfl(sum - cnt, src, 64);
-      const int l = __shfl(lo, src, 64), h = __shfl(hi, src, 64);
+      const int first = __builtin_amdgcn_readlane(sum - cnt, src);
+      const int l = __builtin_amdgcn_readlane(lo, src), h = __builtin_amdgcn_readlane(hi, src);
       const int m0 = l + (int)(t - first) * rows;
       return {m0, min(m0 + rows, h), e0 + src};
     }
-    before = __shfl(sum, 63, 64);
+    before = __builtin_amdgcn_readlane(sum, 63);
   }
   return {0, 0, -1};
+}
+
+// Number of row tiles, each `rows` high, of the grouped product.
+__device__ __forceinline__ int live_tiles(const Args& a, int rows) {
+  const int lane = threadIdx.x & 63, m = (int)a.m;
+  int cnt = 0;
+  for (int e = lane; e < a.experts; e += 64) {
+    const int lo = min(max(a.offsets[e], 0), m), hi = min(max(a.offsets[e + 1], lo), m);
+    cnt += (hi - lo + rows - 1) / rows;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) cnt += __shfl_xor(cnt, o, 64);
+  return __builtin_amdgcn_readfirstlane(cnt);
 }
 
 // The scale bytes of blocks b .. b + 3 of a row of nb blocks, 0 past its end.
@@ -112,132 +125,211 @@ __device__ __forceinline__ void store4(OT* y, int64_t row, int64_t n, int64_t nn
   }
 }
 
+// Memory from p on of which loads past `bytes` read zero.
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+}
+
 // ---- tile kernel -------------------------------------------------------------
 // A BN x BM tile of y (BN rows of W, BM of X) per workgroup of four waves (2x2),
-// each wave (BN/2) x (BM/2) in 32x32 accumulators, 256 elements of K a step.
+// each wave (BN/2) x (BM/2) in 32x32 accumulators, 256 elements of K a step; two
+// steps are a "window", whose scale bytes are 16 bytes a row.  As many workgroups
+// as CUs; each walks through the tiles.
 //
-// LDS: two buffers of a step's codes, filled by direct-to-LDS loads of whole
-// 128-byte row pieces.  A piece is eight 16-byte chunks; chunk c of row r lies at
-// place c ^ (r & 7), so the lanes of a fragment read (one chunk of 32 rows)
-// spread over the banks.  Direct loads write lane-linear, so the loading lane
-// picks its chunk by the same rule.  Scale bytes come through registers, 16
-// bytes a row (two steps, a "window"), into one LDS area.
+// LDS: two steps' codes, filled by direct-to-LDS loads of whole 128-byte row
+// pieces (64-byte pieces, four of them in flight, took 1.7 times as long: a line
+// is fetched whole and gone before its other half is asked for).  A piece is eight
+// 16-byte chunks; chunk c of row r lies at place c ^ (r & 7) ^ (r >> 3 & 1), so
+// that 16 lanes of a fragment read (one chunk of 16 rows) cover all banks.  Direct
+// loads write lane-linear, so the loading lane picks its chunk by the same rule.  Lane half h
+// takes chunk 4h + i at product i; scale bytes pass through registers, a window
+// ahead.
 //
-// Schedule of a step (four sub-steps of 64 elements): the fragments of the next
-// sub-step are read while the products of this one run.  The barrier sits before
-// the last sub-step, whose fragments are then in registers: behind it the next
-// step's buffer is complete and this step's is free, so the loads of the step
-// after next and the first fragments of the next step go out under its products.
-constexpr int kStep = 256, kRowB = kStep / 2;
+// Schedule of a step (products 0..3): the fragments of the next product are read
+// under this one's.  The barrier sits before the last product, whose fragments are
+// then in registers: behind it the next step is complete (each wave has waited for
+// its own loads) and nobody reads this one any more, so the step after next is
+// loaded in its place, half of it under the last product and half under the next
+// step's first (a load takes the CU's address unit 16 cycles; all 64 under one
+// product, 512 cycles, would stall it).  The loads run on into the next tile, so they are under way while this
+// tile's results go through LDS to be stored in whole 128-byte lines.
+constexpr int kStepB = 128;   // code bytes of a row and step
+constexpr int kWindow = 16;   // blocks of a window
 
-typedef __attribute__((address_space(1))) const void* GlobalPtr;
-typedef __attribute__((address_space(3))) void* LdsPtr;
-__device__ __forceinline__ void load_lds16(const uint8_t* g, uint8_t* l) {
-  __builtin_amdgcn_global_load_lds((GlobalPtr)g, (LdsPtr)l, 16, 0, 0);
+// 16 bytes a lane straight to LDS, lane i's at l + 16 i.  (The buffer form: behind
+// the global one the compiler waits for every load under way.)
+__device__ __forceinline__ void load_lds16(Rsrc r, uint32_t offset, uint8_t* l) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, (int)offset, 0, 0, 0);
 }
 
-// Number of the tile that workgroup b computes: consecutive workgroups go to the
-// eight XCDs in turn, so each XCD gets a contiguous run of tiles (and its L2 the
-// W rows that the run shares).
-__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t tiles) {
-  const int64_t per = tiles / 8, extra = tiles % 8, x = b % 8, i = b / 8;
-  return x * per + min(x, extra) + i;
+// The workgroup's barrier, once this wave's loads have arrived.
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-template <int BN, int BM, typename OT>
-__global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kernel(Args a, int64_t m_tiles) {
-  constexpr int NI = BN / 64, MI = BM / 64;  // 32-row fragments of a wave
-  __shared__ __attribute__((aligned(16))) uint8_t w0[BN * kRowB], x0[BM * kRowB], w1[BN * kRowB], x1[BM * kRowB];
-  __shared__ __attribute__((aligned(16))) uint8_t scw[BN * 16], scx[BM * 16];
-  const int64_t id = xcd_tile(blockIdx.x, gridDim.x);
-  const Tile t = find_tile(a, BM, id % m_tiles);
-  if (t.expert < 0) return;
-  const int64_t n0 = id / m_tiles * BN;
+// How a product is cut: mt x nt tiles (grouped: as many row tiles as there are),
+// the last `rest` of them each in `split` slices of K whose fp32 sums go to slots
+// of `part`.
+struct TilePlan {
+  int mt, nt;
+  int full, rest, split;
+  float* part;
+};
+
+// Place of tile `pos`: bands of eight row tiles, within a band the row tiles of
+// one column tile side by side, so that what runs at one time shares few rows of
+// W and X.
+__device__ __forceinline__ void tile_place(int pos, int mt, int nt, int& im, int& in) {
+  const int band = pos / (8 * nt), at = pos - band * 8 * nt;
+  const int high = min(8, mt - band * 8);
+  in = at / high;
+  im = band * 8 + at - in * high;
+}
+
+template <int BN, int BM, typename OT, bool GROUPED>
+__global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) {
+  constexpr int NI = BN / 64, MI = BM / 64;      // 32-row fragments of a wave
+  constexpr int NL = BN / 32, ML = BM / 32;      // direct loads of a wave and step
+  __shared__ __attribute__((aligned(16))) uint8_t s0[(BN + BM) * kStepB], s1[(BN + BM) * kStepB];
+  __shared__ __attribute__((aligned(16))) uint8_t scl[(BN + BM) * kWindow];
+  __shared__ __attribute__((aligned(16))) uint8_t out[4 * 32 * 128];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nb = (int)(a.k / kMxBlock);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
+  const int all_nb = (int)(a.k / kMxBlock);
   const int64_t kb = a.k / 2;
-  const int steps = (nb + 7) / 8;
-  auto w_row = [&](int r) { return (int64_t)t.expert * a.n + min(n0 + r, a.n - 1); };
-  auto x_row = [&](int r) -> int64_t {
-    const int64_t row = min(t.m0 + r, t.m1 - 1);
-    return a.x_rows ? min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1) : row;
+
+  // ---- the tile at hand
+  int64_t n0;
+  Tile t;
+  int b0, nb, slot;                              // first block and blocks of its slice of K; slot of `part` or -1
+  Rsrc wc, xc;
+  const uint8_t *psw, *psx;
+  uint32_t ow[NL], ox[ML];                       // direct load i of this lane: bytes from wc, xc
+  const int mt = GROUPED ? live_tiles(a, BM) : plan.mt;
+  const int full = GROUPED ? mt * plan.nt : plan.full;
+  const int items = full + plan.rest * plan.split;
+  // Consecutive workgroups go to the eight XCDs in turn: of every round of tiles
+  // each XCD takes adjacent ones.
+  const int grid = gridDim.x, b = blockIdx.x;
+  const int place = (b % 8) * (grid / 8) + min(b % 8, grid % 8) + b / 8;
+  const int chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+  auto set_tile = [&](int item) {
+    int im, in, pos = item;
+    b0 = 0;
+    nb = all_nb;
+    slot = -1;
+    if (!GROUPED && item >= full) {
+      slot = item - full;
+      pos = full + slot / plan.split;
+      const int s = slot % plan.split, windows = (all_nb + kWindow - 1) / kWindow;
+      b0 = windows * s / plan.split * kWindow;
+      nb = min(windows * (s + 1) / plan.split * kWindow, all_nb) - b0;
+    }
+    tile_place(pos, mt, plan.nt, im, in);
+    if (GROUPED)
+      t = find_tile(a, BM, im);
+    else
+      t = Tile{(int64_t)im * BM, min((int64_t)(im + 1) * BM, a.m), 0};
+    n0 = (int64_t)in * BN;
+    const int64_t w0 = (int64_t)t.expert * a.n + n0;
+    const int w_rows = (int)min((int64_t)BN, a.n - n0), x_rows = (int)(t.m1 - t.m0);
+    // X rows, from row x0: of this lane's direct loads and of its scale bytes
+    int64_t xr[ML + 1];
+#pragma unroll
+    for (int i = 0; i <= ML; i++) xr[i] = min(i < ML ? (4 * i + wave) * 8 + (lane >> 3) : tid % BM, x_rows - 1);
+    if (GROUPED && a.x_rows) {
+#pragma unroll
+      for (int i = 0; i <= ML; i++) xr[i] = a.x_rows[t.m0 + xr[i]];
+#pragma unroll
+      for (int i = 0; i <= ML; i++) xr[i] = min(max(xr[i], (int64_t)0), a.x_rows_total - 1);
+    }
+    const bool gather = GROUPED && a.x_rows;
+    const int64_t x0 = gather ? 0 : t.m0, x_span = gather ? a.x_rows_total : x_rows;
+    wc = rsrc_of(a.wc + w0 * kb + b0 * 16, w_rows * kb - b0 * 16);
+    xc = rsrc_of(a.xc + x0 * kb + b0 * 16, x_span * kb - b0 * 16);
+#pragma unroll
+    for (int i = 0; i < NL; i++) ow[i] = (uint32_t)(min((4 * i + wave) * 8 + (lane >> 3), w_rows - 1) * kb);
+#pragma unroll
+    for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(xr[i] * kb);
+    psw = a.ws + (w0 + min(tid % BN, w_rows - 1)) * all_nb + b0;
+    psx = a.xs + (x0 + xr[ML]) * all_nb + b0;
   };
-  // direct loads: instruction i of a wave fills rows (4 i + wave) * 8 ..+7
-  const int chunk = (lane & 7) ^ (lane >> 3);
-  const uint8_t* wc = a.wc + ((int64_t)t.expert * a.n + n0) * kb;
-  const int64_t x_first = a.x_rows ? 0 : t.m0;
-  const uint8_t* xc = a.xc + x_first * kb;
-  uint32_t ow[BN / 32], ox[BM / 32];  // the rows' bytes, from the tile's first row (gathered ones from X's)
-#pragma unroll
-  for (int i = 0; i < BN / 32; i++) ow[i] = (uint32_t)(min((int64_t)((4 * i + wave) * 8 + (lane >> 3)), a.n - 1 - n0) * kb);
-#pragma unroll
-  for (int i = 0; i < BM / 32; i++) ox[i] = (uint32_t)((x_row((4 * i + wave) * 8 + (lane >> 3)) - x_first) * kb);
-  auto load_step = [&](int s, uint8_t* lw, uint8_t* lx) {
+  // A step's loads go out in two parts, the X rows' behind the W rows'.
+  struct XLoads {
+    Rsrc r;
+    uint32_t at[ML];
+  };
+  auto load_w = [&](int s, uint8_t* l) {
     const uint32_t col = (uint32_t)min(s * 8 + chunk, nb - 1) * 16;
 #pragma unroll
-    for (int i = 0; i < BN / 32; i++) load_lds16(wc + (uint64_t)(ow[i] + col), lw + (4 * i + wave) * 1024);
+    for (int i = 0; i < NL; i++) load_lds16(wc, ow[i] + col, l + (4 * i + wave) * 1024);
+    XLoads x;
+    x.r = xc;
 #pragma unroll
-    for (int i = 0; i < BM / 32; i++) load_lds16(xc + (uint64_t)(ox[i] + col), lx + (4 * i + wave) * 1024);
+    for (int i = 0; i < ML; i++) x.at[i] = ox[i] + col;
+    return x;
   };
-  // scale bytes: thread i carries row i of either tile, 16 blocks (a window) at a time
-  const uint8_t* psw = a.ws + w_row(tid % BN) * nb;
-  const uint8_t* psx = a.xs + x_row(tid % BM) * nb;
+  auto load_x = [&](const XLoads& x, uint8_t* l) {
+#pragma unroll
+    for (int i = 0; i < ML; i++) load_lds16(x.r, x.at[i], l + BN * kStepB + (4 * i + wave) * 1024);
+  };
+  // scale bytes: thread i carries row i of either side.  A window that K does not
+  // fill is read further left and moved down, with zeros behind.
   struct Window {
     u32x4_t w, x;
+    int skip;  // bytes ahead of the window's first
   };
-  auto load_window = [&](int b) {
+  auto load_window = [&](int w) {
     Window v;
+    const int b = min(w * kWindow, all_nb - b0 - kWindow);
+    v.skip = w * kWindow - b;
     __builtin_memcpy(&v.w, psw + b, 16);
     __builtin_memcpy(&v.x, psx + b, 16);
     return v;
   };
-  auto store_window = [&](const Window& v) {
-    if (BN == 256 || tid < BN) *(u32x4_t*)(scw + tid * 16) = v.w;
-    if (BM == 256 || tid < BM) *(u32x4_t*)(scx + tid * 16) = v.x;
+  auto moved = [&](u32x4_t v, int skip) {
+    if (skip & 8) v = u32x4_t{v[2], v[3], 0, 0};
+    if (skip & 4) v = u32x4_t{v[1], v[2], v[3], 0};
+    const uint32_t n = (uint32_t)skip & 3;
+    return u32x4_t{__builtin_amdgcn_alignbyte(v[1], v[0], n), __builtin_amdgcn_alignbyte(v[2], v[1], n),
+                   __builtin_amdgcn_alignbyte(v[3], v[2], n), __builtin_amdgcn_alignbyte(0u, v[3], n)};
   };
-  auto tail_window = [&](int b) {  // zeros from the end of K on
-#pragma unroll 1
-    for (int i = 0; i < 16; i++) {
-      const int c = min(b + i, nb - 1);
-      if (tid < BN) scw[tid * 16 + i] = b + i < nb ? psw[c] : 0;
-      if (tid < BM) scx[tid * 16 + i] = b + i < nb ? psx[c] : 0;
-    }
+  auto store_window = [&](const Window& v) {
+    if (BN == 256 || tid < BN) *(u32x4_t*)(scl + tid * 16) = moved(v.w, v.skip);
+    if (BM == 256 || tid < BM) *(u32x4_t*)(scl + (BN + tid) * 16) = moved(v.x, v.skip);
   };
 
-  const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
-  const int half = lane >> 5, l32 = lane & 31;
   struct Frags {
     u32x4_t w[NI], x[MI];
   };
-  struct Dwords {
+  struct Scales {
     uint32_t w[NI], x[MI];
   };
-  auto read_frags = [&](const uint8_t* lw, const uint8_t* lx, int kk) {
+  auto read_frags = [&](const uint8_t* l, int i) {
     Frags f;
-    const int place = ((half * 4 + kk) ^ (l32 & 7)) * 16;
+    const int at = l32 * kStepB + ((4 * half + i) ^ (l32 & 7) ^ ((l32 >> 3) & 1)) * 16;
 #pragma unroll
-    for (int i = 0; i < NI; i++) f.w[i] = *(const u32x4_t*)(lw + (wn + i * 32 + l32) * kRowB + place);
+    for (int j = 0; j < NI; j++) f.w[j] = *(const u32x4_t*)(l + (wn + j * 32) * kStepB + at);
 #pragma unroll
-    for (int i = 0; i < MI; i++) f.x[i] = *(const u32x4_t*)(lx + (wm + i * 32 + l32) * kRowB + place);
+    for (int j = 0; j < MI; j++) f.x[j] = *(const u32x4_t*)(l + (BN + wm + j * 32) * kStepB + at);
     return f;
   };
   auto read_scales = [&](int step) {  // of the window
-    Dwords d;
+    Scales d;
+    const int at = l32 * 16 + step * 8 + half * 4;
 #pragma unroll
-    for (int i = 0; i < NI; i++) d.w[i] = *(const uint32_t*)(scw + (wn + i * 32 + l32) * 16 + step * 8 + half * 4);
+    for (int i = 0; i < NI; i++) d.w[i] = *(const uint32_t*)(scl + (wn + i * 32) * 16 + at);
 #pragma unroll
-    for (int i = 0; i < MI; i++) d.x[i] = *(const uint32_t*)(scx + (wm + i * 32 + l32) * 16 + step * 8 + half * 4);
+    for (int i = 0; i < MI; i++) d.x[i] = *(const uint32_t*)(scl + (BN + wm + i * 32) * 16 + at);
     return d;
   };
   f32x16_t acc[NI][MI];
-#pragma unroll
-  for (int i = 0; i < NI; i++)
-#pragma unroll
-    for (int j = 0; j < MI; j++)
-#pragma unroll
-      for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
-  auto products = [&](auto kk, const Frags& f, const Dwords& d) {
-    constexpr int I = decltype(kk)::value;
+  auto products = [&](auto ii, const Frags& f, const Scales& d) {
+    constexpr int I = decltype(ii)::value;
 #pragma unroll
     for (int i = 0; i < NI; i++)
 #pragma unroll
@@ -251,103 +343,159 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
 #pragma unroll
       for (int j = 0; j < MI; j++) asm volatile("" : "+a"(acc[i][j]));
   };
-  typedef std::integral_constant<int, 0> K0;
-  typedef std::integral_constant<int, 1> K1;
-  typedef std::integral_constant<int, 2> K2;
-  typedef std::integral_constant<int, 3> K3;
-  // One step from buffer (lw, lx), f its first fragments; `behind` runs after the
-  // barrier and returns the next step's first fragments.
-  // The instruction order asked for: a sub-step's LDS reads, then the direct loads,
-  // one at a time between its products.
+  // The instruction order asked for: LDS reads, then memory loads, one at a time
+  // between the products.
   auto spread = [&](int reads, int loads) {
 #pragma unroll
     for (int i = 0; i < NI * MI; i++) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i < reads - NI * MI) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       if (i < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (i < loads - NI * MI) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto step = [&](const uint8_t* lw, const uint8_t* lx, Frags f, const Dwords& d, auto behind) {
-    Frags g = read_frags(lw, lx, 1);
-    products(K0{}, f, d);
-    spread(NI + MI, 2);
-    f = read_frags(lw, lx, 2);
-    products(K1{}, g, d);
+  typedef std::integral_constant<int, 0> C0;
+  typedef std::integral_constant<int, 1> C1;
+  typedef std::integral_constant<int, 2> C2;
+  typedef std::integral_constant<int, 3> C3;
+  // A step from `l` with its first fragments f; returns the next step's, from
+  // `next`.  `late` issues the loads that the step before left, `behind` those
+  // that wait for the barrier.
+  auto run_step = [&](const uint8_t* l, const uint8_t* next, Frags f, const Scales& d, auto late, auto behind) {
+    Frags g = read_frags(l, 1);
+    late();
+    products(C0{}, f, d);
+    spread(NI + MI, ML + 2);
+    f = read_frags(l, 2);
+    products(C1{}, g, d);
     spread(NI + MI, 0);
-    g = read_frags(lw, lx, 3);
-    products(K2{}, f, d);
+    g = read_frags(l, 3);
+    products(C2{}, f, d);
     spread(NI + MI, 0);
     pin();
-    __syncthreads();
-    f = behind();
-    products(K3{}, g, d);
-    spread(NI * MI, (BN + BM) / 32);
+    wait_and_meet();
+    behind();
+    f = read_frags(next, 0);
+    products(C3{}, g, d);
+    spread(2 * (NI + MI), NL);
     pin();
     return f;
   };
 
-  load_step(0, w0, x0);
-  if (steps > 1) load_step(1, w1, x1);
-  if (nb >= 16)
-    store_window(load_window(0));
-  else
-    tail_window(0);
-  __syncthreads();
-  Frags f = read_frags(w0, x0, 0);
-  Dwords da = read_scales(0), db = read_scales(1);
-  int s = 0;
-  // Two steps (a window) a round.  While the next window lies within K there is
-  // nothing to ask on the way, and the loads spread between the products.
-  for (; s * 8 + 32 <= nb; s += 2) {
-    const Window v = load_window(s * 8 + 16);
-    f = step(w0, x0, f, da, [&]() {
-      store_window(v);  // ahead of the loads, which the compiler would have it wait for
-      __builtin_amdgcn_sched_barrier(0);
-      load_step(s + 2, w0, x0);
-      return read_frags(w1, x1, 0);
-    });
-    f = step(w1, x1, f, db, [&]() {
-      load_step(s + 3, w1, x1);
-      da = read_scales(0);
-      return read_frags(w0, x0, 0);
-    });
-    db = read_scales(1);
-  }
-  // the last ones, where K may end
-  for (; s < steps; s += 2) {
-    f = step(w0, x0, f, da, [&]() {
-      if (s + 2 < steps) load_step(s + 2, w0, x0);
-      tail_window(s * 8 + 16);
-      return read_frags(w1, x1, 0);
-    });
-    if (s + 1 == steps) break;
-    f = step(w1, x1, f, db, [&]() {
-      if (s + 3 < steps) load_step(s + 3, w1, x1);
-      da = read_scales(0);
-      return read_frags(w0, x0, 0);
-    });
-    db = read_scales(1);
-  }
-#pragma unroll
-  for (int j = 0; j < MI; j++) {
-    const int64_t row = t.m0 + wm + j * 32 + l32;
-    if (row >= t.m1) continue;
-    bool none = false;
-    if (a.x_rows) {
-      const int64_t r = a.x_rows[row];
-      none = r < 0 || r >= a.x_rows_total;
-    }
+  int item = place;
+  if (item >= items) return;
+  set_tile(item);
+  load_x(load_w(0, s0), s0);
+  XLoads x = load_w(1, s1);
+  store_window(load_window(0));
+  wait_and_meet();
+  Frags f = read_frags(s0, 0);
+  Scales d0 = read_scales(0), d1 = read_scales(1);
+  while (true) {
 #pragma unroll
     for (int i = 0; i < NI; i++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int64_t n = n0 + wn + i * 32 + q * 8 + half * 4;
-        float v[4];
+      for (int j = 0; j < MI; j++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = none ? 0.0f : acc[i][j][q * 4 + e];
-        if (n < a.n) store4((OT*)a.y, row, n, a.n, v);
+        for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+    const Tile done = t;
+    const int64_t dn0 = n0;
+    const int dslot = slot, windows = (nb + kWindow - 1) / kWindow;
+    item += grid;
+    // The loads run a window ahead, in the tile's last one into the next tile (the
+    // last tile's go to waste).  K that ends inside a window is filled up with
+    // blocks of scale 0.
+#pragma unroll 1
+    for (int w = 0; w < windows; w++) {
+      int next = w + 1;
+      if (next == windows) {
+        next = 0;
+        if (item < items) set_tile(item);
       }
+      const Window v = load_window(next);
+      f = run_step(s0, s1, f, d0, [&]() { load_x(x, s1); }, [&]() {
+        store_window(v);  // ahead of the loads, so that none is waited for
+        __builtin_amdgcn_sched_barrier(0);
+        x = load_w(next * 2, s0);
+      });
+      f = run_step(s1, s0, f, d1, [&]() { load_x(x, s0); }, [&]() {
+        d0 = read_scales(0);
+        x = load_w(next * 2 + 1, s1);
+      });
+      d1 = read_scales(1);
+    }
+
+    // ---- this tile's results
+    // The accumulators are taken out of their registers where they are written, not
+    // all at once, and the addresses are worked out here, not kept from before the
+    // loop: either would spill.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int half = lane >> 5, l32 = lane & 31;
+    if (!GROUPED && dslot >= 0) {  // a slice's sums, in the order of the registers
+      f32x4_t* p = (f32x4_t*)(plan.part + (int64_t)dslot * BM * BN) + wave * (NI * MI * 4 * 64) + lane;
+#pragma unroll
+      for (int i = 0; i < NI; i++)
+#pragma unroll
+        for (int j = 0; j < MI; j++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            f32x16_t& c = acc[i][j];
+            if (q == 0) asm volatile("" : "+a"(c));
+            p[((i * MI + j) * 4 + q) * 64] = f32x4_t{c[q * 4], c[q * 4 + 1], c[q * 4 + 2], c[q * 4 + 3]};
+          }
+    } else {
+      typedef OT V4 __attribute__((ext_vector_type(4)));
+      constexpr int kCols = 128 / sizeof(OT), kPer = 16 / sizeof(OT), kFr = kCols / 32;  // columns of a pass, a store
+      const int rows = (int)(done.m1 - done.m0), cols = (int)min(a.n - dn0, (int64_t)BN);
+      uint8_t* o = out + wave * (32 * 128);
+      const int r0 = lane >> 3, c0 = (lane & 7) * kPer;  // of a store within its 8 rows
+      OT* y = (OT*)a.y + (done.m0 + wm + r0) * a.n + dn0 + wn + c0;
+#pragma unroll
+      for (int j = 0; j < MI; j++) {
+        bool none = false;
+        if (GROUPED && a.x_rows && wm + j * 32 + l32 < rows) {
+          const int64_t r = a.x_rows[done.m0 + wm + j * 32 + l32];
+          none = r < 0 || r >= a.x_rows_total;
+        }
+#pragma unroll
+        for (int p = 0; p < NI / kFr; p++) {
+#pragma unroll
+          for (int i = 0; i < kFr; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              f32x16_t& c = acc[p * kFr + i][j];
+              if (q == 0) asm volatile("" : "+a"(c));
+              V4 v = {mx_cvt<OT>(c[q * 4]), mx_cvt<OT>(c[q * 4 + 1]), mx_cvt<OT>(c[q * 4 + 2]), mx_cvt<OT>(c[q * 4 + 3])};
+              if (GROUPED && none) v = V4{};
+              const int byte = (i * 32 + q * 8 + half * 4) * (int)sizeof(OT);
+              *(V4*)(o + l32 * 128 + (((byte >> 4) ^ (l32 & 7)) << 4) + (byte & 15)) = v;
+            }
+          wave_lds_sync();
+          const int n = wn + p * kCols + c0;
+          u32x4_t v[4];
+#pragma unroll
+          for (int s = 0; s < 4; s++) v[s] = *(const u32x4_t*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
+#pragma unroll
+          for (int s = 0; s < 4; s++)
+            if (wm + j * 32 + s * 8 + r0 < rows && n + kPer <= cols)
+              __builtin_memcpy(y + (int64_t)(j * 32 + s * 8) * a.n + p * kCols, &v[s], 16);
+          if (cols % kPer) {  // the columns of a width that ends inside a store
+#pragma unroll 1
+            for (int s = 0; s < 4; s++) {
+              const OT* e = (const OT*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
+              if (wm + j * 32 + s * 8 + r0 < rows && n < cols && n + kPer > cols)
+#pragma unroll 1
+                for (int i = 0; n + i < cols; i++) y[(int64_t)(j * 32 + s * 8) * a.n + p * kCols + i] = e[i];
+            }
+          }
+          wave_lds_sync();
+        }
+      }
+    }
+    if (item >= items) return;
   }
 }
 
@@ -370,11 +518,6 @@ __global__ __launch_bounds__(256, BN * BM > 128 * 128 ? 1 : 2) void mx_tile_kern
 // Reads past the last W row return zero (the buffer descriptor ends there), so
 // the loop has no branch around a load.
 constexpr int kSRows = 16, kSUnit = 512, kSAhead = 4, kSMaxWaves = 8;
-
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-__device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
-}
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
@@ -587,34 +730,112 @@ hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream
   }
 }
 
-template <int BN, int BM, typename OT> hipError_t go_tile(const Args& a, hipStream_t stream) {
-  const int64_t nt = (a.n + BN - 1) / BN;
-  const int64_t mt = (a.m + BM - 1) / BM + (a.offsets ? min((int64_t)a.experts, a.m) : 0);
-  hipLaunchKernelGGL((mx_tile_kernel<BN, BM, OT>), dim3((unsigned)(nt * mt)), dim3(256), 0, stream, a, mt);
-  return hipGetLastError();
+// y of the split tiles: adds the slices' sums, slice by slice.  A thread takes 16
+// sums of one fragment in register order; the half-waves swap so that each lane
+// stores runs of eight columns.
+template <int BN, int BM, typename OT>
+__global__ __launch_bounds__(256) void mx_fold_kernel(Args a, TilePlan plan) {
+  constexpr int NI = BN / 64, MI = BM / 64;
+  typedef OT V8 __attribute__((ext_vector_type(8)));
+  const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+  const int piece = blockIdx.x * 4 + (threadIdx.x >> 6);  // fragment of a tile
+  const int tile = piece / (4 * NI * MI), frag = piece % (4 * NI * MI);
+  const int wave = frag / (NI * MI), i = frag % (NI * MI) / MI, j = frag % MI;
+  int im, in;
+  tile_place(plan.full + tile, plan.mt, plan.nt, im, in);
+  f32x4_t v[4] = {};
+  const f32x4_t* p = (const f32x4_t*)plan.part + ((int64_t)tile * plan.split * 4 * NI * MI + frag) * 256 + lane;
+  for (int s = 0; s < plan.split; s++, p += 4 * NI * MI * 256)
+#pragma unroll
+    for (int q = 0; q < 4; q++) v[q] += p[q * 64];
+  const int64_t row = (int64_t)im * BM + (wave >> 1) * (BM / 2) + j * 32 + l32;
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    // of columns 8 q .. 8 q + 15 the lower half-wave stores the first eight, the upper the others
+    f32x4_t other;
+#pragma unroll
+    for (int e = 0; e < 4; e++) other[e] = __shfl_xor(half ? v[q][e] : v[q + 1][e], 32, 64);
+    const f32x4_t lo = half ? other : v[q], hi = half ? v[q + 1] : other;
+    const int64_t n = (int64_t)in * BN + (wave & 1) * (BN / 2) + i * 32 + (q + half) * 8;
+    if (row >= a.m || n >= a.n) continue;
+    OT* y = (OT*)a.y + row * a.n + n;
+    V8 o;
+#pragma unroll
+    for (int e = 0; e < 8; e++) o[e] = mx_cvt<OT>(e < 4 ? lo[e] : hi[e - 4]);
+    if (n + 8 <= a.n) {
+      __builtin_memcpy(y, &o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        if (n + e < a.n) y[e] = o[e];
+    }
+  }
 }
 
-template <typename OT> hipError_t run(const Args& a, hipStream_t stream) {
-  return go_tile<256, 256, OT>(a, stream);
+// The tiles of a product.  The last, partly filled round of tiles is cut along K
+// where that is quicker: a tile costs about 1.75 us a step and 8 us around them,
+// folding 4 us and its sums at 7 TB/s (out of the Infinity Cache).
+constexpr int kTileN = 256, kTileM = 256;
+TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
+  TilePlan p = {};
+  const int cus = device_cu_count();
+  p.nt = (int)((n + kTileN - 1) / kTileN);
+  p.mt = (int)((m + kTileM - 1) / kTileM + min(experts, m));
+  p.full = p.mt * p.nt;
+  p.split = 1;
+  if (experts) return p;
+  const int rest = p.full % cus, windows = (int)((k + kWindow * kMxBlock - 1) / (kWindow * kMxBlock));
+  double best = windows * 3.5;
+  for (int s = 2; s <= 8 && rest > 0 && rest * s <= cus && s <= windows; s++) {
+    const double t = (windows + s - 1) / s * 3.5 + 4.0 + rest * s * (kTileN * kTileM * 4 / 7e6);
+    if (t < best) best = t, p.split = s;
+  }
+  if (p.split > 1) p.rest = rest, p.full -= rest;
+  return p;
+}
+size_t tile_ws_bytes(const TilePlan& p) { return (size_t)p.rest * p.split * kTileN * kTileM * 4; }
+
+template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t stream) {
+  TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0);
+  p.part = (float*)ws;
+  const int grid = min(p.full + p.rest * p.split, device_cu_count());
+  if (a.offsets)
+    hipLaunchKernelGGL((mx_tile_kernel<kTileN, kTileM, OT, true>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<kTileN, kTileM, OT, false>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.rest) {
+    hipLaunchKernelGGL((mx_fold_kernel<kTileN, kTileM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (kTileM / 64))),
+                       dim3(256), 0, stream, a, p);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+// Whether a product runs on the stream kernel: few rows of one product (of one
+// expert, on average), or K below a window of the tile kernel.
+bool streams(int64_t m, int64_t k, int64_t experts, StreamPlan& p) {
+  const int64_t rows = experts ? (m + experts - 1) / experts : m;
+  p = stream_plan(rows, k);
+  return p.u && (rows <= 64 || k < kWindow * kMxBlock);
 }
 
 }  // namespace
 
-size_t mx_gemm_ws_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
+  StreamPlan p;
+  return streams(m, k, experts, p) ? 0 : tile_ws_bytes(tile_plan(m, n, k, experts));
+}
 
-hipError_t launch_mx_gemm(const MxGemm& g, void*, size_t, hipStream_t stream) {
+hipError_t launch_mx_gemm(const MxGemm& g, void* ws, size_t, hipStream_t stream) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
   const Args a = {g.x.codes, g.x.scales, g.w.codes, g.w.scales, g.m, g.n, g.k, g.x.rows, g.y, g.offsets, g.x_rows,
                   g.experts};
-  // rows of one product: of one expert, on average
-  const int64_t rows = g.offsets ? (g.m + g.experts - 1) / g.experts : g.m;
-  if (rows <= 64) {
-    const StreamPlan p = stream_plan(rows, g.k);
-    if (p.u) return run_stream(a, g.y_dtype, p, stream);
-  }
-  if (g.y_dtype == kF32) return run<float>(a, stream);
-  if (g.y_dtype == kF16) return run<_Float16>(a, stream);
-  return run<__bf16>(a, stream);
+  StreamPlan p;
+  if (streams(g.m, g.k, g.offsets ? g.experts : 0, p)) return run_stream(a, g.y_dtype, p, stream);
+  if (g.y_dtype == kF32) return run<float>(a, ws, stream);
+  if (g.y_dtype == kF16) return run<_Float16>(a, ws, stream);
+  return run<__bf16>(a, ws, stream);
 }
 
 }  // namespace rz
