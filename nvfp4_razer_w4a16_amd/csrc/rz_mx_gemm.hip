@@ -502,25 +502,35 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // ---- stream kernel -------------------------------------------------------------
 // For few rows of X the product is a read of W.  A workgroup owns 16 W rows at a
 // time (a "row tile") and all of K; each of its up to eight waves takes U units
-// of 512 elements of K and keeps its share of up to 16 MT rows of X in registers
-// for all the row tiles that the workgroup walks through, so that nothing but W
-// is read in the loop.
+// of 512 elements of K and keeps its share of up to 16 MT rows of X (a "job") in
+// registers for all the row tiles that the workgroup walks through, so that
+// nothing but W is read in the loop.  The row tiles of all jobs stand in one line
+// that is cut evenly between the workgroups, however the rows are spread over the
+// experts; a cut that crosses jobs loads the next one's X on the way.
 //
 // A unit (16 rows x 256 bytes) is loaded with four instructions that each cover
-// 256 contiguous bytes of four rows, four units ahead of their use, and turned
-// through a wave's own LDS stage into the operand's layout (chunk c of row r at
-// place c ^ r: no bank conflicts either way).  Group g = lane / 16 takes block
-// 4g + s of a unit at MFMA s, so its scale bytes are one dword.  The scale bytes
-// of a row tile are one contiguous piece of memory; the workgroup loads it a
-// tile ahead and hands it round in LDS.  The waves' partial sums meet in LDS,
-// one barrier a row tile (both areas are double-buffered).
+// 256 contiguous bytes of four rows, two units ahead of their use (four ahead cost
+// registers, hence waves, and took 5-40 % longer), and turned through a wave's own
+// LDS stage into the operand's layout (chunk c of row r at place c ^ r: no bank
+// conflicts either way).  Group g = lane / 16 takes block 4g + s of a unit at MFMA
+// s, so its scale bytes are one dword.  The scale bytes of a row tile are one
+// contiguous piece of memory; the workgroup loads it a tile ahead and hands it
+// round in LDS.  The waves' partial sums meet in LDS, one barrier a row tile (both
+// areas are double-buffered).
 //
 // Reads past the last W row return zero (the buffer descriptor ends there), so
 // the loop has no branch around a load.
-constexpr int kSRows = 16, kSUnit = 512, kSAhead = 4, kSMaxWaves = 8;
+constexpr int kSRows = 16, kSUnit = 512, kSAhead = 2, kSMaxWaves = 8;
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
+}
+
+// LDS of a workgroup: a stage a wave, two sets of partial sums, the scale bytes of
+// two row tiles, each from the dword that holds the first.
+constexpr int scale_area(int nb) { return (kSRows * nb + 3 + 4 + 15) & ~15; }
+constexpr size_t stream_lds(int waves, int mt, int nb) {
+  return (size_t)waves * (kSRows * 256 + 2 * 4 * kSRows * 16 * mt) + 2 * scale_area(nb);
 }
 
 template <int U, int MT>
@@ -528,91 +538,95 @@ __global__ __launch_bounds__(64 * kSMaxWaves, U * MT == 1 ? 4 : 2) void mx_strea
   constexpr int kPart = kSRows * 16 * MT;  // fp32 sums of one wave
   constexpr int kChunks = U / 4 + 1;       // 16-byte chunks of a tile's scale bytes a thread carries: nb + 1 <= 16 U waves + 1
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const Tile t = find_tile(a, 16 * MT, blockIdx.y);
-  if (t.expert < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
   const int g = lane >> 4, l16 = lane & 15;
+  const int sc_bytes = scale_area(nb);
   uint8_t* stage = smem + wave * (kSRows * 256);
-  float* part = (float*)(smem + waves * (kSRows * 256));            // [2][waves][kPart]
-  uint8_t* sc = (uint8_t*)(part + 2 * waves * kPart);                // [2][sc_bytes]
-  const int sc_bytes = (kSRows * nb + 4 + 15 + 4) & ~15;             // a tile's scale bytes, dword-aligned start
+  float* part = (float*)(smem + waves * (kSRows * 256));  // [2][waves][kPart]
+  uint8_t* sc = (uint8_t*)(part + 2 * waves * kPart);      // [2][sc_bytes]
   const int unit0 = wave * U;
-  const uint8_t* wc = a.wc + (int64_t)t.expert * a.n * kb;
-  const uint8_t* wsc = a.ws + (int64_t)t.expert * a.n * nb;
   const int tiles = (int)((a.n + kSRows - 1) / kSRows);
 
-  // this wave's share of X
-  u32x4_t fx[MT][U][4];
-  uint32_t dx[MT][U];
-  const int64_t last = t.m1 - 1;
-#pragma unroll
-  for (int j = 0; j < MT; j++) {
-    int64_t row = min(t.m0 + 16 * j + l16, last);
-    if (a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
-    const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int b = (unit0 + u) * 16 + 4 * g;
-#pragma unroll
-      for (int s = 0; s < 4; s++) fx[j][u][s] = *(const u32x4_t*)(pc + min(b + s, nb - 1) * 16);
-      dx[j][u] = scales4(ps, b, nb);
-    }
-  }
-
-  // W units: slot i of a round is unit i % U of row tile i / U of the round
-  constexpr int kRound = U > kSAhead ? U : kSAhead, kTilesRound = kRound / U;
-  u32x4_t fw[kSAhead][4];
-  int voff[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) voff[i] = (4 * i + g) * kb + l16 * 16;
-  const int step = (int)gridDim.x;
-  auto load_unit = [&](int tile, int u, u32x4_t (&v)[4]) {
-    const int n0 = tile * kSRows, col = (unit0 + u) * 256;
-    const int rows = min(max((int)a.n - n0, 0), kSRows);
-    const Rsrc r = rsrc_of(wc + (int64_t)n0 * kb + col, max(rows * kb - col, 0));
-#pragma unroll
-    for (int i = 0; i < 4; i++) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 0);
-  };
-  // A row tile's scale bytes, from the dword that holds its first one; thread i
-  // carries 16 bytes of every 16 * (threads).  Dwords that hold none of the bytes
-  // read zero.
-  struct Scales {
-    u32x4_t v[kChunks];
-  };
-  auto load_scales = [&](int tile) {
-    const int n0 = tile * kSRows, rows = min(max((int)a.n - n0, 0), kSRows);
-    const uint8_t* p = wsc + (int64_t)n0 * nb;
-    const int skew = (int)((uintptr_t)p & 3);
-    const Rsrc r = rsrc_of(p - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
-    Scales s;
-#pragma unroll
-    for (int i = 0; i < kChunks; i++)
-      s.v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (i * 64 * waves + tid) * 16, 0, 0);
-    return s;
-  };
-  auto keep_scales = [&](const Scales& s, int buf) {
-#pragma unroll
-    for (int i = 0; i < kChunks; i++) {
-      const int at = (i * 64 * waves + tid) * 16;
-      if (at < sc_bytes) *(u32x4_t*)(sc + buf * sc_bytes + at) = s.v[i];
-    }
-  };
-  auto skew_of = [&](int tile) { return (int)((uintptr_t)(wsc + (int64_t)tile * kSRows * nb) & 3); };
-
-  int tile = blockIdx.x;
-#pragma unroll
-  for (int i = 0; i < kSAhead; i++) load_unit(tile + i / U * step, i % U, fw[i]);
-  keep_scales(load_scales(tile), 0);
-  __syncthreads();
-
-  f32x4_t acc[MT];
+  // this workgroup's piece of the line
+  const int64_t line = (int64_t)tiles * (a.offsets ? live_tiles(a, 16 * MT) : (a.m + 16 * MT - 1) / (16 * MT));
+  int64_t at = line * blockIdx.x / gridDim.x;
+  int left = (int)(line * (blockIdx.x + 1) / gridDim.x - at);
+  int job = (int)(at / tiles), tile = (int)(at - (int64_t)job * tiles);
   int buf = 0;
-  // row tile RT of a round
-  auto row_tile = [&](auto which) {
+  for (; left > 0; job++, tile = 0) {
+    const Tile t = find_tile(a, 16 * MT, job);
+    if (t.expert < 0) return;
+    const uint8_t* wc = a.wc + (int64_t)t.expert * a.n * kb;
+    const uint8_t* wsc = a.ws + (int64_t)t.expert * a.n * nb;
+    const int end = min(tile + left, tiles);
+    left -= end - tile;
+
+    // W units: slot i of a round is unit i % U of row tile i / U of the round
+    constexpr int kRound = U > kSAhead ? U : kSAhead, kTilesRound = kRound / U;
+    u32x4_t fw[kSAhead][4];
+    int voff[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) voff[i] = (4 * i + g) * kb + l16 * 16;
+    auto rows_of = [&](int tile) { return tile < end ? min((int)a.n - tile * kSRows, kSRows) : 0; };
+    auto load_unit = [&](int tile, int u, u32x4_t (&v)[4]) {
+      const int col = (unit0 + u) * 256;
+      const Rsrc r = rsrc_of(wc + (int64_t)tile * kSRows * kb + col, max(rows_of(tile) * kb - col, 0));
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 0);
+    };
+    // A row tile's scale bytes, in whole dwords: up to three bytes on either side
+    // are not its own and not looked at.  Thread i carries 16 bytes of every
+    // 16 * (threads); dwords that hold none of the tile's bytes read zero.
+    struct Scales {
+      u32x4_t v[kChunks];
+    };
+    auto skew_of = [&](int tile) { return (int)((uintptr_t)(wsc + (int64_t)tile * kSRows * nb) & 3); };
+    auto load_scales = [&](int tile) {
+      const int rows = rows_of(tile), skew = skew_of(tile);
+      const Rsrc r = rsrc_of(wsc + (int64_t)tile * kSRows * nb - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
+      Scales s;
+#pragma unroll
+      for (int i = 0; i < kChunks; i++)
+        s.v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (i * 64 * waves + tid) * 16, 0, 0);
+      return s;
+    };
+    auto keep_scales = [&](const Scales& s, int buf) {
+#pragma unroll
+      for (int i = 0; i < kChunks; i++) {
+        const int at = (i * 64 * waves + tid) * 16;
+        if (at < sc_bytes) *(u32x4_t*)(sc + buf * sc_bytes + at) = s.v[i];
+      }
+    };
+    const Scales first_sc = load_scales(tile);
+#pragma unroll
+    for (int i = 0; i < kSAhead; i++) load_unit(tile + i / U, i % U, fw[i]);
+
+    // this wave's share of X
+    u32x4_t fx[MT][U][4];
+    uint32_t dx[MT][U];
+#pragma unroll
+    for (int j = 0; j < MT; j++) {
+      int64_t row = min(t.m0 + 16 * j + l16, t.m1 - 1);
+      if (a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
+      const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int b = (unit0 + u) * 16 + 4 * g;
+#pragma unroll
+        for (int s = 0; s < 4; s++) fx[j][u][s] = *(const u32x4_t*)(pc + min(b + s, nb - 1) * 16);
+        dx[j][u] = scales4(ps, b, nb);
+      }
+    }
+    keep_scales(first_sc, buf);
+    __syncthreads();
+
+    // row tile RT of a round; false behind the last one
+    auto row_tile = [&](auto which) {
       constexpr int rt = decltype(which)::value;
-      const Scales next_sc = load_scales(tile + step);
+      const Scales next_sc = load_scales(tile + 1);
       const int skew = skew_of(tile);
+      f32x4_t acc[MT];
 #pragma unroll
       for (int j = 0; j < MT; j++) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -623,7 +637,7 @@ __global__ __launch_bounds__(64 * kSMaxWaves, U * MT == 1 ? 4 : 2) void mx_strea
         for (int i = 0; i < 4; i++)
           *(u32x4_t*)(stage + (4 * i + g) * 256 + ((l16 ^ (4 * i + g)) * 16)) = fw[slot][i];
         const int ahead = u + kA;  // the unit that takes this slot
-        load_unit(tile + ahead / U * step, ahead % U, fw[slot]);
+        load_unit(tile + ahead / U, ahead % U, fw[slot]);
         // scale bytes of blocks b .. b + 3 of row l16, 0 past K
         const int b = (unit0 + u) * 16 + 4 * g, at = skew + l16 * nb + b;
         const uint32_t* q = (const uint32_t*)(sc + buf * sc_bytes) + (min(at, sc_bytes - 8) >> 2);
@@ -653,33 +667,30 @@ __global__ __launch_bounds__(64 * kSMaxWaves, U * MT == 1 ? 4 : 2) void mx_strea
       __syncthreads();
       for (int o = tid; o < kPart; o += 64 * waves) {
         const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
-        const float* p = part + buf * waves * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
-        float v = 0.0f;
-        for (int w = 0; w < waves; w++) v += p[w * kPart];
         const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
-        if (row < t.m1 && col < a.n) {
-          if (a.x_rows) {
-            const int64_t r = a.x_rows[row];
-            if (r < 0 || r >= a.x_rows_total) v = 0.0f;
-          }
-          const int64_t at = row * a.n + col;
-          if (y_dtype == kF32) ((float*)a.y)[at] = v;
-          else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(v);
-          else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(v);
+        if (row >= t.m1 || col >= a.n) continue;
+        const float* p = part + buf * waves * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+        float v[kSMaxWaves];  // all read at once
+#pragma unroll
+        for (int w = 0; w < kSMaxWaves; w++) v[w] = p[min(w, waves - 1) * kPart];
+        float sum = v[0];
+#pragma unroll
+        for (int w = 1; w < kSMaxWaves; w++) sum += w < waves ? v[w] : 0.0f;
+        if (a.x_rows) {
+          const int64_t r = a.x_rows[row];
+          if (r < 0 || r >= a.x_rows_total) sum = 0.0f;
         }
+        const int64_t at = row * a.n + col;
+        if (y_dtype == kF32) ((float*)a.y)[at] = sum;
+        else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(sum);
+        else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(sum);
       }
       buf ^= 1;
-      tile += step;
-      return tile < tiles;
-  };
-  if (tile >= tiles) return;
-  while (true) {
-    if (!row_tile(std::integral_constant<int, 0>{})) return;
-    if constexpr (kTilesRound > 1)
-      if (!row_tile(std::integral_constant<int, 1>{})) return;
-    if constexpr (kTilesRound > 2) {
-      if (!row_tile(std::integral_constant<int, 2>{})) return;
-      if (!row_tile(std::integral_constant<int, 3>{})) return;
+      return ++tile < end;
+    };
+    while (row_tile(std::integral_constant<int, 0>{})) {
+      if constexpr (kTilesRound > 1)
+        if (!row_tile(std::integral_constant<int, 1>{})) break;
     }
   }
 }
@@ -698,21 +709,18 @@ StreamPlan stream_plan(int64_t rows, int64_t k) {
 }
 
 template <int U, int MT> hipError_t go_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t stream) {
-  const int nb = (int)(a.k / kMxBlock);
-  const int sc_bytes = (kSRows * nb + 4 + 15 + 4) & ~15;
-  const size_t lds = (size_t)p.waves * (kSRows * 256 + 2 * 4 * kSRows * 16 * MT) + 2 * sc_bytes;
-  const int64_t tiles = (a.n + kSRows - 1) / kSRows;
-  const int64_t jobs = a.offsets ? min((a.m + 16 * MT - 1) / (16 * MT) + a.experts, a.m) : (a.m + 16 * MT - 1) / (16 * MT);
-  const int64_t slots = (int64_t)device_cu_count() * 2;
-  int64_t per = (tiles * jobs + slots - 1) / slots;  // row tiles a workgroup
-  if (a.offsets) per = min(per, (int64_t)4);         // many of the jobs may be empty
-  const int64_t gx = (tiles + per - 1) / per;
+  const size_t lds = stream_lds(p.waves, MT, (int)(a.k / kMxBlock));
+  const int64_t tiles = (a.n + kSRows - 1) / kSRows, rows = 16 * MT;
+  const int64_t jobs = a.offsets ? min((a.m + rows - 1) / rows + a.experts, a.m) : (a.m + rows - 1) / rows;
+  // as many workgroups as are resident: by registers (16 or 8 waves a CU) and LDS
+  const int per_cu = max(1, min((U * MT == 1 ? 16 : 8) / p.waves, (int)(160 * 1024 / lds)));
+  const int64_t grid = min(tiles * jobs, (int64_t)device_cu_count() * per_cu);
   auto kern = mx_stream_kernel<U, MT>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)gx, (unsigned)jobs), dim3(64 * p.waves), lds, stream, a, y_dtype, p.waves);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * p.waves), lds, stream, a, y_dtype, p.waves);
   return hipGetLastError();
 }
 
