@@ -824,7 +824,7 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 // expert, on average), or K below a window of the tile kernel.
 bool streams(int64_t m, int64_t k, int64_t experts, StreamPlan& p) {
   const int64_t rows = experts ? (m + experts - 1) / experts : m;
-  p = stream_plan(rows, k);
+  p = stream_plan(experts ? rows + rows / 2 : rows, k);
   return p.u && (rows <= 64 || k < kWindow * kMxBlock);
 }
 

@@ -18,6 +18,13 @@ import torch
 
 from . import _DT, RAZER_OK, RazerError, _check_buffer, lib
 
+# Calls on a few rows take microseconds: the checks below are written to cost
+# little beside a launch.
+_Tensor = torch.Tensor
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 RAZER_NORM_POST = 1
 RAZER_MX_MAX_EXPERTS = 4096
 MX_BLOCK = 32
@@ -59,10 +66,11 @@ def _check(status: int, what: str):
 def _stream(stream, device: torch.device) -> int:
     """The caller's stream, or the current one of the tensors' device, which has
     to be the current device: launches go to that one."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    index = device.index
+    if index != _current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{_current_device()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _raw_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -74,7 +82,7 @@ def _dtype(dt: torch.dtype) -> int:
 
 
 def _on_gpu(t, name: str) -> torch.device:
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, not {t.device}")
@@ -92,10 +100,11 @@ class MxTensor:
     def __init__(self, rows: int, cols: int, device):
         if rows < 0 or cols < 0 or cols % MX_BLOCK:
             raise ValueError(f"cols must be a multiple of {MX_BLOCK}")
-        self.rows, self.cols = rows, cols
+        self.rows = rows
+        self.cols = cols
         # one buffer for both: codes, then scales; their views are made when asked for
-        self._buf = torch.empty(rows * cols // 32 * 17, dtype=torch.uint8, device=device)
-        self.device = self._buf.device
+        self._buf = buf = torch.empty(rows * cols // 32 * 17, dtype=torch.uint8, device=device)
+        self.device = buf.device
         self._codes = self._scales = None
         self._valid = True
 
@@ -170,13 +179,17 @@ def _operand(t, name: str) -> torch.device:
     return dev
 
 
-def _rows_of(x: torch.Tensor) -> torch.Tensor:
-    """x [rows, cols] as the calls take it: contiguous 16-byte rows at any stride
-    of whole 16 bytes; copied where it is not."""
-    if x.stride(1) == 1 and not (x.stride(0) * x.element_size() | x.data_ptr()) % 16 and x.stride(0) >= x.shape[1]:
-        return x
+def _rows_of(x: torch.Tensor, cols: int):
+    """(x, address, stride) of x [rows, cols] as the calls take it: contiguous rows
+    at any stride of whole 16 bytes; copied where it is not."""
+    ptr = x.data_ptr()
+    ld, inner = x.stride()
+    if inner == 1 and not (ld * x.element_size() | ptr) & 15 and ld >= cols:
+        return x, ptr, ld
     x = x.contiguous()
-    return x if x.data_ptr() % 16 == 0 else x.clone()
+    if x.data_ptr() & 15:
+        x = x.clone()
+    return x, x.data_ptr(), max(x.stride(0), cols)
 
 
 def _same(dev: torch.device, want: torch.device, name: str):
@@ -185,8 +198,7 @@ def _same(dev: torch.device, want: torch.device, name: str):
 
 
 def _packed_out(out, rows: int, cols: int, device) -> MxTensor:
-    if out is None:
-        return MxTensor(rows, cols, device)
+    """A caller's output, which has to fit."""
     _same(_operand(out, "out"), device, "out")
     if out.shape != (rows, cols):
         raise ValueError(f"out is {out.rows}x{out.cols}, expected {rows}x{cols}")
@@ -195,15 +207,18 @@ def _packed_out(out, rows: int, cols: int, device) -> MxTensor:
 
 def _encode(call, x, parts: int, out, stream) -> MxTensor:
     dev = _on_gpu(x, "x")
+    dt = _dtype(x.dtype)
     if x.dim() != 2:
         raise ValueError("expected a 2-D tensor")
-    dt = _dtype(x.dtype)
-    rows, cols = x.shape
-    if cols % (parts * MX_BLOCK):
+    rows, width = x.shape
+    cols = width // parts
+    if width % parts or cols % MX_BLOCK:
         raise ValueError(f"columns must be a multiple of {parts * MX_BLOCK}")
-    out = _packed_out(out, rows, cols // parts, dev)
-    x = _rows_of(x)
-    _check(call(x.data_ptr(), dt, x.stride(0), out.struct(), _stream(stream, dev)), call.__name__)
+    out = MxTensor(rows, cols, dev) if out is None else _packed_out(out, rows, cols, dev)
+    x, ptr, ld = _rows_of(x, width)
+    st = call(ptr, dt, ld, out.struct(), _stream(stream, dev))
+    if st:
+        _check(st, call.__name__)
     return out
 
 
@@ -221,11 +236,13 @@ def razer_mx_dequant(t: MxTensor, dtype: torch.dtype = torch.float32, out=None, 
     """The values of t [rows, cols] (exact in f32, rounded once to f16 / bf16)."""
     dev = _operand(t, "t")
     if out is None:
-        out = torch.empty((t.rows, t.cols), dtype=dtype, device=dev)
+        out = torch.empty(t.rows, t.cols, dtype=dtype, device=dev)
     else:
         _check_buffer(out, (t.rows, t.cols), dev, "out")
-    _check(lib().razer_mx_dequant(t.struct(), out.data_ptr(), _dtype(out.dtype), _stream(stream, dev)),
-           "razer_mx_dequant")
+        dtype = out.dtype
+    st = lib().razer_mx_dequant(t.struct(), out.data_ptr(), _dtype(dtype), _stream(stream, dev))
+    if st:
+        _check(st, "razer_mx_dequant")
     return out
 
 
@@ -235,7 +252,7 @@ def razer_mx_workspace_bytes(m: int, n: int, k: int, experts: int = 0) -> int:
 
 def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+        out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _check_buffer(out, (m, n), dev, "out")
     if workspace is None:
@@ -293,6 +310,13 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
     return out
 
 
+def _vector(t, cols: int, dtype, device, name: str) -> int:
+    """Address of a weight [cols]."""
+    if not isinstance(t, _Tensor) or t.dtype != dtype or t.device != device or t.shape != (cols,) or not t.is_contiguous():
+        _check_buffer(t, (cols,), device, name, dtype)
+    return t.data_ptr()
+
+
 def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=None, post_norm: bool | None = None,
                      gate=None, residual_scale: float = 1.0, pre_weight=None, eps: float = 1e-5,
                      packed: bool = False, h_out=None, x_out=None, stream=None):
@@ -312,43 +336,40 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
         raise ValueError(f"columns must be a multiple of {MX_BLOCK}")
     kind = h.dtype
     dt = _dtype(kind)
-    h = _rows_of(h)
+    h, h_ptr, h_stride = _rows_of(h, cols)
     flags, y_ptr, y_stride, post, pre, gates, gate_rows = 0, None, 0, None, None, None, 0
     if y is not None:
         if _on_gpu(y, "y") != dev or y.shape != shape or y.dtype != kind:
             raise ValueError(f"y must be {rows}x{cols} of {kind} on {dev}")
-        y = _rows_of(y)
-        y_ptr, y_stride = y.data_ptr(), y.stride(0)
+        y, y_ptr, y_stride = _rows_of(y, cols)
         if post_norm if post_norm is not None else post_weight is not None:
             flags = RAZER_NORM_POST
     elif post_weight is not None or gate is not None or post_norm:
         raise ValueError("post_weight, post_norm and gate belong to y")
     if post_weight is not None:
-        _check_buffer(post_weight, (cols,), dev, "post_weight", kind)
-        post = post_weight.data_ptr()
+        post = _vector(post_weight, cols, kind, dev, "post_weight")
     if pre_weight is not None:
-        _check_buffer(pre_weight, (cols,), dev, "pre_weight", kind)
-        pre = pre_weight.data_ptr()
+        pre = _vector(pre_weight, cols, kind, dev, "pre_weight")
     if gate is not None:
         gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
         _check_buffer(gate, (cols,) if gate.dim() == 1 else (gate_rows, cols), dev, "gate", kind)
         gates = gate.data_ptr()
     if h_out is None:
-        h_out = h.new_empty(shape)
+        h_out = torch.empty(rows, cols, dtype=kind, device=dev)
     else:
         _check_buffer(h_out, shape, dev, "h_out", kind)
     x_ptr = p_ptr = None
     if packed:
-        x = _packed_out(x_out, rows, cols, dev)
+        x = MxTensor(rows, cols, dev) if x_out is None else _packed_out(x_out, rows, cols, dev)
         p_ptr = ctypes.pointer(x.struct())
     elif x_out is None:
-        x = h.new_empty(shape)
+        x = torch.empty(rows, cols, dtype=kind, device=dev)
         x_ptr = x.data_ptr()
     else:
         x = x_out
         _check_buffer(x, shape, dev, "x_out", kind)
         x_ptr = x.data_ptr()
-    a = razer_norm(rows, cols, dt, flags, y_ptr, h.data_ptr(), y_stride, h.stride(0), post, pre, gates, gate_rows,
+    a = razer_norm(rows, cols, dt, flags, y_ptr, h_ptr, y_stride, h_stride, post, pre, gates, gate_rows,
                    residual_scale, eps, h_out.data_ptr(), x_ptr, p_ptr)
     _check(lib().razer_block_norm(a, _stream(stream, dev)), "razer_block_norm")
     return h_out, x
