@@ -13,6 +13,7 @@
 // stored).  Blocks past K are read from the last block and get scale byte 0 on
 // both sides: every FP4 code is finite, so they add at most 36 * 2^-254 = 0.
 #include <type_traits>
+#include <utility>
 
 #include "rz_mx.h"
 #include "rz_mx_launch.h"
@@ -500,60 +501,119 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 }
 
 // ---- stream kernel -------------------------------------------------------------
-// For few rows of X the product is a read of W.  A workgroup owns 16 W rows at a
-// time (a "row tile") and all of K; each of its up to eight waves takes U units
-// of 512 elements of K and keeps its share of up to 16 MT rows of X (a "job") in
-// registers for all the row tiles that the workgroup walks through, so that
-// nothing but W is read in the loop.  The row tiles of all jobs stand in one line
-// that is cut evenly between the workgroups, however the rows are spread over the
-// experts; a cut that crosses jobs loads the next one's X on the way.
+// For few rows of X the product is a read of W.  A workgroup of eight waves owns 16
+// W rows at a time (a "row tile", one contiguous piece of memory) and all of K,
+// which the waves share: wave w takes every eighth 128-element slice and keeps its
+// share of up to 16 MT rows of X (a "job") in registers for all the row tiles that
+// the workgroup walks through, so that nothing but W is read in the loop.  The row
+// tiles of all jobs stand in one line that is cut evenly between the workgroups,
+// however the rows are spread over the experts; a cut that crosses jobs loads the
+// next one's X on the way.
 //
-// A unit (16 rows x 256 bytes) is loaded with four instructions that each cover
-// 256 contiguous bytes of four rows, two units ahead of their use (four ahead cost
-// registers, hence waves, and took 5-40 % longer), and turned through a wave's own
-// LDS stage into the operand's layout (chunk c of row r at place c ^ r: no bank
-// conflicts either way).  Group g = lane / 16 takes block 4g + s of a unit at MFMA
-// s, so its scale bytes are one dword.  The scale bytes of a row tile are one
-// contiguous piece of memory; the workgroup loads it a tile ahead and hands it
-// round in LDS.  The waves' partial sums meet in LDS, one barrier a row tile (both
-// areas are double-buffered).
+// A row tile comes in CK chunks of up to 4096 elements of K, 32 KiB each, by
+// direct-to-LDS loads into a ring of RING buffers, RING - 1 chunks ahead: memory is
+// read in long runs whatever K is (pieces of 256 bytes a row, turned through
+// registers, took up to 1.5 times as long where rows do not start on whole lines),
+// and what is under way costs no registers.  A chunk's 16-byte pieces lie in LDS as
+// in memory but for an exchange within a row, piece c of row r at c ^ (r & mask),
+// which spreads the rows over the banks where the row's length would not.
 //
-// Reads past the last W row return zero (the buffer descriptor ends there), so
-// the loop has no branch around a load.
-constexpr int kSRows = 16, kSUnit = 512, kSAhead = 2, kSMaxWaves = 8;
+// Lane group g = lane / 16 takes block 4s + g at slice s.  The scale bytes of a row
+// tile are contiguous too and come the same way (through registers they would have
+// to be waited for, and all chunks under way with them: loads finish in order).
+// The waves' sums meet in LDS.  Loads past the last row return zero (the buffer
+// descriptor ends there), so no load has a branch around it and a chunk's loads
+// have a fixed number.
+constexpr int kSRows = 16, kSWaves = 8, kChunkB = 2048, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, 0, (int)sa, I, (int)sb);
 }
 
-// LDS of a workgroup: a stage a wave, two sets of partial sums, the scale bytes of
-// two row tiles, each from the dword that holds the first.
-constexpr int scale_area(int nb) { return (kSRows * nb + 3 + 4 + 15) & ~15; }
-constexpr size_t stream_lds(int waves, int mt, int nb) {
-  return (size_t)waves * (kSRows * 256 + 2 * 4 * kSRows * 16 * mt) + 2 * scale_area(nb);
+// The chunks of a row: `ck` of them, each `pieces` 16-byte pieces, the last `last`.
+struct StreamPlan {
+  int ck, mt;  // ck = 0: not covered
+  int pieces, last;
+  int mul_pieces, mul_last;  // p / d = p * mul >> 20 for p < 2048
+  int sc_pieces, mul_sc;     // 16-byte pieces of a row's scale bytes, 0 where they are not whole
+};
+
+// f(0), f(1) .. as compile-time constants, until one of them is false.
+template <typename F, int... I> __device__ __forceinline__ bool for_each(F& f, std::integer_sequence<int, I...>) {
+  return (f(std::integral_constant<int, I>{}) && ...);
 }
 
-template <int U, int MT>
-__global__ __launch_bounds__(64 * kSMaxWaves, U * MT == 1 ? 4 : 2) void mx_stream_kernel(Args a, int y_dtype, int waves) {
+// Ring places; blocks of K that a row tile's scale area holds.
+constexpr int stream_ring(int mt) { return mt == 4 ? 3 : 4; }
+constexpr int stream_blocks(int ck) { return ck == 4 ? 480 : 128 * ck; }
+
+template <int CK, int MT>
+__global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int y_dtype, StreamPlan plan) {
+  constexpr int kRing = stream_ring(MT);
   constexpr int kPart = kSRows * 16 * MT;  // fp32 sums of one wave
-  constexpr int kChunks = U / 4 + 1;       // 16-byte chunks of a tile's scale bytes a thread carries: nb + 1 <= 16 U waves + 1
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  constexpr int kOuts = (kPart + 64 * kSWaves - 1) / (64 * kSWaves);  // results of a thread
+  // A round is whole row tiles, whole turns of the ring and at least two tiles.
+  constexpr int kRound = CK == 4 ? 8 : kRing % CK == 0 ? kRing : kRing * CK;
+  constexpr int kAreas = kRound / CK;      // scale areas, one a row tile of the round
+  // Row tiles that the scale bytes are requested ahead: enough that the loads of
+  // kRing - 2 chunks are behind them when they are needed.
+  constexpr int kScAhead = CK == 1 ? kRing - 2 : 1;
+  constexpr int kArea = (kSRows * stream_blocks(CK) + 4 + 15) & ~15;
+  static_assert(kArea <= 1024 * kSWaves && kAreas > kScAhead, "one load a wave");
+  __shared__ __attribute__((aligned(16))) uint8_t r0[kSRows * kChunkB], r1[kSRows * kChunkB], r2[kSRows * kChunkB],
+      r3[kRing > 3 ? kSRows * kChunkB : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t a0[kArea], a1[kArea], a2[kAreas > 2 ? kArea : 16], a3[kAreas > 3 ? kArea : 16];
+  __shared__ __attribute__((aligned(16))) float part[kSWaves * kPart];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
   const int g = lane >> 4, l16 = lane & 15;
-  const int sc_bytes = scale_area(nb);
-  uint8_t* stage = smem + wave * (kSRows * 256);
-  float* part = (float*)(smem + waves * (kSRows * 256));  // [2][waves][kPart]
-  uint8_t* sc = (uint8_t*)(part + 2 * waves * kPart);      // [2][sc_bytes]
-  const int unit0 = wave * U;
   const int tiles = (int)((a.n + kSRows - 1) / kSRows);
+  auto ring = [&](auto p) -> uint8_t* {
+    constexpr int i = decltype(p)::value % kRing;
+    return i == 0 ? r0 : i == 1 ? r1 : i == 2 ? r2 : r3;
+  };
+  auto area = [&](auto tile) -> uint8_t* {
+    constexpr int i = decltype(tile)::value % kAreas;
+    return i == 0 ? a0 : i == 1 ? a1 : i == 2 ? a2 : a3;
+  };
+  // exchange of a row's pieces: within aligned groups, at most 16, that divide the row
+  auto key = [](int pieces, int r) { return r & (min(pieces & -pieces, 16) - 1); };
+  auto quotient = [](int p, int mul) { return (int)(((uint32_t)p * (uint32_t)mul) >> 20); };
+  // direct load i of this lane: bytes from the chunk's first one, or past every end
+  uint32_t off[kSLoads], off_last[kSLoads];
+  // its operands: fragment i in a chunk
+  int fo[4], fo_last[4];
+#pragma unroll
+  for (int i = 0; i < kSLoads; i++) {
+    const int p = (i * kSWaves + wave) * 64 + lane;
+    auto offset = [&](int pieces, int mul) {
+      const int r = quotient(p, mul), c = p - r * pieces;
+      return r < kSRows ? (uint32_t)(r * kb + (c ^ key(pieces, r)) * 16) : 0x7FFFFFFFu;
+    };
+    off_last[i] = offset(plan.last, plan.mul_last);
+    off[i] = CK > 1 ? offset(plan.pieces, plan.mul_pieces) : off_last[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int c = 4 * (8 * i + wave) + g;
+    auto offset = [&](int pieces) {  // past the row: some other codes
+      return min(l16 * pieces + (c ^ key(pieces, l16)), kSRows * kChunkB / 16 - 1) * 16;
+    };
+    fo_last[i] = offset(plan.last);
+    fo[i] = CK > 1 ? offset(plan.pieces) : fo_last[i];
+  }
+  // the scale bytes' pieces are exchanged likewise, by their place in the area
+  auto sc_place = [&](int piece) {
+    return plan.sc_pieces ? piece ^ key(plan.sc_pieces, quotient(piece, plan.mul_sc)) : piece;
+  };
+  const uint32_t sc_from = (uint32_t)sc_place(tid) * 16;
 
   // this workgroup's piece of the line
-  const int64_t line = (int64_t)tiles * (a.offsets ? live_tiles(a, 16 * MT) : (a.m + 16 * MT - 1) / (16 * MT));
-  int64_t at = line * blockIdx.x / gridDim.x;
-  int left = (int)(line * (blockIdx.x + 1) / gridDim.x - at);
-  int job = (int)(at / tiles), tile = (int)(at - (int64_t)job * tiles);
-  int buf = 0;
+  const uint32_t line = (uint32_t)tiles * (uint32_t)(a.offsets ? live_tiles(a, 16 * MT) : (int)((a.m + 16 * MT - 1) / (16 * MT)));
+  const uint32_t share = line / gridDim.x, extra = line % gridDim.x;
+  const uint32_t start = share * blockIdx.x + min(blockIdx.x, extra);
+  int left = (int)(share + (blockIdx.x < extra ? 1 : 0));
+  int job = (int)(start / (uint32_t)tiles), tile = (int)(start - (uint32_t)job * (uint32_t)tiles);
   for (; left > 0; job++, tile = 0) {
     const Tile t = find_tile(a, 16 * MT, job);
     if (t.expert < 0) return;
@@ -561,175 +621,175 @@ __global__ __launch_bounds__(64 * kSMaxWaves, U * MT == 1 ? 4 : 2) void mx_strea
     const uint8_t* wsc = a.ws + (int64_t)t.expert * a.n * nb;
     const int end = min(tile + left, tiles);
     left -= end - tile;
-
-    // W units: slot i of a round is unit i % U of row tile i / U of the round
-    constexpr int kRound = U > kSAhead ? U : kSAhead, kTilesRound = kRound / U;
-    u32x4_t fw[kSAhead][4];
-    int voff[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) voff[i] = (4 * i + g) * kb + l16 * 16;
     auto rows_of = [&](int tile) { return tile < end ? min((int)a.n - tile * kSRows, kSRows) : 0; };
-    auto load_unit = [&](int tile, int u, u32x4_t (&v)[4]) {
-      const int col = (unit0 + u) * 256;
+    auto load_chunk = [&](int tile, int ck, uint8_t* l) {
+      const int col = ck * plan.pieces * 16;
       const Rsrc r = rsrc_of(wc + (int64_t)tile * kSRows * kb + col, max(rows_of(tile) * kb - col, 0));
 #pragma unroll
-      for (int i = 0; i < 4; i++) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 0);
+      for (int i = 0; i < kSLoads; i++)
+        load_lds16(r, ck == CK - 1 ? off_last[i] : off[i], l + (i * kSWaves + wave) * 1024);
     };
     // A row tile's scale bytes, in whole dwords: up to three bytes on either side
-    // are not its own and not looked at.  Thread i carries 16 bytes of every
-    // 16 * (threads); dwords that hold none of the tile's bytes read zero.
-    struct Scales {
-      u32x4_t v[kChunks];
-    };
-    auto skew_of = [&](int tile) { return (int)((uintptr_t)(wsc + (int64_t)tile * kSRows * nb) & 3); };
-    auto load_scales = [&](int tile) {
-      const int rows = rows_of(tile), skew = skew_of(tile);
+    // are not its own and not looked at.  Wave i takes bytes 1024 i on; dwords that
+    // hold none of the tile's bytes read zero.
+    const int skew = (int)((uintptr_t)wsc & 3);  // of every row tile: 16 rows are whole dwords
+    auto load_scales = [&](int tile, uint8_t* l) {
+      const int rows = rows_of(tile);
       const Rsrc r = rsrc_of(wsc + (int64_t)tile * kSRows * nb - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
-      Scales s;
-#pragma unroll
-      for (int i = 0; i < kChunks; i++)
-        s.v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (i * 64 * waves + tid) * 16, 0, 0);
-      return s;
+      if (tid * 16 < kArea) load_lds16(r, sc_from, l + wave * 1024);
     };
-    auto keep_scales = [&](const Scales& s, int buf) {
+    int so[CK][4];  // this lane's scale bytes in the area
 #pragma unroll
-      for (int i = 0; i < kChunks; i++) {
-        const int at = (i * 64 * waves + tid) * 16;
-        if (at < sc_bytes) *(u32x4_t*)(sc + buf * sc_bytes + at) = s.v[i];
+    for (int u = 0; u < CK; u++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int at = skew + l16 * nb + min(u * plan.pieces + 4 * (8 * i + wave) + g, nb - 1);
+        so[u][i] = sc_place(at >> 4) * 16 + (at & 15);
       }
-    };
-    const Scales first_sc = load_scales(tile);
-#pragma unroll
-    for (int i = 0; i < kSAhead; i++) load_unit(tile + i / U, i % U, fw[i]);
 
-    // this wave's share of X
-    u32x4_t fx[MT][U][4];
-    uint32_t dx[MT][U];
+    __syncthreads();  // the job before still reads the ring
+    load_scales(tile, a0);
+    load_chunk(tile, 0, r0);
+    // this wave's share of X: slices 8 i + wave of every chunk
+    u32x4_t fx[MT][CK][4];
+    uint32_t dx[MT][CK];
 #pragma unroll
     for (int j = 0; j < MT; j++) {
       int64_t row = min(t.m0 + 16 * j + l16, t.m1 - 1);
       if (a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
       const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int b = (unit0 + u) * 16 + 4 * g;
+      for (int u = 0; u < CK; u++) {
+        uint32_t byte[4];
 #pragma unroll
-        for (int s = 0; s < 4; s++) fx[j][u][s] = *(const u32x4_t*)(pc + min(b + s, nb - 1) * 16);
-        dx[j][u] = scales4(ps, b, nb);
+        for (int i = 0; i < 4; i++) {
+          const int b = min(u * plan.pieces + 4 * (8 * i + wave) + g, nb - 1);
+          fx[j][u][i] = *(const u32x4_t*)(pc + b * 16);
+          byte[i] = ps[b];
+        }
+        dx[j][u] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++)  // past the chunk: scale 0
+          dx[j][u] |= 4 * (8 * i + wave) + g < (u == CK - 1 ? plan.last : plan.pieces) ? byte[i] << (8 * i) : 0u;
+        __builtin_amdgcn_sched_barrier(0);  // the addresses of one chunk at a time
       }
     }
-    keep_scales(first_sc, buf);
-    __syncthreads();
+    // this thread's results: rows that padding leaves zero
+    bool none[kOuts];
+#pragma unroll
+    for (int i = 0; i < kOuts; i++) {
+      none[i] = false;
+      const int64_t row = t.m0 + ((tid + i * 64 * kSWaves) >> 4);
+      if (a.x_rows && row < t.m1) {
+        const int64_t r = a.x_rows[row];
+        none[i] = r < 0 || r >= a.x_rows_total;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // X first: it is here long before the chunks
+    if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
+    load_chunk(tile + 1 / CK, 1 % CK, r1);
+    if constexpr (kRing > 3) load_chunk(tile + 2 / CK, 2 % CK, r2);
 
-    // row tile RT of a round; false behind the last one
-    auto row_tile = [&](auto which) {
-      constexpr int rt = decltype(which)::value;
-      const Scales next_sc = load_scales(tile + 1);
-      const int skew = skew_of(tile);
-      f32x4_t acc[MT];
+    f32x4_t acc[MT];
+    // position P of a round: chunk P % CK of the row tile, ring place P % kRing;
+    // false behind the last row tile
+    auto chunk = [&](auto which) {
+      constexpr int P = decltype(which)::value, ck = P % CK, ahead = ck + kRing - 1;
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kSLoads*(kRing - 2)) : "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if constexpr (ck == 0) {
+        load_scales(tile + kScAhead, area(std::integral_constant<int, P / CK + kScAhead>{}));
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < MT; j++) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int u = 0; u < U; u++) {
-        constexpr int kA = kSAhead;
-        const int slot = (rt * U + u) % kA;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          *(u32x4_t*)(stage + (4 * i + g) * 256 + ((l16 ^ (4 * i + g)) * 16)) = fw[slot][i];
-        const int ahead = u + kA;  // the unit that takes this slot
-        load_unit(tile + ahead / U, ahead % U, fw[slot]);
-        // scale bytes of blocks b .. b + 3 of row l16, 0 past K
-        const int b = (unit0 + u) * 16 + 4 * g, at = skew + l16 * nb + b;
-        const uint32_t* q = (const uint32_t*)(sc + buf * sc_bytes) + (min(at, sc_bytes - 8) >> 2);
-        uint32_t dw = __builtin_amdgcn_alignbyte(q[1], q[0], (uint32_t)at & 3u);
-        const int have = nb - b;
-        dw = have >= 4 ? dw : have <= 0 ? 0u : dw & ((1u << (8 * have)) - 1u);
-        wave_lds_sync();
-        u32x4_t f[4];
-#pragma unroll
-        for (int s = 0; s < 4; s++) f[s] = *(const u32x4_t*)(stage + l16 * 256 + (((4 * g + s) ^ l16) * 16));
-#pragma unroll
-        for (int j = 0; j < MT; j++) {
-          acc[j] = mma16<0>(f[0], fx[j][u][0], acc[j], dw, dx[j][u]);
-          acc[j] = mma16<1>(f[1], fx[j][u][1], acc[j], dw, dx[j][u]);
-          acc[j] = mma16<2>(f[2], fx[j][u][2], acc[j], dw, dx[j][u]);
-          acc[j] = mma16<3>(f[3], fx[j][u][3], acc[j], dw, dx[j][u]);
-        }
-        // the products stay here: moved down, all units' fragments would wait in registers
-#pragma unroll
-        for (int j = 0; j < MT; j++) asm volatile("" : "+v"(acc[j]));
-        wave_lds_sync();
+        for (int j = 0; j < MT; j++) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       }
-      float* mine = part + (buf * waves + wave) * kPart;
+      load_chunk(tile + ahead / CK, ahead % CK, ring(std::integral_constant<int, P + kRing - 1>{}));
+      const uint8_t* l = ring(which);
+      const uint8_t* ds = area(std::integral_constant<int, P / CK>{});
+      const int pieces = ck == CK - 1 ? plan.last : plan.pieces;
+      u32x4_t f[4];
+      uint32_t d[4];
 #pragma unroll
-      for (int j = 0; j < MT; j++) *(f32x4_t*)(mine + j * 256 + lane * 4) = acc[j];
-      keep_scales(next_sc, buf ^ 1);
-      __syncthreads();
-      for (int o = tid; o < kPart; o += 64 * waves) {
-        const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
-        const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
-        if (row >= t.m1 || col >= a.n) continue;
-        const float* p = part + buf * waves * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
-        float v[kSMaxWaves];  // all read at once
+      for (int i = 0; i < 4; i++) f[i] = *(const u32x4_t*)(l + (ck == CK - 1 ? fo_last[i] : fo[i]));
 #pragma unroll
-        for (int w = 0; w < kSMaxWaves; w++) v[w] = p[min(w, waves - 1) * kPart];
-        float sum = v[0];
+      for (int i = 0; i < 4; i++) d[i] = ds[so[ck][i]];
 #pragma unroll
-        for (int w = 1; w < kSMaxWaves; w++) sum += w < waves ? v[w] : 0.0f;
-        if (a.x_rows) {
-          const int64_t r = a.x_rows[row];
-          if (r < 0 || r >= a.x_rows_total) sum = 0.0f;
-        }
-        const int64_t at = row * a.n + col;
-        if (y_dtype == kF32) ((float*)a.y)[at] = sum;
-        else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(sum);
-        else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(sum);
+      for (int i = 0; i < 4; i++) d[i] = 4 * (8 * i + wave) + g < pieces ? d[i] : 0u;  // past the row: scale 0
+#pragma unroll
+      for (int j = 0; j < MT; j++) {
+        acc[j] = mma16<0>(f[0], fx[j][ck][0], acc[j], d[0], dx[j][ck]);
+        acc[j] = mma16<1>(f[1], fx[j][ck][1], acc[j], d[1], dx[j][ck]);
+        acc[j] = mma16<2>(f[2], fx[j][ck][2], acc[j], d[2], dx[j][ck]);
+        acc[j] = mma16<3>(f[3], fx[j][ck][3], acc[j], d[3], dx[j][ck]);
+        asm volatile("" : "+v"(acc[j]));  // here, not behind the next barrier with all chunks' operands
       }
-      buf ^= 1;
-      return ++tile < end;
+      if constexpr (ck == CK - 1) {
+#pragma unroll
+        for (int j = 0; j < MT; j++) *(f32x4_t*)(part + wave * kPart + j * 256 + lane * 4) = acc[j];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < kOuts; i++) {
+          const int o = tid + i * 64 * kSWaves;
+          const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
+          const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
+          if (o >= kPart || row >= t.m1 || col >= a.n) continue;
+          const float* p = part + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+          float v[kSWaves];
+#pragma unroll
+          for (int w = 0; w < kSWaves; w++) v[w] = p[w * kPart];
+          float sum = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kSWaves; w++) sum += v[w];
+          if (none[i]) sum = 0.0f;
+          const int64_t at = row * a.n + col;
+          if (y_dtype == kF32) ((float*)a.y)[at] = sum;
+          else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(sum);
+          else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(sum);
+        }
+        return ++tile < end;
+      }
+      return true;
     };
-    while (row_tile(std::integral_constant<int, 0>{})) {
-      if constexpr (kTilesRound > 1)
-        if (!row_tile(std::integral_constant<int, 1>{})) break;
+    while (for_each(chunk, std::make_integer_sequence<int, kRound>{})) {
     }
   }
 }
 
-// The stream kernel's shape for a product: U units a wave, waves, MT.
-struct StreamPlan {
-  int u, waves, mt;  // u = 0: not covered
-};
+// The stream kernel's shape for jobs of about `rows` rows.
 StreamPlan stream_plan(int64_t rows, int64_t k) {
-  const int64_t units = (k + kSUnit - 1) / kSUnit;
-  const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  int u = 1;
-  while ((int64_t)u * kSMaxWaves < units) u *= 2;
-  if (u * mt > 8) return {0, 0, 0};  // X would not fit the registers
-  return {u, (int)((units + u - 1) / u), mt};
+  StreamPlan p = {};
+  const int64_t kb = k / 2;
+  p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  int ck = 1;
+  while ((int64_t)ck * kChunkB < kb) ck *= 2;
+  // X would not fit the registers, or the scale bytes LDS
+  if (ck > 4 || ck * p.mt > 8 || kb / 16 > stream_blocks(ck)) return p;
+  p.ck = ck;
+  p.pieces = (int)(((kb + ck - 1) / ck + 63) / 64 * 4);  // whole slices
+  p.last = (int)(kb / 16) - p.pieces * (ck - 1);
+  p.mul_pieces = (1 << 20) / p.pieces + 1;
+  p.mul_last = (1 << 20) / p.last + 1;
+  const int nb = (int)(kb / 16);
+  if (nb % 16 == 0) p.sc_pieces = nb / 16, p.mul_sc = (1 << 20) / p.sc_pieces + 1;
+  return p;
 }
 
-template <int U, int MT> hipError_t go_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t stream) {
-  const size_t lds = stream_lds(p.waves, MT, (int)(a.k / kMxBlock));
+template <int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t stream) {
   const int64_t tiles = (a.n + kSRows - 1) / kSRows, rows = 16 * MT;
   const int64_t jobs = a.offsets ? min((a.m + rows - 1) / rows + a.experts, a.m) : (a.m + rows - 1) / rows;
-  // as many workgroups as are resident: by registers (16 or 8 waves a CU) and LDS
-  const int per_cu = max(1, min((U * MT == 1 ? 16 : 8) / p.waves, (int)(160 * 1024 / lds)));
-  const int64_t grid = min(tiles * jobs, (int64_t)device_cu_count() * per_cu);
-  auto kern = mx_stream_kernel<U, MT>;
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * p.waves), lds, stream, a, y_dtype, p.waves);
+  const int64_t grid = min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
+  hipLaunchKernelGGL((mx_stream_kernel<CK, MT>), dim3((unsigned)grid), dim3(64 * kSWaves), 0, stream, a, y_dtype, p);
   return hipGetLastError();
 }
 
 hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t s) {
-  switch (p.mt * 16 + p.u) {
+  switch (p.mt * 16 + p.ck) {
     case 17: return go_stream<1, 1>(a, y_dtype, p, s);
     case 18: return go_stream<2, 1>(a, y_dtype, p, s);
     case 20: return go_stream<4, 1>(a, y_dtype, p, s);
-    case 24: return go_stream<8, 1>(a, y_dtype, p, s);
     case 33: return go_stream<1, 2>(a, y_dtype, p, s);
     case 34: return go_stream<2, 2>(a, y_dtype, p, s);
     case 36: return go_stream<4, 2>(a, y_dtype, p, s);
@@ -825,7 +885,7 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 bool streams(int64_t m, int64_t k, int64_t experts, StreamPlan& p) {
   const int64_t rows = experts ? (m + experts - 1) / experts : m;
   p = stream_plan(experts ? rows + rows / 2 : rows, k);
-  return p.u && (rows <= 64 || k < kWindow * kMxBlock);
+  return p.ck && (rows <= 64 || k < kWindow * kMxBlock);
 }
 
 }  // namespace
