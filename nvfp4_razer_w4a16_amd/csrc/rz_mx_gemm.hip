@@ -503,9 +503,9 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // ---- stream kernel -------------------------------------------------------------
 // For few rows of X the product is a read of W.  A workgroup of eight waves owns 16
 // W rows at a time (a "row tile", one contiguous piece of memory) and all of K,
-// which the waves share: wave w takes every eighth 128-element slice and keeps its
-// share of up to 16 MT rows of X (a "job") in registers for all the row tiles that
-// the workgroup walks through, so that nothing but W is read in the loop.  The row
+// which the waves share: wave w takes 512 elements of each 4096 and keeps its share of
+// up to 16 MT rows of X (a "job") in registers for all the row tiles that the
+// workgroup walks through, so that nothing but W is read in the loop.  The row
 // tiles of all jobs stand in one line that is cut evenly between the workgroups,
 // however the rows are spread over the experts; a cut that crosses jobs loads the
 // next one's X on the way.
@@ -518,7 +518,11 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // in memory but for an exchange within a row, piece c of row r at c ^ (r & mask),
 // which spreads the rows over the banks where the row's length would not.
 //
-// Lane group g = lane / 16 takes block 4s + g at slice s.  The scale bytes of a row
+// Of a wave's sixteen blocks, lane group g = lane / 16 takes the four from 4 g on, one
+// a product: K is summed in another order, the same for both operands.  So a lane's
+// four pieces of a row are 64 bytes in one run and its four scale bytes one dword.
+// (With block 4 s + g at product s they were four bytes in four places, and 27 rows of
+// 8192 took 32.0 us, 64 rows 40, against 28.9 and 34.4.)  The scale bytes of a row
 // tile are contiguous too and come the same way (through registers they would have
 // to be waited for, and all chunks under way with them: loads finish in order).
 // The waves' sums meet in LDS.  Loads past the last row return zero (the buffer
@@ -527,7 +531,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 constexpr int kSRows = 16, kSWaves = 8, kChunkB = 2048, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, 0, (int)sa, I, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
 }
 
 // The chunks of a row: `ck` of them, each `pieces` 16-byte pieces, the last `last`.
@@ -563,7 +567,11 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   __shared__ __attribute__((aligned(16))) uint8_t r0[kSRows * kChunkB], r1[kSRows * kChunkB], r2[kSRows * kChunkB],
       r3[kRing > 3 ? kSRows * kChunkB : 16];
   __shared__ __attribute__((aligned(16))) uint8_t a0[kArea], a1[kArea], a2[kAreas > 2 ? kArea : 16], a3[kAreas > 3 ? kArea : 16];
-  __shared__ __attribute__((aligned(16))) float part[kSWaves * kPart];
+  // The waves' sums of a row tile are added behind the next chunk's barrier, where
+  // the place to keep them until then is not needed again or there is a second one.
+  constexpr bool kDefer = CK > 1 || MT == 1;
+  constexpr int kParts = CK == 1 && MT == 1 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) float part[kParts * kSWaves * kPart];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
   const int g = lane >> 4, l16 = lane & 15;
@@ -578,6 +586,10 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   };
   // exchange of a row's pieces: within aligned groups, at most 16, that divide the row
   auto key = [](int pieces, int r) { return r & (min(pieces & -pieces, 16) - 1); };
+  const int mine = 16 * wave + 4 * g;  // this lane's first of four blocks in a chunk
+  // of its blocks' scale bytes, those that the chunk has: past the row, scale 0
+  auto kept = [&](int pieces) { return mine + 4 <= pieces ? ~0u : mine >= pieces ? 0u : ~(~0u << 8 * (pieces - mine)); };
+  const uint32_t keep_last = kept(plan.last), keep = CK > 1 ? kept(plan.pieces) : keep_last;
   auto quotient = [](int p, int mul) { return (int)(((uint32_t)p * (uint32_t)mul) >> 20); };
   // direct load i of this lane: bytes from the chunk's first one, or past every end
   uint32_t off[kSLoads], off_last[kSLoads];
@@ -595,7 +607,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   }
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int c = 4 * (8 * i + wave) + g;
+    const int c = mine + i;
     auto offset = [&](int pieces) {  // past the row: some other codes
       return min(l16 * pieces + (c ^ key(pieces, l16)), kSRows * kChunkB / 16 - 1) * 16;
     };
@@ -638,19 +650,21 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       const Rsrc r = rsrc_of(wsc + (int64_t)tile * kSRows * nb - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
       if (tid * 16 < kArea) load_lds16(r, sc_from, l + wave * 1024);
     };
-    int so[CK][4];  // this lane's scale bytes in the area
+    // this lane's four scale bytes in the area: the two dwords that hold them
+    const int sc_shift = (skew + l16 * nb) & 3;
+    int so[CK][2];
 #pragma unroll
     for (int u = 0; u < CK; u++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int at = skew + l16 * nb + min(u * plan.pieces + 4 * (8 * i + wave) + g, nb - 1);
+      for (int i = 0; i < 2; i++) {
+        const int at = min(((skew + l16 * nb + u * plan.pieces + mine) & ~3) + 4 * i, kArea - 4);
         so[u][i] = sc_place(at >> 4) * 16 + (at & 15);
       }
 
     __syncthreads();  // the job before still reads the ring
     load_scales(tile, a0);
     load_chunk(tile, 0, r0);
-    // this wave's share of X: slices 8 i + wave of every chunk
+    // this wave's share of X
     u32x4_t fx[MT][CK][4];
     uint32_t dx[MT][CK];
 #pragma unroll
@@ -660,20 +674,21 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
 #pragma unroll
       for (int u = 0; u < CK; u++) {
-        uint32_t byte[4];
+        const int b = u * plan.pieces + mine;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int b = min(u * plan.pieces + 4 * (8 * i + wave) + g, nb - 1);
-          fx[j][u][i] = *(const u32x4_t*)(pc + b * 16);
-          byte[i] = ps[b];
-        }
-        dx[j][u] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++)  // past the chunk: scale 0
-          dx[j][u] |= 4 * (8 * i + wave) + g < (u == CK - 1 ? plan.last : plan.pieces) ? byte[i] << (8 * i) : 0u;
-        __builtin_amdgcn_sched_barrier(0);  // the addresses of one chunk at a time
+        for (int i = 0; i < 4; i++) fx[j][u][i] = *(const u32x4_t*)(pc + min(b + i, nb - 1) * 16);
+        dx[j][u] = scales4(ps, b, nb);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
+    load_chunk(tile + 1 / CK, 1 % CK, r1);
+    if constexpr (kRing > 3) load_chunk(tile + 2 / CK, 2 % CK, r2);
+#pragma unroll
+    for (int j = 0; j < MT; j++)
+#pragma unroll
+      for (int u = 0; u < CK; u++) dx[j][u] &= u == CK - 1 ? keep_last : keep;
+
     // this thread's results: rows that padding leaves zero
     bool none[kOuts];
 #pragma unroll
@@ -685,12 +700,35 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
         none[i] = r < 0 || r >= a.x_rows_total;
       }
     }
-    __builtin_amdgcn_sched_barrier(0);  // X first: it is here long before the chunks
-    if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
-    load_chunk(tile + 1 / CK, 1 % CK, r1);
-    if constexpr (kRing > 3) load_chunk(tile + 2 / CK, 2 % CK, r2);
-
+    // y of a row tile, from set `set` of the waves' sums
+    auto finish = [&](int tile, int set) {
+#pragma unroll
+      for (int i = 0; i < kOuts; i++) {
+        const int o = tid + i * 64 * kSWaves;
+        const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
+        const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
+        if (o >= kPart || row >= t.m1 || col >= a.n) continue;
+        const float* p = part + set * kSWaves * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+        float v[kSWaves];
+#pragma unroll
+        for (int w = 0; w < kSWaves; w++) v[w] = p[w * kPart];
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSWaves; w++) sum += v[w];
+        if (none[i]) sum = 0.0f;
+        const int64_t at = row * a.n + col;
+        if (y_dtype == kF32) ((float*)a.y)[at] = sum;
+        else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(sum);
+        else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(sum);
+      }
+    };
+    auto meet = [&]() {  // once this wave's LDS accesses are done
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
     f32x4_t acc[MT];
+    const int first = tile;
     // position P of a round: chunk P % CK of the row tile, ring place P % kRing;
     // false behind the last row tile
     auto chunk = [&](auto which) {
@@ -707,53 +745,40 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       load_chunk(tile + ahead / CK, ahead % CK, ring(std::integral_constant<int, P + kRing - 1>{}));
       const uint8_t* l = ring(which);
       const uint8_t* ds = area(std::integral_constant<int, P / CK>{});
-      const int pieces = ck == CK - 1 ? plan.last : plan.pieces;
       u32x4_t f[4];
-      uint32_t d[4];
+      uint32_t d[2];
 #pragma unroll
       for (int i = 0; i < 4; i++) f[i] = *(const u32x4_t*)(l + (ck == CK - 1 ? fo_last[i] : fo[i]));
 #pragma unroll
-      for (int i = 0; i < 4; i++) d[i] = ds[so[ck][i]];
-#pragma unroll
-      for (int i = 0; i < 4; i++) d[i] = 4 * (8 * i + wave) + g < pieces ? d[i] : 0u;  // past the row: scale 0
+      for (int i = 0; i < 2; i++) d[i] = *(const uint32_t*)(ds + so[ck][i]);
+      const uint32_t dw = __builtin_amdgcn_alignbyte(d[1], d[0], sc_shift) & (ck == CK - 1 ? keep_last : keep);
 #pragma unroll
       for (int j = 0; j < MT; j++) {
-        acc[j] = mma16<0>(f[0], fx[j][ck][0], acc[j], d[0], dx[j][ck]);
-        acc[j] = mma16<1>(f[1], fx[j][ck][1], acc[j], d[1], dx[j][ck]);
-        acc[j] = mma16<2>(f[2], fx[j][ck][2], acc[j], d[2], dx[j][ck]);
-        acc[j] = mma16<3>(f[3], fx[j][ck][3], acc[j], d[3], dx[j][ck]);
+        acc[j] = mma16<0>(f[0], fx[j][ck][0], acc[j], dw, dx[j][ck]);
+        acc[j] = mma16<1>(f[1], fx[j][ck][1], acc[j], dw, dx[j][ck]);
+        acc[j] = mma16<2>(f[2], fx[j][ck][2], acc[j], dw, dx[j][ck]);
+        acc[j] = mma16<3>(f[3], fx[j][ck][3], acc[j], dw, dx[j][ck]);
         asm volatile("" : "+v"(acc[j]));  // here, not behind the next barrier with all chunks' operands
       }
+      if constexpr (kDefer && ck == 0)
+        if (tile > first) finish(tile - 1, (P / CK + kParts - 1) % kParts);
       if constexpr (ck == CK - 1) {
+        float* sums = part + (P / CK % kParts * kSWaves + wave) * kPart;
 #pragma unroll
-        for (int j = 0; j < MT; j++) *(f32x4_t*)(part + wave * kPart + j * 256 + lane * 4) = acc[j];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < kOuts; i++) {
-          const int o = tid + i * 64 * kSWaves;
-          const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
-          const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
-          if (o >= kPart || row >= t.m1 || col >= a.n) continue;
-          const float* p = part + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
-          float v[kSWaves];
-#pragma unroll
-          for (int w = 0; w < kSWaves; w++) v[w] = p[w * kPart];
-          float sum = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kSWaves; w++) sum += v[w];
-          if (none[i]) sum = 0.0f;
-          const int64_t at = row * a.n + col;
-          if (y_dtype == kF32) ((float*)a.y)[at] = sum;
-          else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(sum);
-          else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(sum);
+        for (int j = 0; j < MT; j++) *(f32x4_t*)(sums + j * 256 + lane * 4) = acc[j];
+        if constexpr (!kDefer) {
+          meet();
+          finish(tile, 0);
         }
         return ++tile < end;
       }
       return true;
     };
     while (for_each(chunk, std::make_integer_sequence<int, kRound>{})) {
+    }
+    if constexpr (kDefer) {
+      meet();
+      finish(end - 1, (end - 1 - first) % kParts);
     }
   }
 }
