@@ -537,6 +537,7 @@ template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, 
 // The chunks of a row: `ck` of them, each `pieces` 16-byte pieces, the last `last`.
 struct StreamPlan {
   int ck, mt;  // ck = 0: not covered
+  int rows;    // of a job, at most 16 mt
   int pieces, last;
   int mul_pieces, mul_last;  // p / d = p * mul >> 20 for p < 2048
   int sc_pieces, mul_sc;     // 16-byte pieces of a row's scale bytes, 0 where they are not whole
@@ -621,13 +622,13 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   const uint32_t sc_from = (uint32_t)sc_place(tid) * 16;
 
   // this workgroup's piece of the line
-  const uint32_t line = (uint32_t)tiles * (uint32_t)(a.offsets ? live_tiles(a, 16 * MT) : (int)((a.m + 16 * MT - 1) / (16 * MT)));
+  const uint32_t line = (uint32_t)tiles * (uint32_t)(a.offsets ? live_tiles(a, plan.rows) : (int)((a.m + plan.rows - 1) / plan.rows));
   const uint32_t share = line / gridDim.x, extra = line % gridDim.x;
   const uint32_t start = share * blockIdx.x + min(blockIdx.x, extra);
   int left = (int)(share + (blockIdx.x < extra ? 1 : 0));
   int job = (int)(start / (uint32_t)tiles), tile = (int)(start - (uint32_t)job * (uint32_t)tiles);
   for (; left > 0; job++, tile = 0) {
-    const Tile t = find_tile(a, 16 * MT, job);
+    const Tile t = find_tile(a, plan.rows, job);
     if (t.expert < 0) return;
     const uint8_t* wc = a.wc + (int64_t)t.expert * a.n * kb;
     const uint8_t* wsc = a.ws + (int64_t)t.expert * a.n * nb;
@@ -783,17 +784,27 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   }
 }
 
-// The stream kernel's shape for jobs of about `rows` rows.
-StreamPlan stream_plan(int64_t rows, int64_t k) {
+// The stream kernel's shape for `m` rows, of each of `experts` on average if that is not 0.
+StreamPlan stream_plan(int64_t m, int64_t k, int64_t experts) {
   StreamPlan p = {};
   const int64_t kb = k / 2;
-  p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   int ck = 1;
   while ((int64_t)ck * kChunkB < kb) ck *= 2;
-  // X would not fit the registers, or the scale bytes LDS
-  if (ck > 4 || ck * p.mt > 8 || kb / 16 > stream_blocks(ck)) return p;
+  if (ck > 4 || kb / 16 > stream_blocks(ck)) return p;  // the scale bytes would not fit LDS
+  // rows a job: X of CK chunks has to fit the registers; experts' rows scatter about the average
+  const int64_t rows = experts ? (m + experts - 1) / experts * 3 / 2 : m;
+  const int most = min(4, 8 / ck);
+  p.mt = min(rows <= 16 ? 1 : rows <= 32 ? 2 : 4, most);
+  p.rows = 16 * p.mt;
+  if (!experts && m > p.rows) {
+    // A power of two of jobs: workgroups that walk through the same piece of W are then
+    // on one XCD and share its L2 (192 x 28672 x 8192 as three jobs 76 us, as four 61).
+    int64_t jobs = 1;
+    while (jobs < 32 && jobs * p.rows < m) jobs *= 2;
+    if (jobs * p.rows >= m) p.rows = (int)((m + jobs - 1) / jobs);
+  }
   p.ck = ck;
-  p.pieces = (int)(((kb + ck - 1) / ck + 63) / 64 * 4);  // whole slices
+  p.pieces = (int)(((kb + ck - 1) / ck + 63) / 64 * 4);  // whole products' blocks
   p.last = (int)(kb / 16) - p.pieces * (ck - 1);
   p.mul_pieces = (1 << 20) / p.pieces + 1;
   p.mul_last = (1 << 20) / p.last + 1;
@@ -803,8 +814,8 @@ StreamPlan stream_plan(int64_t rows, int64_t k) {
 }
 
 template <int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t stream) {
-  const int64_t tiles = (a.n + kSRows - 1) / kSRows, rows = 16 * MT;
-  const int64_t jobs = a.offsets ? min((a.m + rows - 1) / rows + a.experts, a.m) : (a.m + rows - 1) / rows;
+  const int64_t tiles = (a.n + kSRows - 1) / kSRows, full = (a.m + p.rows - 1) / p.rows;
+  const int64_t jobs = a.offsets ? min(full + a.experts, a.m) : full;
   const int64_t grid = min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
   hipLaunchKernelGGL((mx_stream_kernel<CK, MT>), dim3((unsigned)grid), dim3(64 * kSWaves), 0, stream, a, y_dtype, p);
   return hipGetLastError();
@@ -866,9 +877,16 @@ __global__ __launch_bounds__(256) void mx_fold_kernel(Args a, TilePlan plan) {
 }
 
 // The tiles of a product.  The last, partly filled round of tiles is cut along K
-// where that is quicker: a tile costs about 1.75 us a step and 8 us around them,
-// folding 4 us and its sums at 7 TB/s (out of the Infinity Cache).
+// where that is quicker by the times below.
 constexpr int kTileN = 256, kTileM = 256;
+// us a window of a tile takes, in a full round and in one that leaves CUs (and power)
+// to spare; what slices cost, their sums written and read.  2048 x 28672 x 8192, three
+// and a half rounds: 262 us as it is, 272 with the half round cut in two; 2041 x 4096 x
+// 14336, half a round: 82.7 and 80.2; 128 x 4096 x 14336, 16 tiles: 78 and, in eight, 27.
+constexpr double kFullUs = 3.5, kRestUs = 3.0;
+double fold_us(int slices) { return 4.0 + slices * 0.09; }
+int windows_of(int64_t k) { return (int)((k + kWindow * kMxBlock - 1) / (kWindow * kMxBlock)); }
+
 TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
   TilePlan p = {};
   const int cus = device_cu_count();
@@ -877,10 +895,10 @@ TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
   p.full = p.mt * p.nt;
   p.split = 1;
   if (experts) return p;
-  const int rest = p.full % cus, windows = (int)((k + kWindow * kMxBlock - 1) / (kWindow * kMxBlock));
-  double best = windows * 3.5;
+  const int rest = p.full % cus, windows = windows_of(k);
+  double best = windows * kRestUs;
   for (int s = 2; s <= 8 && rest > 0 && rest * s <= cus && s <= windows; s++) {
-    const double t = (windows + s - 1) / s * 3.5 + 4.0 + rest * s * (kTileN * kTileM * 4 / 7e6);
+    const double t = (windows + s - 1) / s * kRestUs + fold_us(rest * s);
     if (t < best) best = t, p.split = s;
   }
   if (p.split > 1) p.rest = rest, p.full -= rest;
@@ -905,19 +923,39 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
   return e;
 }
 
-// Whether a product runs on the stream kernel: few rows of one product (of one
-// expert, on average), or K below a window of the tile kernel.
-bool streams(int64_t m, int64_t k, int64_t experts, StreamPlan& p) {
-  const int64_t rows = experts ? (m + experts - 1) / experts : m;
-  p = stream_plan(experts ? rows + rows / 2 : rows, k);
-  return p.ck && (rows <= 64 || k < kWindow * kMxBlock);
+// Whether a product runs on the stream kernel: K below a window of the tile kernel, or
+// the shorter time of two estimates, in us.  Both take what the kernel's own work and
+// the read of W come to, one of them half hidden behind the other, and what a launch
+// costs.  The stream kernel's work is its row tiles, whose sums meet in LDS; the tile
+// kernel's its rounds of tiles.  Measured, stream and tile kernel:
+//   64 x 28672 x 8192   34.4 and 51.5    256 x 28672 x 8192   61.1 and 60.7
+//   256 x 14336 x 4096  26.8 and 28.2    512 x 14336 x 4096   44.9 and 29.9
+//   256 x 8192 x 1024   17.4 and 12.2    512 x 1024 x 1024     9.8 and 11.8
+//   128 x 4096 x 14336  20.6 and 27.1    1024 x 4096 x 14336  67.7 and 52.9
+//   8 experts of 14336 x 4096, 64 rows each 73.7 and 78.3, 128 rows 115 and 85
+bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
+  p = stream_plan(m, k, experts);
+  if (!p.ck) return false;
+  const int windows = windows_of(k), cus = device_cu_count();
+  if (k < kWindow * kMxBlock) return true;
+  const int64_t parts = experts ? min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
+  const double read = parts * n * (k / 2 + k / 32) / 5e6;
+  auto rounds = [&](int64_t units) { return (double)((units + cus - 1) / cus); };
+  auto total = [&](double work, double fixed) { return max(work, read) + min(work, read) / 2 + fixed; };
+  const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows - 1) / kSRows)) *
+                        (0.25 * p.mt + 0.3 * p.ck);
+  const TilePlan t = tile_plan(m, n, k, experts);
+  const int64_t whole = experts ? parts * ((rows + kTileM - 1) / kTileM) * t.nt : t.full;
+  double tile = (whole / cus * kFullUs + (whole % cus ? kRestUs : 0.0)) * windows;
+  if (t.rest) tile += (windows + t.split - 1) / t.split * kRestUs + fold_us(t.rest * t.split);
+  return total(stream, 4.0) <= total(tile, 5.0);
 }
 
 }  // namespace
 
 size_t mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
   StreamPlan p;
-  return streams(m, k, experts, p) ? 0 : tile_ws_bytes(tile_plan(m, n, k, experts));
+  return streams(m, n, k, experts, p) ? 0 : tile_ws_bytes(tile_plan(m, n, k, experts));
 }
 
 hipError_t launch_mx_gemm(const MxGemm& g, void* ws, size_t, hipStream_t stream) {
@@ -925,7 +963,7 @@ hipError_t launch_mx_gemm(const MxGemm& g, void* ws, size_t, hipStream_t stream)
   const Args a = {g.x.codes, g.x.scales, g.w.codes, g.w.scales, g.m, g.n, g.k, g.x.rows, g.y, g.offsets, g.x_rows,
                   g.experts};
   StreamPlan p;
-  if (streams(g.m, g.k, g.offsets ? g.experts : 0, p)) return run_stream(a, g.y_dtype, p, stream);
+  if (streams(g.m, g.n, g.k, g.offsets ? g.experts : 0, p)) return run_stream(a, g.y_dtype, p, stream);
   if (g.y_dtype == kF32) return run<float>(a, ws, stream);
   if (g.y_dtype == kF16) return run<_Float16>(a, ws, stream);
   return run<__bf16>(a, ws, stream);
