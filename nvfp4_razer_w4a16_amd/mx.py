@@ -8,6 +8,8 @@ scale byte each.  Both operands of a product are MxTensors::
     gu   = razer_mx_gemm(x, gate_up)                  # [M, 2 * I]
     y    = razer_mx_gemm(razer_mx_quantize_gated(gu), down)
 
+Calls run on the current stream; with ``stream`` they run as inside
+``torch.cuda.stream(stream)``, and what they return belongs to that stream.
 The package re-exports every name here.
 """
 from __future__ import annotations
@@ -63,15 +65,22 @@ def _check(status: int, what: str):
         raise RazerError(status, what)
 
 
-def _stream(stream, device: torch.device) -> int:
-    """The caller's stream, or the current one of the tensors' device, which has
-    to be the current device: launches go to that one."""
+def _stream(device: torch.device) -> int:
+    """The current stream of the tensors' device, which has to be the current
+    device: launches go to that one."""
     index = device.index
     if index != _current_device():
         raise ValueError(f"tensors are on {device}, the current device is cuda:{_current_device()}")
-    if stream is None:
-        return _raw_stream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return _raw_stream(index)
+
+
+def _entered(stream):
+    """`stream` (a torch stream or a handle) as the current one: what a call
+    allocates or copies on the way is then ordered with its launch."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _dtype(dt: torch.dtype) -> int:
@@ -206,6 +215,9 @@ def _packed_out(out, rows: int, cols: int, device) -> MxTensor:
 
 
 def _encode(call, x, parts: int, out, stream) -> MxTensor:
+    if stream is not None:
+        with _entered(stream):
+            return _encode(call, x, parts, out, None)
     dev = _on_gpu(x, "x")
     dt = _dtype(x.dtype)
     if x.dim() != 2:
@@ -216,7 +228,7 @@ def _encode(call, x, parts: int, out, stream) -> MxTensor:
         raise ValueError(f"columns must be a multiple of {parts * MX_BLOCK}")
     out = MxTensor(rows, cols, dev) if out is None else _packed_out(out, rows, cols, dev)
     x, ptr, ld = _rows_of(x, width)
-    st = call(ptr, dt, ld, out.struct(), _stream(stream, dev))
+    st = call(ptr, dt, ld, out.struct(), _stream(dev))
     if st:
         _check(st, call.__name__)
     return out
@@ -234,13 +246,16 @@ def razer_mx_quantize_gated(gu: torch.Tensor, out: MxTensor | None = None, strea
 
 def razer_mx_dequant(t: MxTensor, dtype: torch.dtype = torch.float32, out=None, stream=None) -> torch.Tensor:
     """The values of t [rows, cols] (exact in f32, rounded once to f16 / bf16)."""
+    if stream is not None:
+        with _entered(stream):
+            return razer_mx_dequant(t, dtype, out)
     dev = _operand(t, "t")
     if out is None:
         out = torch.empty(t.rows, t.cols, dtype=dtype, device=dev)
     else:
         _check_buffer(out, (t.rows, t.cols), dev, "out")
         dtype = out.dtype
-    st = lib().razer_mx_dequant(t.struct(), out.data_ptr(), _dtype(dtype), _stream(stream, dev))
+    st = lib().razer_mx_dequant(t.struct(), out.data_ptr(), _dtype(dtype), _stream(dev))
     if st:
         _check(st, "razer_mx_dequant")
     return out
@@ -268,13 +283,16 @@ def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
 def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
                   stream=None) -> torch.Tensor:
     """y[M, N] = x[M, K] . w[N, K]^T."""
+    if stream is not None:
+        with _entered(stream):
+            return razer_mx_gemm(x, w, out_dtype, out, workspace)
     dev = _operand(x, "x")
     _same(_operand(w, "w"), dev, "w")
     if x.cols != w.cols:
         raise ValueError(f"x has {x.cols} columns, w {w.cols}")
     out, ws, wsb = _product_buffers(x.rows, w.rows, x.cols, 0, dev, out_dtype, out, workspace)
     _check(lib().razer_mx_gemm(x.struct(), w.struct(), out.data_ptr(), _dtype(out.dtype), ws, wsb,
-                               _stream(stream, dev)), "razer_mx_gemm")
+                               _stream(dev)), "razer_mx_gemm")
     return out
 
 
@@ -286,6 +304,9 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
     x[x_rows[r]] . w_e^T (x[r] without x_rows).  offsets (int32 [E + 1]) and
     x_rows (int32 [M]) stay on the GPU.  Rows outside every run are not written;
     a row number outside x makes its row zero."""
+    if stream is not None:
+        with _entered(stream):
+            return razer_mx_gemm_grouped(x, w, offsets, x_rows, out_dtype, out, workspace)
     dev = _operand(x, "x")
     _same(_operand(w, "w"), dev, "w")
     if x.cols != w.cols:
@@ -305,7 +326,7 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
     n = w.rows // experts
     out, ws, wsb = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
     _check(lib().razer_mx_gemm_grouped(x.struct(), w.struct(), offsets.data_ptr(), experts, rows, m,
-                                       out.data_ptr(), _dtype(out.dtype), ws, wsb, _stream(stream, dev)),
+                                       out.data_ptr(), _dtype(out.dtype), ws, wsb, _stream(dev)),
            "razer_mx_gemm_grouped")
     return out
 
@@ -328,6 +349,11 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     [gate_rows, cols], gate_rows a divisor of rows.  packed: x is an MxTensor, else
     a tensor of h's dtype.  h_out (h itself, if contiguous) and x_out take the
     results."""
+    if stream is not None:
+        with _entered(stream):
+            return razer_block_norm(y, h, post_weight=post_weight, post_norm=post_norm, gate=gate,
+                                    residual_scale=residual_scale, pre_weight=pre_weight, eps=eps, packed=packed,
+                                    h_out=h_out, x_out=x_out)
     dev = _on_gpu(h, "h")
     if h.dim() != 2:
         raise ValueError("h must be 2-D")
@@ -371,5 +397,5 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
         x_ptr = x.data_ptr()
     a = razer_norm(rows, cols, dt, flags, y_ptr, h_ptr, y_stride, h_stride, post, pre, gates, gate_rows,
                    residual_scale, eps, h_out.data_ptr(), x_ptr, p_ptr)
-    _check(lib().razer_block_norm(a, _stream(stream, dev)), "razer_block_norm")
+    _check(lib().razer_block_norm(a, _stream(dev)), "razer_block_norm")
     return h_out, x
