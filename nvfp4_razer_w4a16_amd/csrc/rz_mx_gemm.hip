@@ -133,8 +133,8 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
 }
 
 // ---- tile kernel -------------------------------------------------------------
-// A BN x BM tile of y (BN rows of W, BM of X) per workgroup of four waves (2x2),
-// each wave (BN/2) x (BM/2) in 32x32 accumulators, 256 elements of K a step; two
+// A BN x BM tile of y (BN = 256 rows of W, BM = 256 or 128 of X) per workgroup of four
+// waves (2x2), each wave (BN/2) x (BM/2) in 32x32 accumulators, 256 elements of K a step; two
 // steps are a "window", whose scale bytes are 16 bytes a row.  As many workgroups
 // as CUs; each walks through the tiles.
 //
@@ -175,6 +175,7 @@ __device__ __forceinline__ void wait_and_meet() {
 // the last `rest` of them each in `split` slices of K whose fp32 sums go to slots
 // of `part`.
 struct TilePlan {
+  int high;  // rows of X of a tile
   int mt, nt;
   int full, rest, split;
   float* part;
@@ -876,51 +877,68 @@ __global__ __launch_bounds__(256) void mx_fold_kernel(Args a, TilePlan plan) {
   }
 }
 
-// The tiles of a product.  The last, partly filled round of tiles is cut along K
-// where that is quicker by the times below.
-constexpr int kTileN = 256, kTileM = 256;
-// us a window of a tile takes, in a full round and in one that leaves CUs (and power)
-// to spare; what slices cost, their sums written and read.  2048 x 28672 x 8192, three
-// and a half rounds: 262 us as it is, 272 with the half round cut in two; 2041 x 4096 x
-// 14336, half a round: 82.7 and 80.2; 128 x 4096 x 14336, 16 tiles: 78 and, in eight, 27.
-constexpr double kFullUs = 3.5, kRestUs = 3.0;
-double fold_us(int slices) { return 4.0 + slices * 0.09; }
+// us that a window of a tile of 256 or 128 rows takes in a full round, and in one that
+// leaves CUs (and power) to spare; what slices cost, their sums written and read.
+// Measured, 256 rows, 256 with K cut, 128 rows, 128 with K cut:
+//   2048 x 28672 x 8192  262 272 325    -      1024 x 4096 x 14336  81.3 52.5 64.2 48.7
+//   2048 x 4096 x 14336 82.7 78.3  74.3 -      1024 x 4096 x 4096   29.0  -   22.7  -
+//   512 x 14336 x 4096  29.8   -   24.4 -      1024 x 14336 x 4096  35.7  -   44.2  -
+//   64 experts of 1536 x 2048, 64 rows each 44.3 and (128) 38.4, 128 rows 48.3 and 52.8
+constexpr int kTileN = 256;
+double window_us(int high, bool full) { return high == 256 ? full ? 3.75 : 3.0 : full ? 2.5 : 2.2; }
+double fold_us(int slices, int high) { return 4.0 + slices * high * (0.1 / 256); }
 int windows_of(int64_t k) { return (int)((k + kWindow * kMxBlock - 1) / (kWindow * kMxBlock)); }
 
-TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
+// The tiles of a product, `high` rows each, and its time in us.  The last, partly
+// filled round of tiles is cut along K where that is quicker.
+TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t experts, double& us) {
   TilePlan p = {};
-  const int cus = device_cu_count();
+  const int cus = device_cu_count(), windows = windows_of(k);
+  p.high = high;
   p.nt = (int)((n + kTileN - 1) / kTileN);
-  p.mt = (int)((m + kTileM - 1) / kTileM + min(experts, m));
+  p.mt = (int)((m + high - 1) / high + min(experts, m));
   p.full = p.mt * p.nt;
   p.split = 1;
-  if (experts) return p;
-  const int rest = p.full % cus, windows = windows_of(k);
-  double best = windows * kRestUs;
+  if (experts) {  // of about the same number of rows, whose last tile is half full
+    const int64_t parts = min(experts, m), tiles = p.nt * max(parts, m / high + parts / 2);
+    us = (tiles / cus * window_us(high, true) + (tiles % cus ? window_us(high, false) : 0)) * windows;
+    return p;
+  }
+  const int rest = p.full % cus;
+  double best = rest ? windows * window_us(high, false) : 0;
   for (int s = 2; s <= 8 && rest > 0 && rest * s <= cus && s <= windows; s++) {
-    const double t = (windows + s - 1) / s * kRestUs + fold_us(rest * s);
+    const double t = (windows + s - 1) / s * window_us(high, false) + fold_us(rest * s, high);
     if (t < best) best = t, p.split = s;
   }
+  us = p.full / cus * window_us(high, true) * windows + best;
   if (p.split > 1) p.rest = rest, p.full -= rest;
   return p;
 }
-size_t tile_ws_bytes(const TilePlan& p) { return (size_t)p.rest * p.split * kTileN * kTileM * 4; }
+TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts, double& us) {
+  double low_us;
+  const TilePlan p = tiles_of(256, m, n, k, experts, us), low = tiles_of(128, m, n, k, experts, low_us);
+  if (low_us >= us + 1.0) return p;  // the larger tile's results take longer to store
+  us = low_us;
+  return low;
+}
+size_t tile_ws_bytes(const TilePlan& p) { return (size_t)p.rest * p.split * kTileN * p.high * 4; }
+
+template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
+  const int grid = min(p.full + p.rest * p.split, device_cu_count());
+  hipLaunchKernelGGL((mx_tile_kernel<kTileN, BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !p.rest) return e;
+  hipLaunchKernelGGL((mx_fold_kernel<kTileN, BM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (BM / 64))), dim3(256), 0,
+                     stream, a, p);
+  return hipGetLastError();
+}
 
 template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t stream) {
-  TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0);
+  double us;
+  TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0, us);
   p.part = (float*)ws;
-  const int grid = min(p.full + p.rest * p.split, device_cu_count());
-  if (a.offsets)
-    hipLaunchKernelGGL((mx_tile_kernel<kTileN, kTileM, OT, true>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
-  else
-    hipLaunchKernelGGL((mx_tile_kernel<kTileN, kTileM, OT, false>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess && p.rest) {
-    hipLaunchKernelGGL((mx_fold_kernel<kTileN, kTileM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (kTileM / 64))),
-                       dim3(256), 0, stream, a, p);
-    e = hipGetLastError();
-  }
-  return e;
+  if (p.high == 256) return a.offsets ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<256, OT, false>(a, p, stream);
+  return a.offsets ? go_tiles<128, OT, true>(a, p, stream) : go_tiles<128, OT, false>(a, p, stream);
 }
 
 // Whether a product runs on the stream kernel: K below a window of the tile kernel, or
@@ -928,15 +946,16 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 // the read of W come to, one of them half hidden behind the other, and what a launch
 // costs.  The stream kernel's work is its row tiles, whose sums meet in LDS; the tile
 // kernel's its rounds of tiles.  Measured, stream and tile kernel:
-//   64 x 28672 x 8192   34.4 and 51.5    256 x 28672 x 8192   61.1 and 60.7
-//   256 x 14336 x 4096  26.8 and 28.2    512 x 14336 x 4096   44.9 and 29.9
-//   256 x 8192 x 1024   17.4 and 12.2    512 x 1024 x 1024     9.8 and 11.8
-//   128 x 4096 x 14336  20.6 and 27.1    1024 x 4096 x 14336  67.7 and 52.9
-//   8 experts of 14336 x 4096, 64 rows each 73.7 and 78.3, 128 rows 115 and 85
+//   128 x 28672 x 8192  41.8 and 46.8    256 x 28672 x 8192   61.1 and 56.3
+//   128 x 14336 x 4096  17.8 and 22.5    256 x 14336 x 4096   26.8 and 22.9
+//   512 x 4096 x 4096   18.8 and 22.1    1024 x 4096 x 4096   29.5 and 22.7
+//   33 x 8192 x 1024     8.3 and  8.3    128 x 8192 x 1024    12.3 and  8.3
+//   256 x 4096 x 14336  27.5 and 25.2    1024 x 4096 x 14336  67.7 and 48.7
+//   8 experts of 14336 x 4096, 64 rows each 73.7 and 70.1, 128 rows 115 and 84
 bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   p = stream_plan(m, k, experts);
   if (!p.ck) return false;
-  const int windows = windows_of(k), cus = device_cu_count();
+  const int cus = device_cu_count();
   if (k < kWindow * kMxBlock) return true;
   const int64_t parts = experts ? min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
   const double read = parts * n * (k / 2 + k / 32) / 5e6;
@@ -944,18 +963,17 @@ bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   auto total = [&](double work, double fixed) { return max(work, read) + min(work, read) / 2 + fixed; };
   const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows - 1) / kSRows)) *
                         (0.25 * p.mt + 0.3 * p.ck);
-  const TilePlan t = tile_plan(m, n, k, experts);
-  const int64_t whole = experts ? parts * ((rows + kTileM - 1) / kTileM) * t.nt : t.full;
-  double tile = (whole / cus * kFullUs + (whole % cus ? kRestUs : 0.0)) * windows;
-  if (t.rest) tile += (windows + t.split - 1) / t.split * kRestUs + fold_us(t.rest * t.split);
-  return total(stream, 4.0) <= total(tile, 5.0);
+  double tile;
+  tile_plan(m, n, k, experts, tile);
+  return total(stream, 3.0 + 0.4 * p.ck * p.mt) <= total(tile, 4.0);  // X is loaded first
 }
 
 }  // namespace
 
 size_t mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
   StreamPlan p;
-  return streams(m, n, k, experts, p) ? 0 : tile_ws_bytes(tile_plan(m, n, k, experts));
+  double us;
+  return streams(m, n, k, experts, p) ? 0 : tile_ws_bytes(tile_plan(m, n, k, experts, us));
 }
 
 hipError_t launch_mx_gemm(const MxGemm& g, void* ws, size_t, hipStream_t stream) {
