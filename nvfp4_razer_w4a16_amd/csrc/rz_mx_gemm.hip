@@ -600,7 +600,6 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   __shared__ __attribute__((aligned(16))) float part[kParts * kSWaves * kPart];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
-  const int g = lane >> 4, l16 = lane & 15;
   const int tiles = (int)((a.n + kSRows - 1) / kSRows);
   auto ring = [&](auto p) -> uint8_t* {
     constexpr int i = decltype(p)::value % kRing;
@@ -612,15 +611,9 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   };
   // exchange of a row's pieces: within aligned groups, at most 16, that divide the row
   auto key = [](int pieces, int r) { return r & (min(pieces & -pieces, 16) - 1); };
-  const int mine = 16 * wave + 4 * g;  // this lane's first of four blocks in a chunk
-  // of its blocks' scale bytes, those that the chunk has: past the row, scale 0
-  auto kept = [&](int pieces) { return mine + 4 <= pieces ? ~0u : mine >= pieces ? 0u : ~(~0u << 8 * (pieces - mine)); };
-  const uint32_t keep_last = kept(plan.last), keep = CK > 1 ? kept(plan.pieces) : keep_last;
   auto quotient = [](int p, int mul) { return (int)(((uint32_t)p * (uint32_t)mul) >> 20); };
   // direct load i of this lane: bytes from the chunk's first one, or past every end
   uint32_t off[kSLoads], off_last[kSLoads];
-  // its operands: fragment i in a chunk
-  int fo[4], fo_last[4];
 #pragma unroll
   for (int i = 0; i < kSLoads; i++) {
     const int p = (i * kSWaves + wave) * 64 + lane;
@@ -630,15 +623,6 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     };
     off_last[i] = offset(plan.last, plan.mul_last);
     off[i] = CK > 1 ? offset(plan.pieces, plan.mul_pieces) : off_last[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int c = mine + i;
-    auto offset = [&](int pieces) {  // past the row: some other codes
-      return min(l16 * pieces + (c ^ key(pieces, l16)), kSRows * kChunkB / 16 - 1) * 16;
-    };
-    fo_last[i] = offset(plan.last);
-    fo[i] = CK > 1 ? offset(plan.pieces) : fo_last[i];
   }
   // the scale bytes' pieces are exchanged likewise, by their place in the area
   auto sc_place = [&](int piece) {
@@ -690,6 +674,49 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       const Rsrc r = rsrc_of(wsc + (int64_t)tile * kSRows * nb - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
       if (tid * 16 < kArea) load_lds16(r, sc_from, l + wave * 1024);
     };
+    __syncthreads();  // the job before still reads the ring
+    load_scales(tile, a0);
+    load_chunk(tile, 0, r0);
+    __builtin_amdgcn_sched_barrier(0);
+    // this wave's share of X
+    u32x4_t fx[MT][CK][4];
+    uint32_t dx[MT][CK];
+#pragma unroll
+    for (int j = 0; j < MT; j++) {
+      int64_t row = min(t.m0 + 16 * j + (lane & 15), t.m1 - 1);
+      if (GROUPED && a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
+      const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
+#pragma unroll
+      for (int u = 0; u < CK; u++) {
+        const int b = u * plan.pieces + 16 * wave + 4 * (lane >> 4);  // the first of its four blocks
+#pragma unroll
+        for (int i = 0; i < 4; i++) fx[j][u][i] = *(const u32x4_t*)(pc + min(b + i, nb - 1) * 16);
+        dx[j][u] = scales4(ps, b, nb);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
+    load_chunk(tile + 1 / CK, 1 % CK, r1);
+    if constexpr (kRing > 3) load_chunk(tile + 2 / CK, 2 % CK, r2);
+    // Where the operands lie: worked out while the first loads are under way, hence
+    // from a lane number that the compiler cannot follow up to the kernel's start.
+    int at_lane = lane;
+    asm volatile("" : "+v"(at_lane));
+    const int g = at_lane >> 4, l16 = at_lane & 15, mine = 16 * wave + 4 * g;
+    // of its blocks' scale bytes, those that the chunk has: past the row, scale 0
+    auto kept = [&](int pieces) { return mine + 4 <= pieces ? ~0u : mine >= pieces ? 0u : ~(~0u << 8 * (pieces - mine)); };
+    const uint32_t keep_last = kept(plan.last), keep = CK > 1 ? kept(plan.pieces) : keep_last;
+    // fragment i of W in a chunk
+    int fo[4], fo_last[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int c = mine + i;
+      auto offset = [&](int pieces) {  // past the row: some other codes
+        return min(l16 * pieces + (c ^ key(pieces, l16)), kSRows * kChunkB / 16 - 1) * 16;
+      };
+      fo_last[i] = offset(plan.last);
+      fo[i] = CK > 1 ? offset(plan.pieces) : fo_last[i];
+    }
     // this lane's four scale bytes in the area: the two dwords that hold them
     const int sc_shift = (skew + l16 * nb) & 3;
     int so[CK][2];
@@ -700,30 +727,6 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
         const int at = min(((skew + l16 * nb + u * plan.pieces + mine) & ~3) + 4 * i, kArea - 4);
         so[u][i] = sc_place(at >> 4) * 16 + (at & 15);
       }
-
-    __syncthreads();  // the job before still reads the ring
-    load_scales(tile, a0);
-    load_chunk(tile, 0, r0);
-    // this wave's share of X
-    u32x4_t fx[MT][CK][4];
-    uint32_t dx[MT][CK];
-#pragma unroll
-    for (int j = 0; j < MT; j++) {
-      int64_t row = min(t.m0 + 16 * j + l16, t.m1 - 1);
-      if (GROUPED && a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
-      const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
-#pragma unroll
-      for (int u = 0; u < CK; u++) {
-        const int b = u * plan.pieces + mine;
-#pragma unroll
-        for (int i = 0; i < 4; i++) fx[j][u][i] = *(const u32x4_t*)(pc + min(b + i, nb - 1) * 16);
-        dx[j][u] = scales4(ps, b, nb);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
-    load_chunk(tile + 1 / CK, 1 % CK, r1);
-    if constexpr (kRing > 3) load_chunk(tile + 2 / CK, 2 % CK, r2);
 #pragma unroll
     for (int j = 0; j < MT; j++)
 #pragma unroll
