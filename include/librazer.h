@@ -340,9 +340,11 @@ razer_status razer_mx_quantize_gated(const void* gu, razer_dtype gu_dt, int64_t 
 razer_status razer_mx_dequant(const razer_mx* t, void* out, razer_dtype out_dt, void* stream);
 
 /* y[M, N] = x[M, K] * w[N, K]^T of two MXFP4 tensors, M from one token up; fp32
- * accumulation, one rounding to y_dt.  K == 0 is RAZER_E_UNSUPPORTED.  ws: at
- * least razer_mx_workspace_bytes(M, N, K, 0) bytes, 16-byte aligned (may be 0
- * -> NULL). */
+ * accumulation in an order that is the same from call to call, one rounding to
+ * y_dt (F16 above its range: infinity).  K == 0, K > 2^23 and M or N > 2^30 are
+ * RAZER_E_UNSUPPORTED.  y: 16-byte aligned, and not in memory that x or w hold.
+ * ws: at least razer_mx_workspace_bytes(M, N, K, 0) bytes, 16-byte aligned (may
+ * be 0 -> NULL). */
 razer_status razer_mx_gemm(const razer_mx* x, const razer_mx* w, void* y, razer_dtype y_dt, void* ws,
                            size_t ws_bytes, void* stream);
 
@@ -360,8 +362,9 @@ razer_status razer_mx_gemm(const razer_mx* x, const razer_mx* w, void* y, razer_
  * without waiting for it and the call can be captured.  Runs of no rows are
  * allowed; rows of y outside every run are left as they were; a row number
  * outside x (such as -1, padding) makes its row of y zero.  Offsets outside
- * [0, M] are clamped.  ws: razer_mx_workspace_bytes(M, N, K, experts) bytes,
- * 16-byte aligned. */
+ * [0, M] are clamped.  Limits as of razer_mx_gemm; with x_rows the codes of x
+ * are less than 4 GiB (RAZER_E_UNSUPPORTED).  ws: razer_mx_workspace_bytes(M, N,
+ * K, experts) bytes, 16-byte aligned. */
 razer_status razer_mx_gemm_grouped(const razer_mx* x, const razer_mx* w, const int32_t* offsets,
                                    int64_t experts, const int32_t* x_rows, int64_t m, void* y,
                                    razer_dtype y_dt, void* ws, size_t ws_bytes, void* stream);

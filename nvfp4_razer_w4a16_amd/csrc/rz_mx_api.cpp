@@ -32,8 +32,8 @@ razer_status check_mx(const razer_mx* t) {
 
 // A [rows, cols] operand of `stride` elements from row to row: 16-byte rows.
 bool strided_ok(const void* p, int64_t stride, int64_t cols, int dt) {
-  if (!p || !aligned(p, 16) || stride < cols) return false;
-  return stride * dtype_size(dt) % 16 == 0 && stride < INT64_MAX / 8;
+  if (!p || !aligned(p, 16) || stride < cols || stride >= INT64_MAX / 8) return false;
+  return stride * dtype_size(dt) % 16 == 0;
 }
 
 rz::MxView view_of(const razer_mx* t) { return {t->rows, t->cols, t->codes, t->scales}; }
@@ -159,7 +159,9 @@ razer_status razer_block_norm(const razer_norm* a, void* stream) {
 }
 
 size_t razer_mx_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
-  return m <= 0 || n <= 0 || k <= 0 || experts < 0 ? 0 : rz::mx_gemm_ws_bytes(m, n, k, experts);
+  if (m <= 0 || n <= 0 || k <= 0 || experts < 0) return 0;
+  if (m > kMaxGemmRows || n > kMaxGemmRows || k > kMaxGemmK || experts > RAZER_MX_MAX_EXPERTS) return 0;  // refused
+  return rz::mx_gemm_ws_bytes(m, n, k, experts);
 }
 
 }  // extern "C"

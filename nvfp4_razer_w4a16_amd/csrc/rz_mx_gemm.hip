@@ -944,11 +944,12 @@ TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t experts, do
   p.high = high;
   p.nt = (int)((n + kTileN - 1) / kTileN);
   p.mt = (int)((m + high - 1) / high + min(experts, m));
-  p.full = p.mt * p.nt;
+  p.full = (int)min((int64_t)p.mt * p.nt, (int64_t)INT32_MAX);  // more have no memory for their results
   p.split = 1;
   if (experts) {  // of about the same number of rows, whose last tile is half full
-    const int64_t parts = min(experts, m), tiles = p.nt * max(parts, m / high + parts / 2);
-    us = (tiles / cus * window_us(high, true) + (tiles % cus ? window_us(high, false) : 0)) * windows;
+    const int64_t parts = min(experts, m);
+    const double tiles = (double)p.nt * max(parts, m / high + parts / 2), rounds = floor(tiles / cus);
+    us = (rounds * window_us(high, true) + (tiles > rounds * cus ? window_us(high, false) : 0)) * windows;
     return p;
   }
   const int rest = p.full % cus;
@@ -1005,7 +1006,7 @@ bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   const int cus = device_cu_count();
   if (k < kWindow * kMxBlock) return true;
   const int64_t parts = experts ? min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
-  const double read = parts * n * (k / 2 + k / 32) / 5e6;
+  const double read = (double)parts * n * (k / 2 + k / 32) / 5e6;
   auto rounds = [&](int64_t units) { return (double)((units + cus - 1) / cus); };
   auto total = [&](double work, double fixed) { return max(work, read) + min(work, read) / 2 + fixed; };
   const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows - 1) / kSRows)) *

@@ -184,3 +184,11 @@ def test_binding_refuses_before_it_writes():
             rz.razer_mx_quantize(h.to(bad))
     torch.cuda.synchronize()
     assert (out == 7.0).all()
+
+
+def test_workspace_bytes_of_refused_sizes():
+    for a in ((2 ** 30 + 1, 8, 64, 0), (8, 2 ** 62, 64, 0), (8, 8, 2 ** 23 + 32, 0), (8, 8, 64, rz.RAZER_MX_MAX_EXPERTS + 1),
+              (2 ** 63 - 1, 2 ** 63 - 1, 2 ** 63 - 1, 2 ** 63 - 1)):
+        assert rz.razer_mx_workspace_bytes(*a) == 0
+    for a in ((2 ** 30, 2 ** 30, 2 ** 23, 0), (2 ** 30, 2 ** 30, 2 ** 23, 4096), (1, 2 ** 30, 32, 0)):
+        assert rz.razer_mx_workspace_bytes(*a) >= 0
