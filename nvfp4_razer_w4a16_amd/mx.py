@@ -15,6 +15,7 @@ The package re-exports every name here.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -126,9 +127,9 @@ class MxTensor:
         if len(shape) != 2:
             codes, scales = codes.view(-1, shape[-1]), scales.view(-1, scales.shape[-1])
             shape = codes.shape
-        t.rows, t.cols = shape[0], 2 * shape[1]
-        t._buf, t._codes, t._scales, t._valid = None, codes, scales, False
-        t.check()
+        rows, half = shape
+        t.rows, t.cols, t._buf, t._codes, t._scales = rows, 2 * half, None, codes, scales
+        t._check_buffers("MxTensor")
         return t
 
     @property
@@ -162,15 +163,19 @@ class MxTensor:
         """Its buffers match its shape (buffers it was given are looked at once);
         returns their device."""
         if not self._valid:
-            c, s, rows, cols = self._codes, self._scales, self.rows, self.cols
-            if not (c.dtype == s.dtype == torch.uint8 and c.is_contiguous() and s.is_contiguous()
-                    and cols % MX_BLOCK == 0 and c.shape == (rows, cols // 2) and s.shape == (rows, cols // MX_BLOCK)
-                    and c.device == s.device):
-                raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
-                                 f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
-            self.device = c.device
-            self._valid = True
+            self._check_buffers(name)
         return self.device
+
+    def _check_buffers(self, name: str):
+        c, s, rows, cols = self._codes, self._scales, self.rows, self.cols
+        dev, u8 = c.device, torch.uint8
+        if (c.dtype is not u8 or s.dtype is not u8 or cols % MX_BLOCK or s.device != dev
+                or c.shape != (rows, cols // 2) or s.shape != (rows, cols // MX_BLOCK)
+                or not c.is_contiguous() or not s.is_contiguous()):
+            raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {dev} and scales {tuple(s.shape)} "
+                             f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
+        self.device = dev
+        self._valid = True
 
     def struct(self) -> razer_mx:
         if self._buf is not None:
@@ -182,8 +187,8 @@ class MxTensor:
 def _operand(t, name: str) -> torch.device:
     if not isinstance(t, MxTensor):
         raise TypeError(f"{name} must be an MxTensor")
-    dev = t.check(name)
-    if dev.type != "cuda":
+    dev = t.device if t._valid else t.check(name)
+    if dev.index is None:  # of a tensor on a GPU it never is
         raise ValueError(f"{name} must be on a GPU, not {dev}")
     return dev
 
@@ -265,13 +270,19 @@ def razer_mx_workspace_bytes(m: int, n: int, k: int, experts: int = 0) -> int:
     return int(lib().razer_mx_workspace_bytes(m, n, k, experts))
 
 
+@functools.lru_cache(4096)
+def _workspace_bytes(m: int, n: int, k: int, device: int) -> int:
+    """razer_mx_workspace_bytes on a device: a function of the sizes and its compute units."""
+    return razer_mx_workspace_bytes(m, n, k)
+
+
 def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
     if out is None:
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _check_buffer(out, (m, n), dev, "out")
     if workspace is None:
-        need = lib().razer_mx_workspace_bytes(m, n, k, experts)
+        need = razer_mx_workspace_bytes(m, n, k, experts) if experts else _workspace_bytes(m, n, k, dev.index)
         if not need:
             return out, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -290,9 +301,11 @@ def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloa
     _same(_operand(w, "w"), dev, "w")
     if x.cols != w.cols:
         raise ValueError(f"x has {x.cols} columns, w {w.cols}")
+    current = _stream(dev)
     out, ws, wsb = _product_buffers(x.rows, w.rows, x.cols, 0, dev, out_dtype, out, workspace)
-    _check(lib().razer_mx_gemm(x.struct(), w.struct(), out.data_ptr(), _dtype(out.dtype), ws, wsb,
-                               _stream(dev)), "razer_mx_gemm")
+    status = lib().razer_mx_gemm(x.struct(), w.struct(), out.data_ptr(), _dtype(out.dtype), ws, wsb, current)
+    if status:
+        _check(status, "razer_mx_gemm")
     return out
 
 
