@@ -507,9 +507,9 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // which the waves share: wave w takes 512 elements of each 4096 and keeps its share of
 // up to 16 MT rows of X (a "job") in registers for all the row tiles that the
 // workgroup walks through, so that nothing but W is read in the loop.  The row
-// tiles of all jobs stand in one line that is cut evenly between the workgroups,
-// however the rows are spread over the experts; a cut that crosses jobs loads the
-// next one's X on the way.
+// tiles of all jobs stand in one line that is cut between the workgroups, however
+// the rows are spread over the experts; a piece that crosses jobs loads the next
+// one's X on the way.
 //
 // A row tile comes in CK chunks of up to 4096 elements of K, 32 KiB each, by
 // direct-to-LDS loads into a ring of RING buffers, RING - 1 chunks ahead: memory is
@@ -518,6 +518,11 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // and what is under way costs no registers.  A chunk's 16-byte pieces lie in LDS as
 // in memory but for an exchange within a row, piece c of row r at c ^ (r & mask),
 // which spreads the rows over the banks where the row's length would not.
+//
+// Rows of at most 2048 or 1024 elements come RT = two or four row tiles a chunk, each
+// of which has four or two of the waves to share its K: a chunk keeps its size, its
+// one barrier and its number of sums.  (128 experts of 2048 x 768, 4 rows each: 40.7 us
+// with one row tile a chunk, 25.8 with four; 16 x 28672 x 2048: 9.8 and 8.5.)
 //
 // Of a wave's sixteen blocks, lane group g = lane / 16 takes the four from 4 g on, one
 // a product: K is summed in another order, the same for both operands.  So a lane's
@@ -543,11 +548,11 @@ struct Cuts {
   uint32_t jobs, per_job;  // 0: even pieces of the line
   uint32_t share, extra;   // the first `extra` pieces are share + 1 tiles
 };
-__host__ __device__ __forceinline__ Cuts cuts_of(uint32_t tiles, uint32_t jobs, uint32_t grid) {
+__host__ __device__ __forceinline__ Cuts cuts_of(uint32_t tiles, uint32_t jobs, uint32_t grid, uint32_t rt) {
   const uint32_t line = tiles * jobs;
   Cuts c = {jobs, jobs ? grid / jobs : 0, line / grid, 0};
   const uint32_t most = c.per_job ? tiles / c.per_job : 0, rest = tiles - most * c.per_job;
-  if (c.per_job && most + (rest ? 1 : 0) <= c.share + 2) {
+  if (c.per_job && most + (rest ? 1 : 0) <= c.share + 2 * rt) {
     c.share = most;
     c.extra = rest;
   } else {
@@ -560,6 +565,7 @@ __host__ __device__ __forceinline__ Cuts cuts_of(uint32_t tiles, uint32_t jobs, 
 // The chunks of a row: `ck` of them, each `pieces` 16-byte pieces, the last `last`.
 struct StreamPlan {
   int ck, mt;  // ck = 0: not covered
+  int rt;      // row tiles of a chunk
   int rows;    // of a job, at most 16 mt
   int pieces, last;
   int mul_pieces, mul_last;  // p / d = p * mul >> 20 for p < 2048
@@ -577,11 +583,13 @@ template <typename F, int... I> __device__ __forceinline__ bool for_each(F& f, s
 constexpr int stream_ring(int mt) { return mt == 4 ? 3 : 4; }
 constexpr int stream_blocks(int ck) { return ck == 4 ? 480 : 128 * ck; }
 
-template <int CK, int MT, bool GROUPED>
+template <int RT, int CK, int MT, bool GROUPED>
 __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int y_dtype, StreamPlan plan) {
   constexpr int kRing = stream_ring(MT);
   constexpr int kPart = kSRows * 16 * MT;  // fp32 sums of one wave
-  constexpr int kOuts = (kPart + 64 * kSWaves - 1) / (64 * kSWaves);  // results of a thread
+  constexpr int kOuts = (RT * kPart + 64 * kSWaves - 1) / (64 * kSWaves);  // results of a thread
+  static_assert(RT == 1 || CK == 1, "chunks of several row tiles hold whole rows");
+  constexpr int kRows = kSRows * RT, kAlong = kSWaves / RT;  // rows of W in a chunk, waves along K
   // A round is whole row tiles, whole turns of the ring and at least two tiles.
   constexpr int kRound = CK == 4 ? 8 : kRing % CK == 0 ? kRing : kRing * CK;
   constexpr int kAreas = kRound / CK;      // scale areas, one a row tile of the round
@@ -600,7 +608,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   __shared__ __attribute__((aligned(16))) float part[kParts * kSWaves * kPart];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
-  const int tiles = (int)((a.n + kSRows - 1) / kSRows);
+  const int units = (int)((a.n + kSRows - 1) / kSRows);  // what the line is cut into
   auto ring = [&](auto p) -> uint8_t* {
     constexpr int i = decltype(p)::value % kRing;
     return i == 0 ? r0 : i == 1 ? r1 : i == 2 ? r2 : r3;
@@ -619,7 +627,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     const int p = (i * kSWaves + wave) * 64 + lane;
     auto offset = [&](int pieces, int mul) {
       const int r = quotient(p, mul), c = p - r * pieces;
-      return r < kSRows ? (uint32_t)(r * kb + (c ^ key(pieces, r)) * 16) : 0x7FFFFFFFu;
+      return r < kRows ? (uint32_t)(r * kb + (c ^ key(pieces, r)) * 16) : 0x7FFFFFFFu;
     };
     off_last[i] = offset(plan.last, plan.mul_last);
     off[i] = CK > 1 ? offset(plan.pieces, plan.mul_pieces) : off_last[i];
@@ -633,34 +641,37 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   // this workgroup's piece of the line
   const uint32_t b = blockIdx.x;
   Cuts c = plan.cuts;
-  if (GROUPED) c = cuts_of((uint32_t)tiles, (uint32_t)live_tiles(a, plan.rows), gridDim.x);
-  int job, tile, left;
+  if (GROUPED) c = cuts_of((uint32_t)units, (uint32_t)live_tiles(a, plan.rows), gridDim.x, RT);
+  int job, unit, left;
   if (c.per_job) {
     job = GROUPED ? (int)(b / c.per_job) : quotient((int)b, plan.mul_per_job);
     const uint32_t cut = b - (uint32_t)job * c.per_job;
-    tile = (int)(c.share * cut + min(cut, c.extra));
+    unit = (int)(c.share * cut + min(cut, c.extra));
     left = job < (int)c.jobs ? (int)(c.share + (cut < c.extra ? 1 : 0)) : 0;
   } else {
     const uint32_t start = c.share * b + min(b, c.extra);
-    job = (int)(start / (uint32_t)tiles);
-    tile = (int)(start - (uint32_t)job * (uint32_t)tiles);
+    job = (int)(start / (uint32_t)units);
+    unit = (int)(start - (uint32_t)job * (uint32_t)units);
     left = (int)(c.share + (b < c.extra ? 1 : 0));
   }
-  for (; left > 0; job++, tile = 0) {
+  for (; left > 0; job++, unit = 0) {
     Tile t;
     if (GROUPED)
       t = find_tile(a, plan.rows, job);
     else
       t = Tile{(int64_t)job * plan.rows, min((int64_t)(job + 1) * plan.rows, a.m), 0};
     if (GROUPED && t.expert < 0) return;
-    const uint8_t* wc = a.wc + (int64_t)t.expert * a.n * kb;
-    const uint8_t* wsc = a.ws + (int64_t)t.expert * a.n * nb;
-    const int end = min(tile + left, tiles);
-    left -= end - tile;
-    auto rows_of = [&](int tile) { return tile < end ? min((int)a.n - tile * kSRows, kSRows) : 0; };
+    // its rows of W in this job: n_rows from n0 on, in `end` chunks or times CK
+    const int taken = min(left, units - unit), n0 = unit * kSRows;
+    const int n_rows = (int)min((int64_t)taken * kSRows, a.n - n0), end = (n_rows + kRows - 1) / kRows;
+    left -= taken;
+    int tile = 0;
+    const uint8_t* wc = a.wc + ((int64_t)t.expert * a.n + n0) * kb;
+    const uint8_t* wsc = a.ws + ((int64_t)t.expert * a.n + n0) * nb;
+    auto rows_of = [&](int tile) { return tile < end ? min(n_rows - tile * kRows, kRows) : 0; };
     auto load_chunk = [&](int tile, int ck, uint8_t* l) {
       const int col = ck * plan.pieces * 16;
-      const Rsrc r = rsrc_of(wc + (int64_t)tile * kSRows * kb + col, max(rows_of(tile) * kb - col, 0));
+      const Rsrc r = rsrc_of(wc + (int64_t)tile * kRows * kb + col, max(rows_of(tile) * kb - col, 0));
 #pragma unroll
       for (int i = 0; i < kSLoads; i++)
         load_lds16(r, ck == CK - 1 ? off_last[i] : off[i], l + (i * kSWaves + wave) * 1024);
@@ -671,7 +682,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     const int skew = (int)((uintptr_t)wsc & 3);  // of every row tile: 16 rows are whole dwords
     auto load_scales = [&](int tile, uint8_t* l) {
       const int rows = rows_of(tile);
-      const Rsrc r = rsrc_of(wsc + (int64_t)tile * kSRows * nb - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
+      const Rsrc r = rsrc_of(wsc + (int64_t)tile * kRows * nb - skew, rows ? (rows * nb + skew + 3) & ~3 : 0);
       if (tid * 16 < kArea) load_lds16(r, sc_from, l + wave * 1024);
     };
     __syncthreads();  // the job before still reads the ring
@@ -688,7 +699,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
 #pragma unroll
       for (int u = 0; u < CK; u++) {
-        const int b = u * plan.pieces + 16 * wave + 4 * (lane >> 4);  // the first of its four blocks
+        const int b = u * plan.pieces + 16 * (wave % kAlong) + 4 * (lane >> 4);  // the first of its four blocks
 #pragma unroll
         for (int i = 0; i < 4; i++) fx[j][u][i] = *(const u32x4_t*)(pc + min(b + i, nb - 1) * 16);
         dx[j][u] = scales4(ps, b, nb);
@@ -702,7 +713,8 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     // from a lane number that the compiler cannot follow up to the kernel's start.
     int at_lane = lane;
     asm volatile("" : "+v"(at_lane));
-    const int g = at_lane >> 4, l16 = at_lane & 15, mine = 16 * wave + 4 * g;
+    const int g = at_lane >> 4, w_row = (RT == 1 ? 0 : wave / kAlong * kSRows) + (at_lane & 15),
+              mine = 16 * (wave % kAlong) + 4 * g;
     // of its blocks' scale bytes, those that the chunk has: past the row, scale 0
     auto kept = [&](int pieces) { return mine + 4 <= pieces ? ~0u : mine >= pieces ? 0u : ~(~0u << 8 * (pieces - mine)); };
     const uint32_t keep_last = kept(plan.last), keep = CK > 1 ? kept(plan.pieces) : keep_last;
@@ -712,19 +724,19 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     for (int i = 0; i < 4; i++) {
       const int c = mine + i;
       auto offset = [&](int pieces) {  // past the row: some other codes
-        return min(l16 * pieces + (c ^ key(pieces, l16)), kSRows * kChunkB / 16 - 1) * 16;
+        return min(w_row * pieces + (c ^ key(pieces, w_row)), kSRows * kChunkB / 16 - 1) * 16;
       };
       fo_last[i] = offset(plan.last);
       fo[i] = CK > 1 ? offset(plan.pieces) : fo_last[i];
     }
     // this lane's four scale bytes in the area: the two dwords that hold them
-    const int sc_shift = (skew + l16 * nb) & 3;
+    const int sc_shift = (skew + w_row * nb) & 3;
     int so[CK][2];
 #pragma unroll
     for (int u = 0; u < CK; u++)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        const int at = min(((skew + l16 * nb + u * plan.pieces + mine) & ~3) + 4 * i, kArea - 4);
+        const int at = min(((skew + w_row * nb + u * plan.pieces + mine) & ~3) + 4 * i, kArea - 4);
         so[u][i] = sc_place(at >> 4) * 16 + (at & 15);
       }
 #pragma unroll
@@ -737,7 +749,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
 #pragma unroll
     for (int i = 0; i < kOuts; i++) {
       none[i] = false;
-      const int64_t row = t.m0 + ((tid + i * 64 * kSWaves) >> 4);
+      const int64_t row = t.m0 + ((tid + i * 64 * kSWaves) % kPart >> 4);
       if (GROUPED && a.x_rows && row < t.m1) {
         const int64_t r = a.x_rows[row];
         none[i] = r < 0 || r >= a.x_rows_total;
@@ -748,18 +760,19 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
 #pragma unroll
       for (int i = 0; i < kOuts; i++) {
         const int o = tid + i * 64 * kSWaves;
-        const int n = o & 15, m = o >> 4;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
-        const int64_t row = t.m0 + m, col = (int64_t)tile * kSRows + n;
-        if (o >= kPart || row >= t.m1 || col >= a.n) continue;
-        const float* p = part + set * kSWaves * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
-        float v[kSWaves];
+        const int n = o & 15, m = (RT == 1 ? o : o % kPart) >> 4, at_tile = RT == 1 ? 0 : o / kPart;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
+        const int64_t row = t.m0 + m;
+        const int col = tile * kRows + at_tile * kSRows + n;
+        if (o >= RT * kPart || row >= t.m1 || col >= n_rows) continue;
+        const float* p = part + (set * kSWaves + at_tile * kAlong) * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+        float v[kAlong];
 #pragma unroll
-        for (int w = 0; w < kSWaves; w++) v[w] = p[w * kPart];
+        for (int w = 0; w < kAlong; w++) v[w] = p[w * kPart];
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kSWaves; w++) sum += v[w];
+        for (int w = 0; w < kAlong; w++) sum += v[w];
         if (none[i]) sum = 0.0f;
-        const int64_t at = row * a.n + col;
+        const int64_t at = row * a.n + n0 + col;
         if (y_dtype == kF32) ((float*)a.y)[at] = sum;
         else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(sum);
         else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(sum);
@@ -771,7 +784,6 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       asm volatile("" ::: "memory");
     };
     f32x4_t acc[MT];
-    const int first = tile;
     // position P of a round: chunk P % CK of the row tile, ring place P % kRing;
     // false behind the last row tile
     auto chunk = [&](auto which) {
@@ -804,7 +816,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
         asm volatile("" : "+v"(acc[j]));  // here, not behind the next barrier with all chunks' operands
       }
       if constexpr (kDefer && ck == 0)
-        if (tile > first) finish(tile - 1, (P / CK + kParts - 1) % kParts);
+        if (tile > 0) finish(tile - 1, (P / CK + kParts - 1) % kParts);
       if constexpr (ck == CK - 1) {
         float* sums = part + (P / CK % kParts * kSWaves + wave) * kPart;
 #pragma unroll
@@ -821,13 +833,13 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     }
     if constexpr (kDefer) {
       meet();
-      finish(end - 1, (end - 1 - first) % kParts);
+      finish(end - 1, (end - 1) % kParts);
     }
   }
 }
 
 // The stream kernel's shape for `m` rows, of each of `experts` on average if that is not 0.
-StreamPlan stream_plan(int64_t m, int64_t k, int64_t experts) {
+StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
   StreamPlan p = {};
   const int64_t kb = k / 2;
   int ck = 1;
@@ -846,6 +858,12 @@ StreamPlan stream_plan(int64_t m, int64_t k, int64_t experts) {
     if (jobs * p.rows >= m) p.rows = (int)((m + jobs - 1) / jobs);
   }
   p.ck = ck;
+  // Short rows: several row tiles a chunk, if there is a chunk for every CU.  Not for
+  // jobs of 64 rows, where the sums of a chunk take as long as two smaller ones' (64 x
+  // 28672 x 2048: 15.2 us and, one row tile a chunk, 14.1).
+  const int64_t jobs = experts ? min(experts, m) : (m + p.rows - 1) / p.rows;
+  p.rt = p.mt == 4 ? 1 : kb <= kChunkB / 4 ? 4 : kb <= kChunkB / 2 ? 2 : 1;
+  while (p.rt > 1 && jobs * ((n + kSRows * p.rt - 1) / (kSRows * p.rt)) < device_cu_count()) p.rt /= 2;
   p.pieces = (int)(((kb + ck - 1) / ck + 63) / 64 * 4);  // whole products' blocks
   p.last = (int)(kb / 16) - p.pieces * (ck - 1);
   p.mul_pieces = (1 << 20) / p.pieces + 1;
@@ -855,30 +873,32 @@ StreamPlan stream_plan(int64_t m, int64_t k, int64_t experts) {
   return p;
 }
 
-template <int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, StreamPlan p, hipStream_t stream) {
+template <int RT, int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, StreamPlan p, hipStream_t stream) {
   const int64_t tiles = (a.n + kSRows - 1) / kSRows, full = (a.m + p.rows - 1) / p.rows;
   const int64_t jobs = a.offsets ? min(full + a.experts, a.m) : full;
   const int64_t grid = min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
   if (!a.offsets) {
-    p.cuts = cuts_of((uint32_t)tiles, (uint32_t)jobs, (uint32_t)grid);
+    p.cuts = cuts_of((uint32_t)tiles, (uint32_t)jobs, (uint32_t)grid, RT);
     if (p.cuts.per_job) p.mul_per_job = (1 << 20) / (int)p.cuts.per_job + 1;
   }
   const dim3 blocks((unsigned)grid), threads(64 * kSWaves);
-  if (a.offsets) hipLaunchKernelGGL((mx_stream_kernel<CK, MT, true>), blocks, threads, 0, stream, a, y_dtype, p);
-  else hipLaunchKernelGGL((mx_stream_kernel<CK, MT, false>), blocks, threads, 0, stream, a, y_dtype, p);
+  if (a.offsets) hipLaunchKernelGGL((mx_stream_kernel<RT, CK, MT, true>), blocks, threads, 0, stream, a, y_dtype, p);
+  else hipLaunchKernelGGL((mx_stream_kernel<RT, CK, MT, false>), blocks, threads, 0, stream, a, y_dtype, p);
   return hipGetLastError();
 }
 
 hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t s) {
+  if (p.rt == 4) return p.mt == 1 ? go_stream<4, 1, 1>(a, y_dtype, p, s) : go_stream<4, 1, 2>(a, y_dtype, p, s);
+  if (p.rt == 2) return p.mt == 1 ? go_stream<2, 1, 1>(a, y_dtype, p, s) : go_stream<2, 1, 2>(a, y_dtype, p, s);
   switch (p.mt * 16 + p.ck) {
-    case 17: return go_stream<1, 1>(a, y_dtype, p, s);
-    case 18: return go_stream<2, 1>(a, y_dtype, p, s);
-    case 20: return go_stream<4, 1>(a, y_dtype, p, s);
-    case 33: return go_stream<1, 2>(a, y_dtype, p, s);
-    case 34: return go_stream<2, 2>(a, y_dtype, p, s);
-    case 36: return go_stream<4, 2>(a, y_dtype, p, s);
-    case 65: return go_stream<1, 4>(a, y_dtype, p, s);
-    default: return go_stream<2, 4>(a, y_dtype, p, s);
+    case 17: return go_stream<1, 1, 1>(a, y_dtype, p, s);
+    case 18: return go_stream<1, 2, 1>(a, y_dtype, p, s);
+    case 20: return go_stream<1, 4, 1>(a, y_dtype, p, s);
+    case 33: return go_stream<1, 1, 2>(a, y_dtype, p, s);
+    case 34: return go_stream<1, 2, 2>(a, y_dtype, p, s);
+    case 36: return go_stream<1, 4, 2>(a, y_dtype, p, s);
+    case 65: return go_stream<1, 1, 4>(a, y_dtype, p, s);
+    default: return go_stream<1, 2, 4>(a, y_dtype, p, s);
   }
 }
 
@@ -1001,7 +1021,7 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 //   256 x 4096 x 14336  27.5 and 25.2    1024 x 4096 x 14336  67.7 and 48.7
 //   8 experts of 14336 x 4096, 64 rows each 73.7 and 70.1, 128 rows 115 and 84
 bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
-  p = stream_plan(m, k, experts);
+  p = stream_plan(m, n, k, experts);
   if (!p.ck) return false;
   const int cus = device_cu_count();
   if (k < kWindow * kMxBlock) return true;
@@ -1009,7 +1029,7 @@ bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   const double read = (double)parts * n * (k / 2 + k / 32) / 5e6;
   auto rounds = [&](int64_t units) { return (double)((units + cus - 1) / cus); };
   auto total = [&](double work, double fixed) { return max(work, read) + min(work, read) / 2 + fixed; };
-  const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows - 1) / kSRows)) *
+  const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows * p.rt - 1) / (kSRows * p.rt))) *
                         (0.25 * p.mt + 0.3 * p.ck);
   double tile;
   tile_plan(m, n, k, experts, tile);
