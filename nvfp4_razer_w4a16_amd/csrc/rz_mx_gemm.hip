@@ -504,9 +504,9 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // ---- stream kernel -------------------------------------------------------------
 // For few rows of X the product is a read of W.  A workgroup of eight waves owns 16
 // W rows at a time (a "row tile", one contiguous piece of memory) and all of K,
-// which the waves share: wave w takes 512 elements of each 4096 and keeps its share of
-// up to 16 MT rows of X (a "job") in registers for all the row tiles that the
-// workgroup walks through, so that nothing but W is read in the loop.  The row
+// which the waves share in units of 512 elements; each keeps its share of up to 16 MT
+// rows of X (a "job") in registers for all the row tiles that the workgroup walks
+// through, so that nothing but W is read in the loop.  The row
 // tiles of all jobs stand in one line that is cut between the workgroups, however
 // the rows are spread over the experts; a piece that crosses jobs loads the next
 // one's X on the way.
@@ -586,13 +586,21 @@ constexpr int stream_blocks(int ck) { return ck == 4 ? 480 : 128 * ck; }
 template <int RT, int CK, int MT, bool GROUPED>
 __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int y_dtype, StreamPlan plan) {
   constexpr int kRing = stream_ring(MT);
-  constexpr int kPart = kSRows * 16 * MT;  // fp32 sums of one wave
-  constexpr int kOuts = (RT * kPart + 64 * kSWaves - 1) / (64 * kSWaves);  // results of a thread
   static_assert(RT == 1 || CK == 1, "chunks of several row tiles hold whole rows");
-  constexpr int kRows = kSRows * RT, kAlong = kSWaves / RT;  // rows of W in a chunk, waves along K
-  // A round is whole row tiles, whole turns of the ring and at least two tiles.
-  constexpr int kRound = CK == 4 ? 8 : kRing % CK == 0 ? kRing : kRing * CK;
-  constexpr int kAreas = kRound / CK;      // scale areas, one a row tile of the round
+  // Of the waves of a row tile, kAlong share its K and kX the job's rows; a wave has
+  // kUnits times 512 elements of K and kMT times 16 rows.  Sharing the rows reads W's
+  // fragments twice from LDS, but leaves room for a second set of sums: 128 x 14336 x
+  // 4096 17.0 us without and 16.0 with it, 27 rows 10.3 and 9.8.  (64 experts of 1503 x
+  // 2080, 1000 rows: 29.8 and 31.7.)
+  constexpr int kX = !GROUPED && CK == 1 && MT > 1 ? 2 : 1, kAlong = kSWaves / RT / kX, kUnits = kX, kMT = MT / kX;
+  constexpr int kRows = kSRows * RT;         // rows of W in a chunk
+  constexpr int kPart = kSRows * 16 * kMT;   // fp32 sums of one wave
+  constexpr int kSums = kSRows * 16 * MT;    // results of a row tile
+  constexpr int kOuts = (RT * kSums + 64 * kSWaves - 1) / (64 * kSWaves);  // of a thread in a chunk
+  // A round is whole row tiles and whole turns of the ring, and an even number of tiles
+  // where there are two sets of sums.
+  constexpr int kRound = CK == 4 ? 8 : kRing % 2 ? 2 * kRing : kRing;
+  constexpr int kAreas = CK == 1 ? kRing : kRound / CK;  // scale areas, in turn for the round's row tiles
   // Row tiles that the scale bytes are requested ahead: enough that the loads of
   // kRing - 2 chunks are behind them when they are needed.
   constexpr int kScAhead = CK == 1 ? kRing - 2 : 1;
@@ -601,10 +609,10 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   __shared__ __attribute__((aligned(16))) uint8_t r0[kSRows * kChunkB], r1[kSRows * kChunkB], r2[kSRows * kChunkB],
       r3[kRing > 3 ? kSRows * kChunkB : 16];
   __shared__ __attribute__((aligned(16))) uint8_t a0[kArea], a1[kArea], a2[kAreas > 2 ? kArea : 16], a3[kAreas > 3 ? kArea : 16];
-  // The waves' sums of a row tile are added behind the next chunk's barrier, where
-  // the place to keep them until then is not needed again or there is a second one.
-  constexpr bool kDefer = CK > 1 || MT == 1;
-  constexpr int kParts = CK == 1 && MT == 1 ? 2 : 1;
+  // The waves' sums of a row tile are added behind the next chunk's barrier, where there
+  // is a second set of them or a barrier more before the next tile's are written.
+  constexpr int kParts = CK == 1 && (MT == 1 || kX == 2) ? 2 : 1;
+  constexpr bool kDefer = CK > 1 || kParts == 2;
   __shared__ __attribute__((aligned(16))) float part[kParts * kSWaves * kPart];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = (int)(a.k / kMxBlock), kb = nb * 16;
@@ -690,20 +698,23 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     load_chunk(tile, 0, r0);
     __builtin_amdgcn_sched_barrier(0);
     // this wave's share of X
-    u32x4_t fx[MT][CK][4];
-    uint32_t dx[MT][CK];
+    u32x4_t fx[kMT][CK][kUnits][4];
+    uint32_t dx[kMT][CK][kUnits];
+    const int along = wave % kAlong, x_row = wave / kAlong % kX * 16 * kMT;
 #pragma unroll
-    for (int j = 0; j < MT; j++) {
-      int64_t row = min(t.m0 + 16 * j + (lane & 15), t.m1 - 1);
+    for (int j = 0; j < kMT; j++) {
+      int64_t row = min(t.m0 + x_row + 16 * j + (lane & 15), t.m1 - 1);
       if (GROUPED && a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
       const uint8_t *pc = a.xc + row * kb, *ps = a.xs + row * nb;
 #pragma unroll
-      for (int u = 0; u < CK; u++) {
-        const int b = u * plan.pieces + 16 * (wave % kAlong) + 4 * (lane >> 4);  // the first of its four blocks
+      for (int u = 0; u < CK; u++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) fx[j][u][i] = *(const u32x4_t*)(pc + min(b + i, nb - 1) * 16);
-        dx[j][u] = scales4(ps, b, nb);
-      }
+        for (int v = 0; v < kUnits; v++) {
+          const int b = u * plan.pieces + 16 * (along + v * kAlong) + 4 * (lane >> 4);  // the first of its four blocks
+#pragma unroll
+          for (int i = 0; i < 4; i++) fx[j][u][v][i] = *(const u32x4_t*)(pc + min(b + i, nb - 1) * 16);
+          dx[j][u][v] = scales4(ps, b, nb);
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
@@ -713,43 +724,52 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
     // from a lane number that the compiler cannot follow up to the kernel's start.
     int at_lane = lane;
     asm volatile("" : "+v"(at_lane));
-    const int g = at_lane >> 4, w_row = (RT == 1 ? 0 : wave / kAlong * kSRows) + (at_lane & 15),
-              mine = 16 * (wave % kAlong) + 4 * g;
+    const int g = at_lane >> 4, w_row = wave / (kAlong * kX) * kSRows + (at_lane & 15), mine = 16 * along + 4 * g;
     // of its blocks' scale bytes, those that the chunk has: past the row, scale 0
-    auto kept = [&](int pieces) { return mine + 4 <= pieces ? ~0u : mine >= pieces ? 0u : ~(~0u << 8 * (pieces - mine)); };
-    const uint32_t keep_last = kept(plan.last), keep = CK > 1 ? kept(plan.pieces) : keep_last;
-    // fragment i of W in a chunk
+    auto kept = [&](int left) { return left >= 4 ? ~0u : left <= 0 ? 0u : ~(~0u << 8 * left); };
+    uint32_t keep[kUnits], keep_last[kUnits];
+#pragma unroll
+    for (int v = 0; v < kUnits; v++) {
+      keep_last[v] = kept(plan.last - mine - 16 * v * kAlong);
+      keep[v] = CK > 1 ? kept(plan.pieces - mine - 16 * v * kAlong) : keep_last[v];
+    }
+    // fragment i of W in a chunk; the next unit's lie kAlong * 256
+    // bytes on, as the exchange is within 16 pieces
     int fo[4], fo_last[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int c = mine + i;
       auto offset = [&](int pieces) {  // past the row: some other codes
-        return min(w_row * pieces + (c ^ key(pieces, w_row)), kSRows * kChunkB / 16 - 1) * 16;
+        return min(w_row * pieces + (c ^ key(pieces, w_row)), kSRows * kChunkB / 16 - 1 - 16 * kAlong * (kUnits - 1)) * 16;
       };
       fo_last[i] = offset(plan.last);
       fo[i] = CK > 1 ? offset(plan.pieces) : fo_last[i];
     }
     // this lane's four scale bytes in the area: the two dwords that hold them
     const int sc_shift = (skew + w_row * nb) & 3;
-    int so[CK][2];
+    int so[CK][kUnits][2];
 #pragma unroll
     for (int u = 0; u < CK; u++)
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int at = min(((skew + w_row * nb + u * plan.pieces + mine) & ~3) + 4 * i, kArea - 4);
-        so[u][i] = sc_place(at >> 4) * 16 + (at & 15);
-      }
+      for (int v = 0; v < kUnits; v++)
 #pragma unroll
-    for (int j = 0; j < MT; j++)
+        for (int i = 0; i < 2; i++) {
+          const int at = min(((skew + w_row * nb + u * plan.pieces + mine + 16 * v * kAlong) & ~3) + 4 * i, kArea - 4);
+          so[u][v][i] = sc_place(at >> 4) * 16 + (at & 15);
+        }
 #pragma unroll
-      for (int u = 0; u < CK; u++) dx[j][u] &= u == CK - 1 ? keep_last : keep;
+    for (int j = 0; j < kMT; j++)
+#pragma unroll
+      for (int u = 0; u < CK; u++)
+#pragma unroll
+        for (int v = 0; v < kUnits; v++) dx[j][u][v] &= u == CK - 1 ? keep_last[v] : keep[v];
 
     // this thread's results: rows that padding leaves zero
     bool none[kOuts];
 #pragma unroll
     for (int i = 0; i < kOuts; i++) {
       none[i] = false;
-      const int64_t row = t.m0 + ((tid + i * 64 * kSWaves) % kPart >> 4);
+      const int64_t row = t.m0 + ((tid + i * 64 * kSWaves) % kSums >> 4);
       if (GROUPED && a.x_rows && row < t.m1) {
         const int64_t r = a.x_rows[row];
         none[i] = r < 0 || r >= a.x_rows_total;
@@ -760,11 +780,14 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
 #pragma unroll
       for (int i = 0; i < kOuts; i++) {
         const int o = tid + i * 64 * kSWaves;
-        const int n = o & 15, m = (RT == 1 ? o : o % kPart) >> 4, at_tile = RT == 1 ? 0 : o / kPart;  // lane (n / 4) * 16 + m % 16 holds it in element n % 4
+        const int n = o & 15, m = (RT == 1 ? o : o % kSums) >> 4, at_tile = RT == 1 ? 0 : o / kSums;
+        const int m_x = kX == 1 ? m : m % (16 * kMT);
         const int64_t row = t.m0 + m;
         const int col = tile * kRows + at_tile * kSRows + n;
-        if (o >= RT * kPart || row >= t.m1 || col >= n_rows) continue;
-        const float* p = part + (set * kSWaves + at_tile * kAlong) * kPart + (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+        if (o >= RT * kSums || row >= t.m1 || col >= n_rows) continue;
+        // lane (n / 4) * 16 + m % 16 of a wave holds it in element n % 4
+        const float* p = part + ((set * RT + at_tile) * kX + (kX == 1 ? 0 : m / (16 * kMT))) * kAlong * kPart + (m_x >> 4) * 256 +
+                         ((n >> 2) * 16 + (m_x & 15)) * 4 + (n & 3);
         float v[kAlong];
 #pragma unroll
         for (int w = 0; w < kAlong; w++) v[w] = p[w * kPart];
@@ -783,7 +806,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
-    f32x4_t acc[MT];
+    f32x4_t acc[kMT];
     // position P of a round: chunk P % CK of the row tile, ring place P % kRing;
     // false behind the last row tile
     auto chunk = [&](auto which) {
@@ -795,32 +818,36 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
         load_scales(tile + kScAhead, area(std::integral_constant<int, P / CK + kScAhead>{}));
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < MT; j++) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < kMT; j++) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       }
       load_chunk(tile + ahead / CK, ahead % CK, ring(std::integral_constant<int, P + kRing - 1>{}));
       const uint8_t* l = ring(which);
       const uint8_t* ds = area(std::integral_constant<int, P / CK>{});
-      u32x4_t f[4];
-      uint32_t d[2];
+      auto unit_of = [&](auto which_unit) {
+        constexpr int v = decltype(which_unit)::value;
+        if (v > 0 && 16 * (along + v * kAlong) >= plan.last) return false;  // the row ends before it
+        u32x4_t f[4];
 #pragma unroll
-      for (int i = 0; i < 4; i++) f[i] = *(const u32x4_t*)(l + (ck == CK - 1 ? fo_last[i] : fo[i]));
+        for (int i = 0; i < 4; i++) f[i] = *(const u32x4_t*)(l + (ck == CK - 1 ? fo_last[i] : fo[i]) + v * kAlong * 256);
+        const uint32_t d0 = *(const uint32_t*)(ds + so[ck][v][0]), d1 = *(const uint32_t*)(ds + so[ck][v][1]);
+        const uint32_t dw = __builtin_amdgcn_alignbyte(d1, d0, sc_shift) & (ck == CK - 1 ? keep_last[v] : keep[v]);
 #pragma unroll
-      for (int i = 0; i < 2; i++) d[i] = *(const uint32_t*)(ds + so[ck][i]);
-      const uint32_t dw = __builtin_amdgcn_alignbyte(d[1], d[0], sc_shift) & (ck == CK - 1 ? keep_last : keep);
-#pragma unroll
-      for (int j = 0; j < MT; j++) {
-        acc[j] = mma16<0>(f[0], fx[j][ck][0], acc[j], dw, dx[j][ck]);
-        acc[j] = mma16<1>(f[1], fx[j][ck][1], acc[j], dw, dx[j][ck]);
-        acc[j] = mma16<2>(f[2], fx[j][ck][2], acc[j], dw, dx[j][ck]);
-        acc[j] = mma16<3>(f[3], fx[j][ck][3], acc[j], dw, dx[j][ck]);
-        asm volatile("" : "+v"(acc[j]));  // here, not behind the next barrier with all chunks' operands
-      }
+        for (int j = 0; j < kMT; j++) {
+          acc[j] = mma16<0>(f[0], fx[j][ck][v][0], acc[j], dw, dx[j][ck][v]);
+          acc[j] = mma16<1>(f[1], fx[j][ck][v][1], acc[j], dw, dx[j][ck][v]);
+          acc[j] = mma16<2>(f[2], fx[j][ck][v][2], acc[j], dw, dx[j][ck][v]);
+          acc[j] = mma16<3>(f[3], fx[j][ck][v][3], acc[j], dw, dx[j][ck][v]);
+          asm volatile("" : "+v"(acc[j]));  // here, not behind the next barrier with all chunks' operands
+        }
+        return true;
+      };
+      for_each(unit_of, std::make_integer_sequence<int, kUnits>{});
       if constexpr (kDefer && ck == 0)
         if (tile > 0) finish(tile - 1, (P / CK + kParts - 1) % kParts);
       if constexpr (ck == CK - 1) {
         float* sums = part + (P / CK % kParts * kSWaves + wave) * kPart;
 #pragma unroll
-        for (int j = 0; j < MT; j++) *(f32x4_t*)(sums + j * 256 + lane * 4) = acc[j];
+        for (int j = 0; j < kMT; j++) *(f32x4_t*)(sums + j * 256 + lane * 4) = acc[j];
         if constexpr (!kDefer) {
           meet();
           finish(tile, 0);
