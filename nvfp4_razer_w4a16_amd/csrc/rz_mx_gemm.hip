@@ -153,8 +153,14 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
 // its own loads) and nobody reads this one any more, so the step after next is
 // loaded in its place, half of it under the last product and half under the next
 // step's first (a load takes the CU's address unit 16 cycles; all 64 under one
-// product, 512 cycles, would stall it).  The loads run on into the next tile, so they are under way while this
-// tile's results go through LDS to be stored in whole 128-byte lines.
+// product, 512 cycles, would stall it).  The loads run on into the next tile, so
+// they are under way while this tile's results go through LDS to be stored in whole
+// 128-byte lines.
+//
+// Measured: 2048 x 28672 x 8192 in bf16 262 us (3.7 PFLOP/s, the last of its rounds
+// half full), 8192 cubed 4.4 PFLOP/s; the matrix units are busy 62 % of the time, at a
+// clock that power holds down: on zeros the same code runs at 5.4 PFLOP/s and more,
+// and a loop of products in registers alone at 6.2-6.7 (random codes).
 constexpr int kStepB = 128;   // code bytes of a row and step
 constexpr int kWindow = 16;   // blocks of a window
 
@@ -534,6 +540,10 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // The waves' sums meet in LDS.  Loads past the last row return zero (the buffer
 // descriptor ends there), so no load has a branch around it and a chunk's loads
 // have a fixed number.
+//
+// Bound by the read of W: 27 x 28672 x 8192 24.2 us of kernel (125 MB, 5.2 TB/s; a
+// copy of 1 GiB reaches 5.06), 1 x 14336 x 4096 7.6-7.9 us (31 MB, 4.0 TB/s: a third of
+// it is the ramp of a launch).
 constexpr int kSRows = 16, kSWaves = 8, kChunkB = 2048, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
@@ -1041,12 +1051,12 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 // the read of W come to, one of them half hidden behind the other, and what a launch
 // costs.  The stream kernel's work is its row tiles, whose sums meet in LDS; the tile
 // kernel's its rounds of tiles.  Measured, stream and tile kernel:
-//   128 x 28672 x 8192  41.8 and 46.8    256 x 28672 x 8192   61.1 and 56.3
-//   128 x 14336 x 4096  17.8 and 22.5    256 x 14336 x 4096   26.8 and 22.9
-//   512 x 4096 x 4096   18.8 and 22.1    1024 x 4096 x 4096   29.5 and 22.7
-//   33 x 8192 x 1024     8.3 and  8.3    128 x 8192 x 1024    12.3 and  8.3
-//   256 x 4096 x 14336  27.5 and 25.2    1024 x 4096 x 14336  67.7 and 48.7
-//   8 experts of 14336 x 4096, 64 rows each 73.7 and 70.1, 128 rows 115 and 84
+//   128 x 28672 x 8192  40.5 and 47.1    256 x 28672 x 8192   60.0 and 54.3
+//   128 x 14336 x 4096  16.0 and 22.6    256 x 14336 x 4096   22.6 and 22.9
+//   512 x 4096 x 4096   16.0 and 22.1    1024 x 4096 x 4096   24.5 and 22.7
+//   33 x 8192 x 1024     7.1 and  8.0    128 x 8192 x 1024    10.3 and  8.5
+//   256 x 4096 x 14336  26.3 and 25.2    1024 x 4096 x 14336  66.2 and 48.6
+//   8 experts of 14336 x 4096, 64 rows each 72.7 and 69.8, 128 rows 115 and 85
 bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   p = stream_plan(m, n, k, experts);
   if (!p.ck) return false;
