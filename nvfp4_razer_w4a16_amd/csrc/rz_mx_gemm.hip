@@ -112,20 +112,6 @@ template <int I> __device__ __forceinline__ f32x16_t mma(u32x4_t a, u32x4_t b, f
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
 }
 
-// Stores y[row][n .. n + 3] (those below nn), rounded once.
-template <typename OT>
-__device__ __forceinline__ void store4(OT* y, int64_t row, int64_t n, int64_t nn, const float (&v)[4]) {
-  typedef OT V __attribute__((ext_vector_type(4)));
-  OT* p = y + row * nn + n;
-  if ((nn & 3) == 0 && n + 4 <= nn) {
-    *(V*)p = V{mx_cvt<OT>(v[0]), mx_cvt<OT>(v[1]), mx_cvt<OT>(v[2]), mx_cvt<OT>(v[3])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (n + i < nn) p[i] = mx_cvt<OT>(v[i]);
-  }
-}
-
 // Memory from p on of which loads past `bytes` read zero.
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
