@@ -200,10 +200,12 @@ def _rows_of(x: torch.Tensor, cols: int):
     ld, inner = x.stride()
     if inner == 1 and not (ld * x.element_size() | ptr) & 15 and ld >= cols:
         return x, ptr, ld
+    # A lone row counts as contiguous whatever its stride, and so do copies of it that
+    # keep the stride: below, rows are `cols` apart.
     x = x.contiguous()
     if x.data_ptr() & 15:
         x = x.clone()
-    return x, x.data_ptr(), max(x.stride(0), cols)
+    return x, x.data_ptr(), cols
 
 
 def _same(dev: torch.device, want: torch.device, name: str):
