@@ -23,7 +23,7 @@ from . import _DT, RAZER_OK, RazerError, _check_buffer, lib
 
 # Calls on a few rows take microseconds: the checks below are written to cost
 # little beside a launch.
-_Tensor = torch.Tensor
+_Tensor, _u8 = torch.Tensor, torch.uint8
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -66,12 +66,11 @@ def _check(status: int, what: str):
         raise RazerError(status, what)
 
 
-def _stream(device: torch.device) -> int:
+def _stream(index: int) -> int:
     """The current stream of the tensors' device, which has to be the current
     device: launches go to that one."""
-    index = device.index
     if index != _current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{_current_device()}")
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
     return _raw_stream(index)
 
 
@@ -103,20 +102,22 @@ class MxTensor:
     """An MXFP4 tensor in device memory.
 
     codes: uint8 [rows, cols // 2], the even column in the low half of a byte;
-    scales: uint8 [rows, cols // 32]."""
+    scales: uint8 [rows, cols // 32].  rows, cols and buffers can be replaced; a call
+    refuses a tensor whose buffers do not match its shape."""
 
-    __slots__ = ("rows", "cols", "device", "_buf", "_codes", "_scales", "_valid")
+    # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers it was
+    # given, when their shapes were last looked at
+    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at")
 
     def __init__(self, rows: int, cols: int, device):
         if rows < 0 or cols < 0 or cols % MX_BLOCK:
             raise ValueError(f"cols must be a multiple of {MX_BLOCK}")
-        self.rows = rows
-        self.cols = cols
+        self._rows = rows
+        self._cols = cols
         # one buffer for both: codes, then scales; their views are made when asked for
         self._buf = buf = torch.empty(rows * cols // 32 * 17, dtype=torch.uint8, device=device)
-        self.device = buf.device
+        self._device, self._index = buf.device, buf.get_device()
         self._codes = self._scales = None
-        self._valid = True
 
     @classmethod
     def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "MxTensor":
@@ -127,70 +128,121 @@ class MxTensor:
         if len(shape) != 2:
             codes, scales = codes.view(-1, shape[-1]), scales.view(-1, scales.shape[-1])
             shape = codes.shape
-        rows, half = shape
-        t.rows, t.cols, t._buf, t._codes, t._scales = rows, 2 * half, None, codes, scales
-        t._check_buffers("MxTensor")
+        t._rows, half = shape
+        t._cols, t._buf, t._codes, t._scales = 2 * half, None, codes, scales
+        t._check_buffers("MxTensor", shape)
         return t
+
+    def _detach(self):
+        """From here on the buffers are plain tensors that have to match the shape."""
+        self._codes, self._scales, self._buf, self._at = self.codes, self.scales, None, -1
+
+    @property
+    def rows(self) -> int:
+        return self._rows
+
+    @rows.setter
+    def rows(self, rows: int):
+        self._detach()
+        self._rows = rows
+
+    @property
+    def cols(self) -> int:
+        return self._cols
+
+    @cols.setter
+    def cols(self, cols: int):
+        self._detach()
+        self._cols = cols
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            self._codes = self._buf[:self.rows * self.cols // 2].view(self.rows, self.cols // 2)
+            self._codes = self._buf[:self._rows * self._cols // 2].view(self._rows, self._cols // 2)
         return self._codes
 
     @codes.setter
     def codes(self, t: torch.Tensor):
-        self._scales, self._codes, self._valid, self._buf = self.scales, t, False, None
+        self._detach()
+        self._codes = t
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            self._scales = self._buf[self.rows * self.cols // 2:].view(self.rows, self.cols // MX_BLOCK)
+            self._scales = self._buf[self._rows * self._cols // 2:].view(self._rows, self._cols // MX_BLOCK)
         return self._scales
 
     @scales.setter
     def scales(self, t: torch.Tensor):
-        self._codes, self._scales, self._valid, self._buf = self.codes, t, False, None
+        self._detach()
+        self._scales = t
+
+    @property
+    def device(self) -> torch.device:
+        return self._device if self._buf is not None else self._codes.device
 
     @property
     def shape(self):
-        return (self.rows, self.cols)
+        return (self._rows, self._cols)
 
     def nbytes(self) -> int:
-        return self.rows * self.cols // 32 * 17
+        return self._rows * self._cols // 32 * 17
 
     def check(self, name: str = "MxTensor") -> torch.device:
-        """Its buffers match its shape (buffers it was given are looked at once);
-        returns their device."""
-        if not self._valid:
-            self._check_buffers(name)
-        return self.device
+        """Its buffers match its shape; returns their device."""
+        self._checked(name)
+        return self._device
 
-    def _check_buffers(self, name: str):
-        c, s, rows, cols = self._codes, self._scales, self.rows, self.cols
-        dev, u8 = c.device, torch.uint8
-        if (c.dtype is not u8 or s.dtype is not u8 or cols % MX_BLOCK or s.device != dev
-                or c.shape != (rows, cols // 2) or s.shape != (rows, cols // MX_BLOCK)
+    def _checked(self, name: str) -> razer_mx:
+        """The struct of buffers that match the shape.  The owner of buffers that it
+        was given may have changed them since: every call looks where they are and
+        how long, and at the rest if they have moved."""
+        rows, cols = self._rows, self._cols
+        n = rows * cols >> 1
+        if self._buf is not None:
+            at = self._buf.data_ptr()
+            return razer_mx(rows, cols, at, at + n)
+        c, s = self._codes, self._scales
+        at, scales_at = c.data_ptr(), s.data_ptr()
+        if at != self._at or scales_at != self._scales_at or c.nbytes != n or s.nbytes << 4 != n:
+            self._check_buffers(name)
+        return razer_mx(rows, cols, at, scales_at)
+
+    def _check_buffers(self, name: str, codes_shape=None):
+        c, s, rows, cols = self._codes, self._scales, self._rows, self._cols
+        index = c.get_device()
+        if (c.dtype is not _u8 or s.dtype is not _u8 or cols & 31 or s.get_device() != index
+                or (codes_shape or c.shape) != (rows, cols >> 1) or s.shape != (rows, cols >> 5)
                 or not c.is_contiguous() or not s.is_contiguous()):
-            raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {dev} and scales {tuple(s.shape)} "
+            raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
                              f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
-        self.device = dev
-        self._valid = True
+        self._device, self._index, self._at, self._scales_at = c.device, index, c.data_ptr(), s.data_ptr()
 
     def struct(self) -> razer_mx:
         if self._buf is not None:
             p = self._buf.data_ptr()
-            return razer_mx(self.rows, self.cols, p, p + self.rows * self.cols // 2)
-        return razer_mx(self.rows, self.cols, self._codes.data_ptr(), self._scales.data_ptr())
+            return razer_mx(self._rows, self._cols, p, p + self._rows * self._cols // 2)
+        return razer_mx(self._rows, self._cols, self._codes.data_ptr(), self._scales.data_ptr())
 
 
-def _operand(t, name: str) -> torch.device:
+def _operand(t, name: str) -> razer_mx:
+    """The struct of an operand on a GPU."""
     if not isinstance(t, MxTensor):
         raise TypeError(f"{name} must be an MxTensor")
-    dev = t.device if t._valid else t.check(name)
-    if dev.index is None:  # of a tensor on a GPU it never is
-        raise ValueError(f"{name} must be on a GPU, not {dev}")
-    return dev
+    struct = t._checked(name)
+    if t._index < 0:
+        raise ValueError(f"{name} must be on a GPU, not {t._device}")
+    return struct
+
+
+def _operands(x, w):
+    """Both structs of a product."""
+    xs, ws = _operand(x, "x"), _operand(w, "w")
+    if w._index != x._index:
+        raise ValueError(f"w must be on {x._device}, not {w._device}")
+    if x._cols != w._cols:
+        raise ValueError(f"x has {x._cols} columns, w {w._cols}")
+    return xs, ws
 
 
 def _rows_of(x: torch.Tensor, cols: int):
@@ -208,17 +260,14 @@ def _rows_of(x: torch.Tensor, cols: int):
     return x, x.data_ptr(), cols
 
 
-def _same(dev: torch.device, want: torch.device, name: str):
-    if dev != want:
-        raise ValueError(f"{name} must be on {want}, not {dev}")
-
-
-def _packed_out(out, rows: int, cols: int, device) -> MxTensor:
-    """A caller's output, which has to fit."""
-    _same(_operand(out, "out"), device, "out")
+def _packed_out(out, rows: int, cols: int, device) -> razer_mx:
+    """The struct of a caller's output, which has to fit."""
+    struct = _operand(out, "out")
+    if out._device != device:
+        raise ValueError(f"out must be on {device}, not {out._device}")
     if out.shape != (rows, cols):
         raise ValueError(f"out is {out.rows}x{out.cols}, expected {rows}x{cols}")
-    return out
+    return struct
 
 
 def _encode(call, x, parts: int, out, stream) -> MxTensor:
@@ -233,9 +282,13 @@ def _encode(call, x, parts: int, out, stream) -> MxTensor:
     cols = width // parts
     if width % parts or cols % MX_BLOCK:
         raise ValueError(f"columns must be a multiple of {parts * MX_BLOCK}")
-    out = MxTensor(rows, cols, dev) if out is None else _packed_out(out, rows, cols, dev)
+    if out is None:
+        out = MxTensor(rows, cols, dev)
+        packed = out.struct()
+    else:
+        packed = _packed_out(out, rows, cols, dev)
     x, ptr, ld = _rows_of(x, width)
-    st = call(ptr, dt, ld, out.struct(), _stream(dev))
+    st = call(ptr, dt, ld, packed, _stream(dev.index))
     if st:
         _check(st, call.__name__)
     return out
@@ -256,13 +309,13 @@ def razer_mx_dequant(t: MxTensor, dtype: torch.dtype = torch.float32, out=None, 
     if stream is not None:
         with _entered(stream):
             return razer_mx_dequant(t, dtype, out)
-    dev = _operand(t, "t")
+    packed, dev = _operand(t, "t"), t._device
     if out is None:
-        out = torch.empty(t.rows, t.cols, dtype=dtype, device=dev)
+        out = torch.empty(t._rows, t._cols, dtype=dtype, device=dev)
     else:
-        _check_buffer(out, (t.rows, t.cols), dev, "out")
+        _check_buffer(out, t.shape, dev, "out")
         dtype = out.dtype
-    st = lib().razer_mx_dequant(t.struct(), out.data_ptr(), _dtype(dtype), _stream(dev))
+    st = lib().razer_mx_dequant(packed, out.data_ptr(), _dtype(dtype), _stream(t._index))
     if st:
         _check(st, "razer_mx_dequant")
     return out
@@ -299,13 +352,10 @@ def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloa
     if stream is not None:
         with _entered(stream):
             return razer_mx_gemm(x, w, out_dtype, out, workspace)
-    dev = _operand(x, "x")
-    _same(_operand(w, "w"), dev, "w")
-    if x.cols != w.cols:
-        raise ValueError(f"x has {x.cols} columns, w {w.cols}")
-    current = _stream(dev)
-    out, ws, wsb = _product_buffers(x.rows, w.rows, x.cols, 0, dev, out_dtype, out, workspace)
-    status = lib().razer_mx_gemm(x.struct(), w.struct(), out.data_ptr(), _dtype(out.dtype), ws, wsb, current)
+    xs, ws = _operands(x, w)
+    current = _stream(x._index)
+    out, space, space_bytes = _product_buffers(x._rows, w._rows, x._cols, 0, x._device, out_dtype, out, workspace)
+    status = lib().razer_mx_gemm(xs, ws, out.data_ptr(), _dtype(out.dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_mx_gemm")
     return out
@@ -322,10 +372,8 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
     if stream is not None:
         with _entered(stream):
             return razer_mx_gemm_grouped(x, w, offsets, x_rows, out_dtype, out, workspace)
-    dev = _operand(x, "x")
-    _same(_operand(w, "w"), dev, "w")
-    if x.cols != w.cols:
-        raise ValueError(f"x has {x.cols} columns, w {w.cols}")
+    xs, ws = _operands(x, w)
+    dev = x._device
     if offsets.dim() != 1:
         raise ValueError("offsets must be 1-D")
     _check_buffer(offsets, tuple(offsets.shape), dev, "offsets", torch.int32)
@@ -339,9 +387,9 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
         _check_buffer(x_rows, tuple(x_rows.shape), dev, "x_rows", torch.int32)
         m, rows = x_rows.numel(), x_rows.data_ptr()
     n = w.rows // experts
-    out, ws, wsb = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
-    _check(lib().razer_mx_gemm_grouped(x.struct(), w.struct(), offsets.data_ptr(), experts, rows, m,
-                                       out.data_ptr(), _dtype(out.dtype), ws, wsb, _stream(dev)),
+    out, space, space_bytes = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
+    _check(lib().razer_mx_gemm_grouped(xs, ws, offsets.data_ptr(), experts, rows, m, out.data_ptr(),
+                                       _dtype(out.dtype), space, space_bytes, _stream(x._index)),
            "razer_mx_gemm_grouped")
     return out
 
@@ -401,8 +449,8 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
         _check_buffer(h_out, shape, dev, "h_out", kind)
     x_ptr = p_ptr = None
     if packed:
-        x = MxTensor(rows, cols, dev) if x_out is None else _packed_out(x_out, rows, cols, dev)
-        p_ptr = ctypes.pointer(x.struct())
+        x = MxTensor(rows, cols, dev) if x_out is None else x_out
+        p_ptr = ctypes.pointer(x.struct() if x_out is None else _packed_out(x, rows, cols, dev))
     elif x_out is None:
         x = torch.empty(rows, cols, dtype=kind, device=dev)
         x_ptr = x.data_ptr()
@@ -412,5 +460,5 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
         x_ptr = x.data_ptr()
     a = razer_norm(rows, cols, dt, flags, y_ptr, h_ptr, y_stride, h_stride, post, pre, gates, gate_rows,
                    residual_scale, eps, h_out.data_ptr(), x_ptr, p_ptr)
-    _check(lib().razer_block_norm(a, _stream(dev)), "razer_block_norm")
+    _check(lib().razer_block_norm(a, _stream(dev.index)), "razer_block_norm")
     return h_out, x
