@@ -382,7 +382,8 @@ size_t razer_mx_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts
  * fp32 (x from the unrounded h_out).  Optional parts are NULL. */
 enum { RAZER_NORM_POST = 1u /* y is normalised; without it h_out = h + residual_scale * gate . post_weight . y */ };
 typedef struct razer_norm {
-  int64_t rows;
+  int64_t rows;           /* rows times 64 (cols <= 1024), 256 (cols <= 8192) or 1024 threads are one launch: at
+                             most 2^26 - 4, 2^24 - 1 or 2^22 - 1 rows (RAZER_E_UNSUPPORTED above) */
   int64_t cols;           /* multiple of 32, at most 32768 */
   int32_t dtype;          /* razer_dtype of y, h, the weights, gate, h_out and x_out */
   uint32_t flags;         /* RAZER_NORM_POST */

@@ -171,13 +171,11 @@ template <typename T> hipError_t run(const BlockNorm& b, hipStream_t stream) {
                      (uint32_t*)b.packed.codes,
                      b.packed.scales};
   const int c = a.chunks;
-  if (c <= 64) return go<T, 64, 1>(a, stream);
-  if (c <= 128) return go<T, 64, 2>(a, stream);
-  if (c <= 256) return go<T, 256, 1>(a, stream);
-  if (c <= 512) return go<T, 256, 2>(a, stream);
-  if (c <= 1024) return go<T, 256, 4>(a, stream);
-  if (c <= 2048) return go<T, 1024, 2>(a, stream);
-  return go<T, 1024, 4>(a, stream);
+  switch (block_norm_lanes(b.cols)) {
+    case 64: return c <= 64 ? go<T, 64, 1>(a, stream) : go<T, 64, 2>(a, stream);
+    case 256: return c <= 256 ? go<T, 256, 1>(a, stream) : c <= 512 ? go<T, 256, 2>(a, stream) : go<T, 256, 4>(a, stream);
+    default: return c <= 2048 ? go<T, 1024, 2>(a, stream) : go<T, 1024, 4>(a, stream);
+  }
 }
 
 }  // namespace

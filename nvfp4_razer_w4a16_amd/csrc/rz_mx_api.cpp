@@ -18,7 +18,7 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 bool dtype_ok(int dt) { return dt == RAZER_F32 || dt == RAZER_F16 || dt == RAZER_BF16; }
 int64_t dtype_size(int dt) { return dt == RAZER_F32 ? 4 : 2; }
 
-constexpr int64_t kMaxElems = (int64_t)1 << 34;   // 8 elements a thread, 2^32 threads of a launch
+constexpr int64_t kMaxElems = (int64_t)1 << 34;   // 8 elements a thread, a launch has fewer than 2^32 threads
 constexpr int64_t kMaxGemmRows = (int64_t)1 << 30;
 constexpr int64_t kMaxGemmK = (int64_t)1 << 23;   // the rows of a tile within 32 bits
 constexpr int64_t kMaxNormCols = 32768;           // 1024 threads of at most four 8-element chunks
@@ -136,7 +136,8 @@ razer_status razer_block_norm(const razer_norm* a, void* stream) {
   const void* others[] = {a->post_weight, a->pre_weight, a->gate, a->h_out, a->x_out};
   for (const void* p : others)
     if (!aligned(p, 16)) return RAZER_E_INVALID;
-  if (a->cols > kMaxNormCols || a->rows > INT32_MAX / 4) return RAZER_E_UNSUPPORTED;
+  const int lanes = rz::block_norm_lanes(a->cols), threads = rz::block_norm_threads(a->cols);
+  if (a->cols > kMaxNormCols || a->rows > (int64_t)(UINT32_MAX / threads) * (threads / lanes)) return RAZER_E_UNSUPPORTED;
   rz::BlockNorm b = {};
   b.rows = a->rows;
   b.cols = a->cols;

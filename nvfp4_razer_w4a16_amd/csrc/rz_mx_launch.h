@@ -45,6 +45,10 @@ struct BlockNorm {
   void *h_out, *x_out;       // [rows, cols], either may be NULL
   MxView packed;             // codes NULL: no packed output
 };
+// Lanes that a row of the block norm is spread over.
+inline int block_norm_lanes(int64_t cols) { return cols <= 1024 ? 64 : cols <= 8192 ? 256 : 1024; }
+// Threads of its workgroups: short rows share one.
+inline int block_norm_threads(int64_t cols) { return block_norm_lanes(cols) < 256 ? 256 : block_norm_lanes(cols); }
 hipError_t launch_block_norm(const BlockNorm& b, hipStream_t stream);
 
 int device_cu_count();
