@@ -9,8 +9,8 @@ scale byte each.  Both operands of a product are MxTensors::
     y    = razer_mx_gemm(razer_mx_quantize_gated(gu), down)
 
 Calls run on the current stream; with ``stream`` they run as inside
-``torch.cuda.stream(stream)``, and what they return belongs to that stream.
-The package re-exports every name here.
+``torch.cuda.stream(stream)``, and what they return belongs to that stream.  No
+call has a backward.  The package re-exports every name here.
 """
 from __future__ import annotations
 
@@ -23,7 +23,7 @@ from . import _DT, RAZER_OK, RazerError, _check_buffer, lib
 
 # Calls on a few rows take microseconds: the checks below are written to cost
 # little beside a launch.
-_Tensor, _u8 = torch.Tensor, torch.uint8
+_Tensor, _u8, _grad_enabled = torch.Tensor, torch.uint8, torch.is_grad_enabled
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -394,9 +394,30 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
     return out
 
 
-def _vector(t, cols: int, dtype, device, name: str) -> int:
-    """Address of a weight [cols]."""
-    if not isinstance(t, _Tensor) or t.dtype != dtype or t.device != device or t.shape != (cols,) or not t.is_contiguous():
+class _NoBackward(torch.autograd.Function):
+    """Puts results into the graph of the inputs they came from, where a backward pass raises."""
+
+    @staticmethod
+    def forward(ctx, call, count, *tensors):
+        ctx.call = call
+        ctx.mark_dirty(*tensors[:count])
+        return tensors[:count]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.call} has no backward: call it under torch.no_grad(), or detach its inputs")
+
+
+def _without_backward(call: str, results, inputs):
+    """The results of a call without a backward: those inputs that require a gradient
+    would silently get none, so a backward pass that reaches the results raises."""
+    return _NoBackward.apply(call, len(results), *results, *(t for t in inputs if t is not None))
+
+
+def _vector(t, cols: int, dtype, device, index: int, name: str) -> int:
+    """Address of a weight [cols] on GPU `index`."""
+    if (not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != index or t.shape != (cols,)
+            or not t.is_contiguous()):
         _check_buffer(t, (cols,), device, name, dtype)
     return t.data_ptr()
 
@@ -411,7 +432,8 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     true (by default, where post_weight is given).  gate: [cols] or
     [gate_rows, cols], gate_rows a divisor of rows.  packed: x is an MxTensor, else
     a tensor of h's dtype.  h_out (h itself, if contiguous) and x_out take the
-    results."""
+    results.  There is no backward: one that reaches the results raises.  What is
+    written to h_out and x_out, and a packed x, stands outside any graph."""
     if stream is not None:
         with _entered(stream):
             return razer_block_norm(y, h, post_weight=post_weight, post_norm=post_norm, gate=gate,
@@ -426,9 +448,11 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     kind = h.dtype
     dt = _dtype(kind)
     h, h_ptr, h_stride = _rows_of(h, cols)
+    index = dev.index
     flags, y_ptr, y_stride, post, pre, gates, gate_rows = 0, None, 0, None, None, None, 0
     if y is not None:
-        if _on_gpu(y, "y") != dev or y.shape != shape or y.dtype != kind:
+        _on_gpu(y, "y")
+        if y.get_device() != index or y.shape != shape or y.dtype is not kind:
             raise ValueError(f"y must be {rows}x{cols} of {kind} on {dev}")
         y, y_ptr, y_stride = _rows_of(y, cols)
         if post_norm if post_norm is not None else post_weight is not None:
@@ -436,14 +460,15 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     elif post_weight is not None or gate is not None or post_norm:
         raise ValueError("post_weight, post_norm and gate belong to y")
     if post_weight is not None:
-        post = _vector(post_weight, cols, kind, dev, "post_weight")
+        post = _vector(post_weight, cols, kind, dev, index, "post_weight")
     if pre_weight is not None:
-        pre = _vector(pre_weight, cols, kind, dev, "pre_weight")
+        pre = _vector(pre_weight, cols, kind, dev, index, "pre_weight")
     if gate is not None:
         gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
         _check_buffer(gate, (cols,) if gate.dim() == 1 else (gate_rows, cols), dev, "gate", kind)
         gates = gate.data_ptr()
-    if h_out is None:
+    new_h, new_x = h_out is None, x_out is None and not packed
+    if new_h:
         h_out = torch.empty(rows, cols, dtype=kind, device=dev)
     else:
         _check_buffer(h_out, shape, dev, "h_out", kind)
@@ -460,5 +485,16 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
         x_ptr = x.data_ptr()
     a = razer_norm(rows, cols, dt, flags, y_ptr, h_ptr, y_stride, h_stride, post, pre, gates, gate_rows,
                    residual_scale, eps, h_out.data_ptr(), x_ptr, p_ptr)
-    _check(lib().razer_block_norm(a, _stream(dev.index)), "razer_block_norm")
+    _check(lib().razer_block_norm(a, _stream(index)), "razer_block_norm")
+    if _grad_enabled() and (h.requires_grad or y is not None and y.requires_grad
+                            or post_weight is not None and post_weight.requires_grad
+                            or pre_weight is not None and pre_weight.requires_grad
+                            or gate is not None and gate.requires_grad):
+        inputs = y, h, post_weight, pre_weight, gate
+        if new_h and new_x:
+            return _without_backward("razer_block_norm", (h_out, x), inputs)
+        if new_h:
+            h_out, = _without_backward("razer_block_norm", (h_out,), inputs)
+        elif new_x:
+            x, = _without_backward("razer_block_norm", (x,), inputs)
     return h_out, x
