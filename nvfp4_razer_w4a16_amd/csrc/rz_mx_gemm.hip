@@ -42,10 +42,6 @@ struct Tile {
 // expert l and a running sum over the lanes finds the one that holds t.
 // Offsets outside [0, m] are clamped.
 __device__ __forceinline__ Tile find_tile(const Args& a, int rows, int64_t t) {
-  if (!a.offsets) {
-    const int64_t m0 = t * rows;
-    return {m0, min(m0 + rows, a.m), m0 < a.m ? 0 : -1};
-  }
   const int lane = threadIdx.x & 63;
   const int m = (int)a.m;
   int before = 0;
@@ -119,7 +115,7 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
 }
 
 // ---- tile kernel -------------------------------------------------------------
-// A BN x BM tile of y (BN = 256 rows of W, BM = 256 or 128 of X) per workgroup of four
+// A kTileN x BM tile of y (256 rows of W, BM = 256 or 128 of X) per workgroup of four
 // waves (2x2), each wave (BN/2) x (BM/2) in 32x32 accumulators, 256 elements of K a step; two
 // steps are a "window", whose scale bytes are 16 bytes a row.  As many workgroups
 // as CUs; each walks through the tiles.
@@ -147,6 +143,7 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
 // half full), 8192 cubed 4.4 PFLOP/s; the matrix units are busy 62 % of the time, at a
 // clock that power holds down: on zeros the same code runs at 5.4 PFLOP/s and more,
 // and a loop of products in registers alone at 6.2-6.7 (random codes).
+constexpr int kTileN = 256;
 constexpr int kStepB = 128;   // code bytes of a row and step
 constexpr int kWindow = 16;   // blocks of a window
 
@@ -183,8 +180,9 @@ __device__ __forceinline__ void tile_place(int pos, int mt, int nt, int& im, int
   im = band * 8 + at - in * high;
 }
 
-template <int BN, int BM, typename OT, bool GROUPED>
+template <int BM, typename OT, bool GROUPED>
 __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) {
+  constexpr int BN = kTileN;
   constexpr int NI = BN / 64, MI = BM / 64;      // 32-row fragments of a wave
   constexpr int NL = BN / 32, ML = BM / 32;      // direct loads of a wave and step
   __shared__ __attribute__((aligned(16))) uint8_t s0[(BN + BM) * kStepB], s1[(BN + BM) * kStepB];
@@ -249,7 +247,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
     for (int i = 0; i < NL; i++) ow[i] = (uint32_t)(min((4 * i + wave) * 8 + (lane >> 3), w_rows - 1) * kb);
 #pragma unroll
     for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(xr[i] * kb);
-    psw = a.ws + (w0 + min(tid % BN, w_rows - 1)) * all_nb + b0;
+    psw = a.ws + (w0 + min(tid, w_rows - 1)) * all_nb + b0;
     psx = a.xs + (x0 + xr[ML]) * all_nb + b0;
   };
   // A step's loads go out in two parts, the X rows' behind the W rows'.
@@ -293,7 +291,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
                    __builtin_amdgcn_alignbyte(v[3], v[2], n), __builtin_amdgcn_alignbyte(0u, v[3], n)};
   };
   auto store_window = [&](const Window& v) {
-    if (BN == 256 || tid < BN) *(u32x4_t*)(scl + tid * 16) = moved(v.w, v.skip);
+    *(u32x4_t*)(scl + tid * 16) = moved(v.w, v.skip);
     if (BM == 256 || tid < BM) *(u32x4_t*)(scl + (BN + tid) * 16) = moved(v.x, v.skip);
   };
 
@@ -928,8 +926,9 @@ hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream
 // y of the split tiles: adds the slices' sums, slice by slice.  A thread takes 16
 // sums of one fragment in register order; the half-waves swap so that each lane
 // stores runs of eight columns.
-template <int BN, int BM, typename OT>
+template <int BM, typename OT>
 __global__ __launch_bounds__(256) void mx_fold_kernel(Args a, TilePlan plan) {
+  constexpr int BN = kTileN;
   constexpr int NI = BN / 64, MI = BM / 64;
   typedef OT V8 __attribute__((ext_vector_type(8)));
   const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
@@ -974,7 +973,6 @@ __global__ __launch_bounds__(256) void mx_fold_kernel(Args a, TilePlan plan) {
 //   2048 x 4096 x 14336 82.7 78.3  74.3 -      1024 x 4096 x 4096   29.0  -   22.7  -
 //   512 x 14336 x 4096  29.8   -   24.4 -      1024 x 14336 x 4096  35.7  -   44.2  -
 //   64 experts of 1536 x 2048, 64 rows each 44.3 and (128) 38.4, 128 rows 48.3 and 52.8
-constexpr int kTileN = 256;
 double window_us(int high, bool full) { return high == 256 ? full ? 3.75 : 3.0 : full ? 2.5 : 2.2; }
 double fold_us(int slices, int high) { return 4.0 + slices * high * (0.1 / 256); }
 int windows_of(int64_t k) { return (int)((k + kWindow * kMxBlock - 1) / (kWindow * kMxBlock)); }
@@ -1016,10 +1014,10 @@ size_t tile_ws_bytes(const TilePlan& p) { return (size_t)p.rest * p.split * kTil
 
 template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
   const int grid = min(p.full + p.rest * p.split, device_cu_count());
-  hipLaunchKernelGGL((mx_tile_kernel<kTileN, BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
+  hipLaunchKernelGGL((mx_tile_kernel<BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.rest) return e;
-  hipLaunchKernelGGL((mx_fold_kernel<kTileN, BM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (BM / 64))), dim3(256), 0,
+  hipLaunchKernelGGL((mx_fold_kernel<BM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (BM / 64))), dim3(256), 0,
                      stream, a, p);
   return hipGetLastError();
 }
