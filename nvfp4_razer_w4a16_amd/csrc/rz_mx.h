@@ -83,8 +83,11 @@ template <> struct Chunk<__bf16> {
 // Stores round once, to nearest even.
 template <typename T> __device__ __forceinline__ T mx_cvt(float v) { return (T)v; }
 
-// n / d for n < 2^31 by a multiplication (host-made constants): the quotient of
-// a thread's place by the chunks of a row.
+// n / d for n < 2^31 by a multiplication: the quotient of a thread's place by the
+// chunks of a row.  With s = ceil(log2 d) the multiplier floor(2^32 (2^s - d) / d) + 1
+// is the round-up method of Granlund and Montgomery, "Division by Invariant Integers
+// using Multiplication" (1994); its sum mulhi(n, mul) + n stays within 32 bits for
+// such n.
 struct FastDiv {
   uint32_t d, mul, shift;
 };
