@@ -12,11 +12,13 @@
 // Out of range: rows are clamped to the last one (their results are not
 // stored).  Blocks past K are read from the last block and get scale byte 0 on
 // both sides: every FP4 code is finite, so they add at most 36 * 2^-254 = 0.
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
 #include "rz_mx.h"
 #include "rz_mx_launch.h"
+#include "rz_mx_plan.h"
 
 namespace rz {
 
@@ -143,9 +145,7 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
 // half full), 8192 cubed 4.4 PFLOP/s; the matrix units are busy 62 % of the time, at a
 // clock that power holds down: on zeros the same code runs at 5.4 PFLOP/s and more,
 // and a loop of products in registers alone at 6.2-6.7 (random codes).
-constexpr int kTileN = 256;
 constexpr int kStepB = 128;   // code bytes of a row and step
-constexpr int kWindow = 16;   // blocks of a window
 
 // 16 bytes a lane straight to LDS, lane i's at l + 16 i.  (The buffer form: behind
 // the global one the compiler waits for every load under way.)
@@ -159,16 +159,6 @@ __device__ __forceinline__ void wait_and_meet() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
-
-// How a product is cut: mt x nt tiles (grouped: as many row tiles as there are),
-// the last `rest` of them each in `split` slices of K whose fp32 sums go to slots
-// of `part`.
-struct TilePlan {
-  int high;  // rows of X of a tile
-  int mt, nt;
-  int full, rest, split;
-  float* part;
-};
 
 // Place of tile `pos`: bands of eight row tiles, within a band the row tiles of
 // one column tile side by side, so that what runs at one time shares few rows of
@@ -528,54 +518,19 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // Bound by the read of W: 27 x 28672 x 8192 24.2 us of kernel (125 MB, 5.2 TB/s; a
 // copy of 1 GiB reaches 5.06), 1 x 14336 x 4096 7.6-7.9 us (31 MB, 4.0 TB/s: a third of
 // it is the ramp of a launch).
-constexpr int kSRows = 16, kSWaves = 8, kChunkB = 2048, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
+constexpr int kSWaves = 8, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, I, (int)sa, I, (int)sb);
 }
-
-// How the line of all jobs' row tiles is cut: into pieces as even as can be, or, where
-// that makes none longer by more than loading another job's X takes, two row tiles or
-// so, every job into `per_job` pieces.  (64 experts of 1503 x 2080, 1000 rows: 32.0 us
-// with pieces that cross jobs, 28.9 without.)
-struct Cuts {
-  uint32_t jobs, per_job;  // 0: even pieces of the line
-  uint32_t share, extra;   // the first `extra` pieces are share + 1 tiles
-};
-__host__ __device__ __forceinline__ Cuts cuts_of(uint32_t tiles, uint32_t jobs, uint32_t grid, uint32_t rt) {
-  const uint32_t line = tiles * jobs;
-  Cuts c = {jobs, jobs ? grid / jobs : 0, line / grid, 0};
-  const uint32_t most = c.per_job ? tiles / c.per_job : 0, rest = tiles - most * c.per_job;
-  if (c.per_job && most + (rest ? 1 : 0) <= c.share + 2 * rt) {
-    c.share = most;
-    c.extra = rest;
-  } else {
-    c.per_job = 0;
-    c.extra = line - c.share * grid;
-  }
-  return c;
-}
-
-// The chunks of a row: `ck` of them, each `pieces` 16-byte pieces, the last `last`.
-struct StreamPlan {
-  int ck, mt;  // ck = 0: not covered
-  int rt;      // row tiles of a chunk
-  int rows;    // of a job, at most 16 mt
-  int pieces, last;
-  int mul_pieces, mul_last;  // p / d = p * mul >> 20 for p < 2048
-  int sc_pieces, mul_sc;     // 16-byte pieces of a row's scale bytes, 0 where they are not whole
-  Cuts cuts;                 // of a product without experts
-  int mul_per_job;
-};
 
 // f(0), f(1) .. as compile-time constants, until one of them is false.
 template <typename F, int... I> __device__ __forceinline__ bool for_each(F& f, std::integer_sequence<int, I...>) {
   return (f(std::integral_constant<int, I>{}) && ...);
 }
 
-// Ring places; blocks of K that a row tile's scale area holds.
+// Ring places.
 constexpr int stream_ring(int mt) { return mt == 4 ? 3 : 4; }
-constexpr int stream_blocks(int ck) { return ck == 4 ? 480 : 128 * ck; }
 
 template <int RT, int CK, int MT, bool GROUPED>
 __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int y_dtype, StreamPlan plan) {
@@ -859,45 +814,10 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   }
 }
 
-// The stream kernel's shape for `m` rows, of each of `experts` on average if that is not 0.
-StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
-  StreamPlan p = {};
-  const int64_t kb = k / 2;
-  int ck = 1;
-  while ((int64_t)ck * kChunkB < kb) ck *= 2;
-  if (ck > 4 || kb / 16 > stream_blocks(ck)) return p;  // the scale bytes would not fit LDS
-  // rows a job: X of CK chunks has to fit the registers; experts' rows scatter about the average
-  const int64_t rows = experts ? (m + experts - 1) / experts * 3 / 2 : m;
-  const int most = min(4, 8 / ck);
-  p.mt = min(rows <= 16 ? 1 : rows <= 32 ? 2 : 4, most);
-  p.rows = 16 * p.mt;
-  if (!experts && m > p.rows) {
-    // A power of two of jobs: workgroups that walk through the same piece of W are then
-    // on one XCD and share its L2 (192 x 28672 x 8192 as three jobs 76 us, as four 61).
-    int64_t jobs = 1;
-    while (jobs < 32 && jobs * p.rows < m) jobs *= 2;
-    if (jobs * p.rows >= m) p.rows = (int)((m + jobs - 1) / jobs);
-  }
-  p.ck = ck;
-  // Short rows: several row tiles a chunk, if there is a chunk for every CU.  Not for
-  // jobs of 64 rows, where the sums of a chunk take as long as two smaller ones' (64 x
-  // 28672 x 2048: 15.2 us and, one row tile a chunk, 14.1).
-  const int64_t jobs = experts ? min(experts, m) : (m + p.rows - 1) / p.rows;
-  p.rt = p.mt == 4 ? 1 : kb <= kChunkB / 4 ? 4 : kb <= kChunkB / 2 ? 2 : 1;
-  while (p.rt > 1 && jobs * ((n + kSRows * p.rt - 1) / (kSRows * p.rt)) < device_cu_count()) p.rt /= 2;
-  p.pieces = (int)(((kb + ck - 1) / ck + 63) / 64 * 4);  // whole products' blocks
-  p.last = (int)(kb / 16) - p.pieces * (ck - 1);
-  p.mul_pieces = (1 << 20) / p.pieces + 1;
-  p.mul_last = (1 << 20) / p.last + 1;
-  const int nb = (int)(kb / 16);
-  if (nb % 16 == 0) p.sc_pieces = nb / 16, p.mul_sc = (1 << 20) / p.sc_pieces + 1;
-  return p;
-}
-
 template <int RT, int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, StreamPlan p, hipStream_t stream) {
   const int64_t tiles = (a.n + kSRows - 1) / kSRows, full = (a.m + p.rows - 1) / p.rows;
-  const int64_t jobs = a.offsets ? min(full + a.experts, a.m) : full;
-  const int64_t grid = min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
+  const int64_t jobs = a.offsets ? std::min(full + a.experts, a.m) : full;
+  const int64_t grid = std::min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
   if (!a.offsets) {
     p.cuts = cuts_of((uint32_t)tiles, (uint32_t)jobs, (uint32_t)grid, RT);
     if (p.cuts.per_job) p.mul_per_job = (1 << 20) / (int)p.cuts.per_job + 1;
@@ -966,54 +886,8 @@ __global__ __launch_bounds__(256) void mx_fold_kernel(Args a, TilePlan plan) {
   }
 }
 
-// us that a window of a tile of 256 or 128 rows takes in a full round, and in one that
-// leaves CUs (and power) to spare; what slices cost, their sums written and read.
-// Measured, 256 rows, 256 with K cut, 128 rows, 128 with K cut:
-//   2048 x 28672 x 8192  262 272 325    -      1024 x 4096 x 14336  81.3 52.5 64.2 48.7
-//   2048 x 4096 x 14336 82.7 78.3  74.3 -      1024 x 4096 x 4096   29.0  -   22.7  -
-//   512 x 14336 x 4096  29.8   -   24.4 -      1024 x 14336 x 4096  35.7  -   44.2  -
-//   64 experts of 1536 x 2048, 64 rows each 44.3 and (128) 38.4, 128 rows 48.3 and 52.8
-double window_us(int high, bool full) { return high == 256 ? full ? 3.75 : 3.0 : full ? 2.5 : 2.2; }
-double fold_us(int slices, int high) { return 4.0 + slices * high * (0.1 / 256); }
-int windows_of(int64_t k) { return (int)((k + kWindow * kMxBlock - 1) / (kWindow * kMxBlock)); }
-
-// The tiles of a product, `high` rows each, and its time in us.  The last, partly
-// filled round of tiles is cut along K where that is quicker.
-TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t experts, double& us) {
-  TilePlan p = {};
-  const int cus = device_cu_count(), windows = windows_of(k);
-  p.high = high;
-  p.nt = (int)((n + kTileN - 1) / kTileN);
-  p.mt = (int)((m + high - 1) / high + min(experts, m));
-  p.full = (int)min((int64_t)p.mt * p.nt, (int64_t)INT32_MAX);  // more have no memory for their results
-  p.split = 1;
-  if (experts) {  // of about the same number of rows, whose last tile is half full
-    const int64_t parts = min(experts, m);
-    const double tiles = (double)p.nt * max(parts, m / high + parts / 2), rounds = floor(tiles / cus);
-    us = (rounds * window_us(high, true) + (tiles > rounds * cus ? window_us(high, false) : 0)) * windows;
-    return p;
-  }
-  const int rest = p.full % cus;
-  double best = rest ? windows * window_us(high, false) : 0;
-  for (int s = 2; s <= 8 && rest > 0 && rest * s <= cus && s <= windows; s++) {
-    const double t = (windows + s - 1) / s * window_us(high, false) + fold_us(rest * s, high);
-    if (t < best) best = t, p.split = s;
-  }
-  us = p.full / cus * window_us(high, true) * windows + best;
-  if (p.split > 1) p.rest = rest, p.full -= rest;
-  return p;
-}
-TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts, double& us) {
-  double low_us;
-  const TilePlan p = tiles_of(256, m, n, k, experts, us), low = tiles_of(128, m, n, k, experts, low_us);
-  if (low_us >= us + 1.0) return p;  // the larger tile's results take longer to store
-  us = low_us;
-  return low;
-}
-size_t tile_ws_bytes(const TilePlan& p) { return (size_t)p.rest * p.split * kTileN * p.high * 4; }
-
 template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
-  const int grid = min(p.full + p.rest * p.split, device_cu_count());
+  const int grid = std::min(p.full + p.rest * p.split, device_cu_count());
   hipLaunchKernelGGL((mx_tile_kernel<BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.rest) return e;
@@ -1028,33 +902,6 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
   p.part = (float*)ws;
   if (p.high == 256) return a.offsets ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<256, OT, false>(a, p, stream);
   return a.offsets ? go_tiles<128, OT, true>(a, p, stream) : go_tiles<128, OT, false>(a, p, stream);
-}
-
-// Whether a product runs on the stream kernel: K below a window of the tile kernel, or
-// the shorter time of two estimates, in us.  Both take what the kernel's own work and
-// the read of W come to, one of them half hidden behind the other, and what a launch
-// costs.  The stream kernel's work is its row tiles, whose sums meet in LDS; the tile
-// kernel's its rounds of tiles.  Measured, stream and tile kernel:
-//   128 x 28672 x 8192  40.5 and 47.1    256 x 28672 x 8192   60.0 and 54.3
-//   128 x 14336 x 4096  16.0 and 22.6    256 x 14336 x 4096   22.6 and 22.9
-//   512 x 4096 x 4096   16.0 and 22.1    1024 x 4096 x 4096   24.5 and 22.7
-//   33 x 8192 x 1024     7.1 and  8.0    128 x 8192 x 1024    10.3 and  8.5
-//   256 x 4096 x 14336  26.3 and 25.2    1024 x 4096 x 14336  66.2 and 48.6
-//   8 experts of 14336 x 4096, 64 rows each 72.7 and 69.8, 128 rows 115 and 85
-bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
-  p = stream_plan(m, n, k, experts);
-  if (!p.ck) return false;
-  const int cus = device_cu_count();
-  if (k < kWindow * kMxBlock) return true;
-  const int64_t parts = experts ? min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
-  const double read = (double)parts * n * (k / 2 + k / 32) / 5e6;
-  auto rounds = [&](int64_t units) { return (double)((units + cus - 1) / cus); };
-  auto total = [&](double work, double fixed) { return max(work, read) + min(work, read) / 2 + fixed; };
-  const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows * p.rt - 1) / (kSRows * p.rt))) *
-                        (0.25 * p.mt + 0.3 * p.ck);
-  double tile;
-  tile_plan(m, n, k, experts, tile);
-  return total(stream, 3.0 + 0.4 * p.ck * p.mt) <= total(tile, 4.0);  // X is loaded first
 }
 
 }  // namespace
