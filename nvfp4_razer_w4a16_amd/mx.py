@@ -332,6 +332,8 @@ def _workspace_bytes(m: int, n: int, k: int, device: int) -> int:
 
 
 def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
+    """(out, workspace, its address, its bytes).  The caller keeps the workspace until
+    its launch is enqueued; from then on the stream's order keeps it."""
     if out is None:
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
@@ -339,11 +341,11 @@ def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
     if workspace is None:
         need = razer_mx_workspace_bytes(m, n, k, experts) if experts else _workspace_bytes(m, n, k, dev.index)
         if not need:
-            return out, None, 0
+            return out, None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _check_buffer(workspace, None, dev, "workspace")
-    return out, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return out, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
@@ -354,7 +356,7 @@ def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloa
             return razer_mx_gemm(x, w, out_dtype, out, workspace)
     xs, ws = _operands(x, w)
     current = _stream(x._index)
-    out, space, space_bytes = _product_buffers(x._rows, w._rows, x._cols, 0, x._device, out_dtype, out, workspace)
+    out, workspace, space, space_bytes = _product_buffers(x._rows, w._rows, x._cols, 0, x._device, out_dtype, out, workspace)
     status = lib().razer_mx_gemm(xs, ws, out.data_ptr(), _dtype(out.dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_mx_gemm")
@@ -387,7 +389,7 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
         _check_buffer(x_rows, tuple(x_rows.shape), dev, "x_rows", torch.int32)
         m, rows = x_rows.numel(), x_rows.data_ptr()
     n = w.rows // experts
-    out, space, space_bytes = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
+    out, workspace, space, space_bytes = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
     _check(lib().razer_mx_gemm_grouped(xs, ws, offsets.data_ptr(), experts, rows, m, out.data_ptr(),
                                        _dtype(out.dtype), space, space_bytes, _stream(x._index)),
            "razer_mx_gemm_grouped")
