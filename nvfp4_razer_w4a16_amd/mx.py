@@ -237,8 +237,12 @@ def _operand(t, name: str) -> razer_mx:
 
 def _operands(x, w):
     """Both structs of a product."""
-    xs, ws = _operand(x, "x"), _operand(w, "w")
-    if w._index != x._index:
+    if not (isinstance(x, MxTensor) and isinstance(w, MxTensor)):
+        raise TypeError("x and w must be MxTensors")
+    xs, ws, index = x._checked("x"), w._checked("w"), x._index
+    if index < 0:
+        raise ValueError(f"x must be on a GPU, not {x._device}")
+    if w._index != index:
         raise ValueError(f"w must be on {x._device}, not {w._device}")
     if x._cols != w._cols:
         raise ValueError(f"x has {x._cols} columns, w {w._cols}")
@@ -331,21 +335,16 @@ def _workspace_bytes(m: int, n: int, k: int, device: int) -> int:
     return razer_mx_workspace_bytes(m, n, k)
 
 
-def _product_buffers(m, n, k, experts, dev, out_dtype, out, workspace):
-    """(out, workspace, its address, its bytes).  The caller keeps the workspace until
-    its launch is enqueued; from then on the stream's order keeps it."""
-    if out is None:
-        out = torch.empty(m, n, dtype=out_dtype, device=dev)
-    else:
-        _check_buffer(out, (m, n), dev, "out")
-    if workspace is None:
-        need = razer_mx_workspace_bytes(m, n, k, experts) if experts else _workspace_bytes(m, n, k, dev.index)
-        if not need:
-            return out, None, None, 0
+def _space(need: int, workspace, dev):
+    """(workspace, its address, its bytes): the caller's, or one of `need` bytes.  It is
+    kept until the launch is enqueued; from then on the stream's order keeps it."""
+    if workspace is not None:
+        _check_buffer(workspace, None, dev, "workspace")
+    elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
-        _check_buffer(workspace, None, dev, "workspace")
-    return out, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        return None, None, 0
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
@@ -355,8 +354,15 @@ def razer_mx_gemm(x: MxTensor, w: MxTensor, out_dtype: torch.dtype = torch.bfloa
         with _entered(stream):
             return razer_mx_gemm(x, w, out_dtype, out, workspace)
     xs, ws = _operands(x, w)
-    current = _stream(x._index)
-    out, workspace, space, space_bytes = _product_buffers(x._rows, w._rows, x._cols, 0, x._device, out_dtype, out, workspace)
+    m, n, dev, index, space, space_bytes = x._rows, w._rows, x._device, x._index, None, 0
+    current = _stream(index)
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype, device=dev)
+    else:
+        _check_buffer(out, (m, n), dev, "out")
+    need = _workspace_bytes(m, n, x._cols, index)
+    if need or workspace is not None:
+        workspace, space, space_bytes = _space(need, workspace, dev)
     status = lib().razer_mx_gemm(xs, ws, out.data_ptr(), _dtype(out.dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_mx_gemm")
@@ -389,7 +395,12 @@ def razer_mx_gemm_grouped(x: MxTensor, w: MxTensor, offsets: torch.Tensor, x_row
         _check_buffer(x_rows, tuple(x_rows.shape), dev, "x_rows", torch.int32)
         m, rows = x_rows.numel(), x_rows.data_ptr()
     n = w.rows // experts
-    out, workspace, space, space_bytes = _product_buffers(m, n, x.cols, experts, dev, out_dtype, out, workspace)
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype, device=dev)
+    else:
+        _check_buffer(out, (m, n), dev, "out")
+    need = 0 if workspace is not None else razer_mx_workspace_bytes(m, n, x.cols, experts)
+    workspace, space, space_bytes = _space(need, workspace, dev)
     _check(lib().razer_mx_gemm_grouped(xs, ws, offsets.data_ptr(), experts, rows, m, out.data_ptr(),
                                        _dtype(out.dtype), space, space_bytes, _stream(x._index)),
            "razer_mx_gemm_grouped")
@@ -453,8 +464,7 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     index = dev.index
     flags, y_ptr, y_stride, post, pre, gates, gate_rows = 0, None, 0, None, None, None, 0
     if y is not None:
-        _on_gpu(y, "y")
-        if y.get_device() != index or y.shape != shape or y.dtype is not kind:
+        if not isinstance(y, _Tensor) or y.get_device() != index or y.shape != shape or y.dtype is not kind:
             raise ValueError(f"y must be {rows}x{cols} of {kind} on {dev}")
         y, y_ptr, y_stride = _rows_of(y, cols)
         if post_norm if post_norm is not None else post_weight is not None:
@@ -487,7 +497,9 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
         x_ptr = x.data_ptr()
     a = razer_norm(rows, cols, dt, flags, y_ptr, h_ptr, y_stride, h_stride, post, pre, gates, gate_rows,
                    residual_scale, eps, h_out.data_ptr(), x_ptr, p_ptr)
-    _check(lib().razer_block_norm(a, _stream(index)), "razer_block_norm")
+    status = lib().razer_block_norm(a, _stream(index))
+    if status:
+        _check(status, "razer_block_norm")
     if _grad_enabled() and (h.requires_grad or y is not None and y.requires_grad
                             or post_weight is not None and post_weight.requires_grad
                             or pre_weight is not None and pre_weight.requires_grad
