@@ -335,8 +335,9 @@ razer_status razer_mx_quantize(const void* x, razer_dtype x_dt, int64_t x_stride
 razer_status razer_mx_quantize_gated(const void* gu, razer_dtype gu_dt, int64_t gu_stride, const razer_mx* out,
                                      void* stream);
 
-/* Decode to out[rows, cols]: value(code) * 2^(byte - 127), exact in fp32; F16
- * and BF16 round it to nearest even. */
+/* Decode to out[rows, cols]: value(code) * 2^(byte - 127), exact in fp32 (infinity
+ * above its range, which no encoded block reaches); F16 and BF16 round it to
+ * nearest even. */
 razer_status razer_mx_dequant(const razer_mx* t, void* out, razer_dtype out_dt, void* stream);
 
 /* y[M, N] = x[M, K] * w[N, K]^T of two MXFP4 tensors, M from one token up; fp32
@@ -379,7 +380,8 @@ size_t razer_mx_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts
  *   x_out = N(h_out; pre_weight)            N(v; w) = w * v / sqrt(mean(v^2) + eps)
  *
  * with fp32 arithmetic; h_out, x_out and the packed x are each rounded once from
- * fp32 (x from the unrounded h_out).  Optional parts are NULL. */
+ * fp32 (x from the unrounded h_out).  Optional parts are NULL, others 16-byte
+ * aligned. */
 enum { RAZER_NORM_POST = 1u /* y is normalised; without it h_out = h + residual_scale * gate . post_weight . y */ };
 typedef struct razer_norm {
   int64_t rows;           /* rows times 64 (cols <= 1024), 256 (cols <= 8192) or 1024 threads are one launch: at

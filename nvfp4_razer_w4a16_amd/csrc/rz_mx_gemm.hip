@@ -141,10 +141,13 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
 // they are under way while this tile's results go through LDS to be stored in whole
 // 128-byte lines.
 //
-// Measured: 2048 x 28672 x 8192 in bf16 262 us (3.7 PFLOP/s, the last of its rounds
-// half full), 8192 cubed 4.4 PFLOP/s; the matrix units are busy 62 % of the time, at a
-// clock that power holds down: on zeros the same code runs at 5.4 PFLOP/s and more,
-// and a loop of products in registers alone at 6.2-6.7 (random codes).
+// Measured: 2048 x 28672 x 8192 in bf16 262-277 us (3.5-3.7 PFLOP/s, the last of its
+// rounds half full), 8192 cubed 4.0-4.4 PFLOP/s; a loop of products in registers alone
+// runs at 6.2-6.7 (random codes).  Bound by its schedule, then by power: on zeros,
+// which power does not hold down, it reaches 5.0-5.4 and that loop 9.7, and the matrix
+// units are busy 62 % of the time.  Half of a step's loads go out under its first
+// product and have the next two, some 0.7 us, to arrive; one wave a SIMD has nothing
+// else to run while it waits for them.
 constexpr int kStepB = 128;   // code bytes of a row and step
 
 // 16 bytes a lane straight to LDS, lane i's at l + 16 i.  (The buffer form: behind
@@ -515,9 +518,10 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
 // descriptor ends there), so no load has a branch around it and a chunk's loads
 // have a fixed number.
 //
-// Bound by the read of W: 27 x 28672 x 8192 24.2 us of kernel (125 MB, 5.2 TB/s; a
-// copy of 1 GiB reaches 5.06), 1 x 14336 x 4096 7.6-7.9 us (31 MB, 4.0 TB/s: a third of
-// it is the ramp of a launch).
+// Bound by the read of W: 27 x 28672 x 8192 28.6-30.1 us (125 MB, 4.2-4.4 TB/s; a copy
+// of 1 GiB reaches 5.06), 1 x 14336 x 4096 8.3-8.5 us (31 MB, 3.7 TB/s: a third of it is
+// the ramp of a launch).  With one or two such weights in turn, which the 256 MB behind
+// the L2 caches hold, 24.2-24.6 and 7.4-7.9.
 constexpr int kSWaves = 8, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
 
 template <int I> __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {

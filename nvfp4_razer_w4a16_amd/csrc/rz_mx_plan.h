@@ -120,7 +120,10 @@ inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) 
   const int64_t kb = k / 2;
   int ck = 1;
   while ((int64_t)ck * kChunkB < kb) ck *= 2;
-  if (ck > 4 || kb / 16 > stream_blocks(ck)) return p;  // the scale bytes would not fit LDS
+  // Above 15360 elements a row's scale bytes would not fit LDS: the tile kernel takes such
+  // products, cut along K where they have no experts (1 x 8192 x 15360 12.9 us, x 16384
+  // 27.7, x 28672 40.2; 16 rows through 8 experts of 4096 x 14336 48.8, x 16384 100).
+  if (ck > 4 || kb / 16 > stream_blocks(ck)) return p;
   // rows a job: X of CK chunks has to fit the registers; experts' rows scatter about the average
   const int64_t rows = experts ? (m + experts - 1) / experts * 3 / 2 : m;
   const int most = std::min(4, 8 / ck);
@@ -149,8 +152,10 @@ inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) 
   return p;
 }
 
-// Whether a product runs on the stream kernel: K below a window of the tile kernel, or
-// the shorter time of two estimates, in us.  Both take what the kernel's own work and
+// Whether a product runs on the stream kernel: K below a window of the tile kernel, which
+// reads scale bytes a window at a time, whatever M is (2048 x 28672 x 480 215 us, x 512 on
+// tiles 44.5; 256 x 14336 x 480 17.9, x 512 7.9), or the shorter time of two estimates, in
+// us.  Both take what the kernel's own work and
 // the read of W come to, one of them half hidden behind the other, and what a launch
 // costs.  The stream kernel's work is its row tiles, whose sums meet in LDS; the tile
 // kernel's its rounds of tiles.  Whole us are compared: of 24 products that fractions
@@ -162,6 +167,7 @@ inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) 
 //   33 x 8192 x 1024     7.1 and  8.0    128 x 8192 x 1024    10.3 and  8.5
 //   256 x 4096 x 14336  26.3 and 25.2    1024 x 4096 x 14336  66.2 and 48.6
 //   8 experts of 14336 x 4096, 64 rows each 72.7 and 69.8, 128 rows 115 and 85
+// One of them is misjudged: 256 x 4096 x 14336 streams.
 inline bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   p = stream_plan(m, n, k, experts);
   if (!p.ck) return false;
