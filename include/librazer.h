@@ -406,6 +406,139 @@ typedef struct razer_norm {
 } razer_norm;
 razer_status razer_block_norm(const razer_norm* a, void* stream);
 
+/* ---- 8-bit integer tensors -------------------------------------------------------
+ *
+ * THE FORMAT.  X[rows, cols], row-major, cols % 16 == 0, is held as whole numbers
+ * with one fp32 scale a row: a scale for each token of an activation, for each
+ * output channel of a weight.
+ *
+ *   scale_r = amax_r / 127                     amax_r = max |x_rc|
+ *   code_rc = x_rc * (127 / amax_r), rounded to nearest even (from -127 to 127)
+ *
+ * in fp32, one rounding an operation (rows with amax_r < 2^-64 are scaled by 2^64
+ * on the way, which keeps the quotient finite).  A row of zeros has scale 0 and
+ * codes 0; a row with an infinity or NaN has scale NaN and codes 0: all its values,
+ * and every product they enter, are NaN. */
+typedef struct razer_i8 {
+  int64_t rows;  /* >= 0 */
+  int64_t cols;  /* >= 0, multiple of 16 */
+  int8_t* codes; /* device, rows*cols bytes, 16-byte aligned */
+  float* scales; /* device, rows */
+} razer_i8;
+
+/* Encode x[out->rows, out->cols] (F32, F16 or BF16; x_stride elements from row to
+ * row, a multiple of 16 bytes).  No workspace.  At most 2^34 elements
+ * (RAZER_E_UNSUPPORTED above). */
+razer_status razer_i8_quantize(const void* x, razer_dtype x_dt, int64_t x_stride, const razer_i8* out,
+                               void* stream);
+
+/* Encode silu(g) * u = g * u / (1 + exp(-g)) as razer_mx_quantize_gated does: gu is
+ * [out->rows, 2 * out->cols] = [g | u]; the fp32 product is encoded directly. */
+razer_status razer_i8_quantize_gated(const void* gu, razer_dtype gu_dt, int64_t gu_stride, const razer_i8* out,
+                                     void* stream);
+
+/* Decode to out[rows, cols] = code * scale: one rounding in fp32, and one more to
+ * F16 or BF16.  out: 16-byte aligned. */
+razer_status razer_i8_dequant(const razer_i8* t, void* out, razer_dtype out_dt, void* stream);
+
+/* y[m, n] = sx[m] * sw[n] * sum_k x[m, k] * w[n, k], M from one token up.  The sum is
+ * exact (32-bit integers), is rounded to fp32 and multiplied by sx, then sw; y_dt
+ * takes one more rounding.  K == 0, K > RAZER_I8_MAX_K (codes of -128, which the
+ * encoder does not write, are summed exactly too) and M or N > 2^30 are
+ * RAZER_E_UNSUPPORTED.  y: 16-byte aligned, not in memory that x or w hold.  ws: at
+ * least razer_i8_workspace_bytes(M, N, K, 0) bytes, 16-byte aligned (may be 0 -> NULL);
+ * launches that can overlap need one each. */
+#define RAZER_I8_MAX_K 131056
+razer_status razer_i8_gemm(const razer_i8* x, const razer_i8* w, void* y, razer_dtype y_dt, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* The products of a mixture of experts, as razer_mx_gemm_grouped takes them: w stacks
+ * `experts` (at most RAZER_MX_MAX_EXPERTS) weights [N, K]; rows offsets[e] ..
+ * offsets[e + 1] - 1 of y[M, N] are x[x_rows[r]] * w_e^T (x[r] where x_rows is NULL:
+ * M = x->rows).  offsets (experts + 1 ascending row numbers) and x_rows (M) stay on
+ * the device.  Rows of y outside every run are left as they were; a row number outside
+ * x makes its row zero; offsets outside [0, M] are clamped.  With x_rows the codes of x
+ * are less than 4 GiB (RAZER_E_UNSUPPORTED).  ws: razer_i8_workspace_bytes(M, N, K,
+ * experts) bytes, 16-byte aligned. */
+razer_status razer_i8_gemm_grouped(const razer_i8* x, const razer_i8* w, const int32_t* offsets, int64_t experts,
+                                   const int32_t* x_rows, int64_t m, void* y, razer_dtype y_dt, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Workspace bytes of a product (experts = 0) or of a grouped one (n: columns of
+ * one expert).  Depends on the current device's compute-unit count. */
+size_t razer_i8_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts);
+
+/* ---- mixture of experts: from router logits to the products, and back ------------
+ *
+ * For each token the `top` experts with the best scores, their weights, and the order
+ * of rows that razer_i8_gemm_grouped and razer_mx_gemm_grouped take:
+ *
+ *   s = softmax(logits) or sigmoid(logits)          c = s + bias
+ *   groups > 1: the experts are `groups` equal runs; a group's score is the sum of its
+ *               group_best largest c; the groups_kept best groups stay
+ *   chosen: the `top` largest c of what stays, the best first
+ *   weights = scale * s (RAZER_ROUTE_RENORM: s / sum of the chosen s)
+ *
+ * Equal values go to the lowest index, of groups too.  Scores and choices are worked
+ * out in fp64 (experts' scores lie close together: fp32 would now and then choose
+ * another), weights are rounded to fp32 once.
+ *
+ * Logits of -inf, and experts with a bias of -inf or NaN, are never chosen.  Where
+ * fewer than `top` experts can be, the rest of a token's places are expert -1, weight
+ * 0, slot -1 (a padding token has all its logits -inf).  A token with a NaN or +inf
+ * logit has experts -1 and weights NaN.
+ *
+ * offsets, rows and slots (all given, or all NULL) order the pairs (token, place) by
+ * expert, then token: expert e has rows offsets[e] .. offsets[e + 1] - 1 of the grouped
+ * products, rows[r] is the token of row r (-1 behind the last one), and slots[t, j] the
+ * row of token t's place j.  The order is the same from call to call. */
+#define RAZER_MOE_MAX_EXPERTS 1024
+#define RAZER_MOE_MAX_TOP 32
+#define RAZER_MOE_MAX_GROUPS 64
+enum { RAZER_SCORE_SOFTMAX = 0, RAZER_SCORE_SIGMOID = 1 };
+enum { RAZER_ROUTE_RENORM = 1u };
+typedef struct razer_route {
+  int64_t tokens;      /* >= 0; tokens * top < 2^30 */
+  int64_t stride;      /* elements from row to row of logits, >= experts */
+  int32_t experts;     /* 1 .. RAZER_MOE_MAX_EXPERTS (RAZER_E_UNSUPPORTED above) */
+  int32_t top;         /* 1 .. RAZER_MOE_MAX_TOP, at most the experts of the groups kept */
+  int32_t groups;      /* 1 .. RAZER_MOE_MAX_GROUPS, divides experts */
+  int32_t groups_kept; /* 1 .. groups */
+  int32_t group_best;  /* 1 or 2 */
+  int32_t score;       /* RAZER_SCORE_* */
+  int32_t dtype;       /* razer_dtype of logits */
+  uint32_t flags;      /* RAZER_ROUTE_RENORM */
+  float scale;
+  const void* logits;  /* device [tokens, experts] */
+  const float* bias;   /* device [experts]; NULL: none */
+  int32_t* chosen;     /* device [tokens, top] */
+  float* weights;      /* device [tokens, top] */
+  int32_t* offsets;    /* device [experts + 1] */
+  int32_t* rows;       /* device [tokens * top] */
+  int32_t* slots;      /* device [tokens, top] */
+} razer_route;
+/* ws: razer_moe_workspace_bytes(tokens, experts, top) bytes, 16-byte aligned (0 without
+ * offsets, rows and slots); launches that can overlap need one each. */
+razer_status razer_moe_route(const razer_route* a, void* ws, size_t ws_bytes, void* stream);
+size_t razer_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top);
+
+/* The experts' rows, joined again: out[t] = add[t] + sum_j weights[t, j] * y[slots[t, j]],
+ * in fp32 in the order of j, rounded once.  A slot outside [0, y_rows) stands for a row
+ * of zeros. */
+typedef struct razer_combine {
+  int64_t tokens, top, cols; /* top: 1 .. RAZER_MOE_MAX_TOP */
+  int64_t y_rows;
+  int64_t y_stride;          /* elements from row to row */
+  int64_t add_stride;
+  int32_t dtype;             /* razer_dtype of y, add and out */
+  const void* y;             /* device [y_rows, cols] */
+  const int32_t* slots;      /* device [tokens, top] */
+  const float* weights;      /* device [tokens, top] */
+  const void* add;           /* device [tokens, cols], such as the residual or a shared expert's output; NULL: zeros */
+  void* out;                 /* device [tokens, cols]; may be add (if its rows are contiguous) */
+} razer_combine;
+razer_status razer_moe_combine(const razer_combine* a, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* razer_status_string(razer_status s);
 

@@ -9,8 +9,9 @@ no fallback path.
 Functions carry the C names: ``razer_quantize_weight``, ``razer_quantize_act``,
 ``razer_dequant``, ``razer_gemv``, ``razer_gemm``, ``razer_gemm_w4a4``, ``razer_weight_offset_sse``,
 ``razer_workspace_bytes``, ``razer_status_string``; the microscaled 4-bit (MXFP4)
-operators and the block norm, ``razer_mx_*`` and ``razer_block_norm``, are in ``mx``
-and re-exported here.
+operators and the block norm, ``razer_mx_*`` and ``razer_block_norm``, are in ``mx``,
+the 8-bit integer operators, ``razer_i8_*``, in ``i8``, the routing to experts and the
+combination of their rows, ``razer_moe_*``, in ``moe``; all are re-exported here.
 """
 from __future__ import annotations
 
@@ -35,7 +36,9 @@ SECOND_PAIR_OFFSETS = tuple(range(-7, 8))  # entry i of razer_weight_offset_sse 
 EXPORTED = ("razer_quantize_weight", "razer_quantize_act", "razer_quantize_act_noalloc", "razer_dequant", "razer_gemv",
             "razer_gemv_group", "razer_gemm", "razer_gemm_w4a4", "razer_weight_offset_sse", "razer_workspace_bytes",
             "razer_status_string", "razer_mx_quantize", "razer_mx_quantize_gated", "razer_mx_dequant", "razer_mx_gemm",
-            "razer_mx_gemm_grouped", "razer_mx_workspace_bytes", "razer_block_norm")
+            "razer_mx_gemm_grouped", "razer_mx_workspace_bytes", "razer_block_norm", "razer_i8_quantize",
+            "razer_i8_quantize_gated", "razer_i8_dequant", "razer_i8_gemm", "razer_i8_gemm_grouped",
+            "razer_i8_workspace_bytes", "razer_moe_route", "razer_moe_workspace_bytes", "razer_moe_combine")
 
 DEFAULT_WEIGHT_OFFSETS = (-2, 4)  # special values +/-5 and +/-8
 DEFAULT_ACT_OFFSETS = (-2,)       # special values +/-5
@@ -87,6 +90,8 @@ def lib() -> ctypes.CDLL:
         L.razer_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.razer_status_string.restype, L.razer_status_string.argtypes = ctypes.c_char_p, [i32]
         mx.bind(L)
+        i8.bind(L)
+        moe.bind(L)
         _lib = L
     return _lib
 
@@ -456,3 +461,8 @@ from . import mx  # noqa: E402  (binds to the names above)
 from .mx import (MX_BLOCK, RAZER_MX_MAX_EXPERTS, RAZER_NORM_POST, MxTensor, razer_block_norm,  # noqa: E402
                  razer_mx_dequant, razer_mx_gemm, razer_mx_gemm_grouped, razer_mx_quantize,
                  razer_mx_quantize_gated, razer_mx_workspace_bytes)
+from . import i8, moe  # noqa: E402
+from .i8 import (I8_UNIT, RAZER_I8_MAX_K, I8Tensor, razer_i8_dequant, razer_i8_gemm, razer_i8_gemm_grouped,  # noqa: E402
+                 razer_i8_quantize, razer_i8_quantize_gated, razer_i8_workspace_bytes)
+from .moe import (RAZER_MOE_MAX_EXPERTS, RAZER_MOE_MAX_GROUPS, RAZER_MOE_MAX_TOP, MoeRoutes,  # noqa: E402
+                  razer_moe_combine, razer_moe_route, razer_moe_workspace_bytes)

@@ -40,6 +40,10 @@ SOURCES = {
     "rz_mx_gemm.hip": [],
     "rz_block_norm.hip": [],
     "rz_mx_api.cpp": [],
+    "rz_i8_encode.hip": EXACT,
+    "rz_i8_gemm.hip": EXACT,
+    "rz_moe.hip": [],
+    "rz_i8_api.cpp": [],
     "rz_api.cpp": [],
 }
 

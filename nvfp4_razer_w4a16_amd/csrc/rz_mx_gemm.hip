@@ -16,6 +16,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "rz_groups.h"
 #include "rz_mx.h"
 #include "rz_mx_launch.h"
 #include "rz_mx_plan.h"
@@ -32,61 +33,6 @@ struct Args {
   const int32_t* x_rows;
   int experts;
 };
-
-// The rows [m0, m1) of one expert's tile.
-struct Tile {
-  int64_t m0, m1;
-  int expert;  // -1: no such tile
-};
-
-// Tile t of the grouped product's row tiles, each `rows` high and within one
-// expert's run.  Every wave works it out for itself: lane l counts the tiles of
-// expert l and a running sum over the lanes finds the one that holds t.
-// Offsets outside [0, m] are clamped.
-__device__ __forceinline__ Tile find_tile(const Args& a, int rows, int64_t t) {
-  const int lane = threadIdx.x & 63;
-  const int m = (int)a.m;
-  int before = 0;
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < a.experts) {
-      lo = min(max(a.offsets[e], 0), m);
-      hi = min(max(a.offsets[e + 1], lo), m);
-    }
-    const int cnt = (hi - lo + rows - 1) / rows;
-    int sum = cnt;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += up;
-    }
-    sum += before;
-    const uint64_t hit = __ballot(sum > t);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);
-      const int first = __builtin_amdgcn_readlane(sum - cnt, src);
-      const int l = __builtin_amdgcn_readlane(lo, src), h = __builtin_amdgcn_readlane(hi, src);
-      const int m0 = l + (int)(t - first) * rows;
-      return {m0, min(m0 + rows, h), e0 + src};
-    }
-    before = __builtin_amdgcn_readlane(sum, 63);
-  }
-  return {0, 0, -1};
-}
-
-// Number of row tiles, each `rows` high, of the grouped product.
-__device__ __forceinline__ int live_tiles(const Args& a, int rows) {
-  const int lane = threadIdx.x & 63, m = (int)a.m;
-  int cnt = 0;
-  for (int e = lane; e < a.experts; e += 64) {
-    const int lo = min(max(a.offsets[e], 0), m), hi = min(max(a.offsets[e + 1], lo), m);
-    cnt += (hi - lo + rows - 1) / rows;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) cnt += __shfl_xor(cnt, o, 64);
-  return __builtin_amdgcn_readfirstlane(cnt);
-}
 
 // The scale bytes of blocks b .. b + 3 of a row of nb blocks, 0 past its end.
 __device__ __forceinline__ uint32_t scales4(const uint8_t* row, int b, int nb) {
@@ -194,7 +140,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
   Rsrc wc, xc;
   const uint8_t *psw, *psx;
   uint32_t ow[NL], ox[ML];                       // direct load i of this lane: bytes from wc, xc
-  const int mt = GROUPED ? live_tiles(a, BM) : plan.mt;
+  const int mt = GROUPED ? live_tiles(a.offsets, a.experts, a.m, BM) : plan.mt;
   const int full = GROUPED ? mt * plan.nt : plan.full;
   const int items = full + plan.rest * plan.split;
   // Consecutive workgroups go to the eight XCDs in turn: of every round of tiles
@@ -216,7 +162,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(Args a, TilePlan plan) 
     }
     tile_place(pos, mt, plan.nt, im, in);
     if (GROUPED)
-      t = find_tile(a, BM, im);
+      t = find_tile(a.offsets, a.experts, a.m, BM, im);
     else
       t = Tile{(int64_t)im * BM, min((int64_t)(im + 1) * BM, a.m), 0};
     n0 = (int64_t)in * BN;
@@ -602,7 +548,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   // this workgroup's piece of the line
   const uint32_t b = blockIdx.x;
   Cuts c = plan.cuts;
-  if (GROUPED) c = cuts_of((uint32_t)units, (uint32_t)live_tiles(a, plan.rows), gridDim.x, RT);
+  if (GROUPED) c = cuts_of((uint32_t)units, (uint32_t)live_tiles(a.offsets, a.experts, a.m, plan.rows), gridDim.x, RT);
   int job, unit, left;
   if (c.per_job) {
     job = GROUPED ? (int)(b / c.per_job) : quotient((int)b, plan.mul_per_job);
@@ -618,7 +564,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void mx_stream_kernel(Args a, int 
   for (; left > 0; job++, unit = 0) {
     Tile t;
     if (GROUPED)
-      t = find_tile(a, plan.rows, job);
+      t = find_tile(a.offsets, a.experts, a.m, plan.rows, job);
     else
       t = Tile{(int64_t)job * plan.rows, min((int64_t)(job + 1) * plan.rows, a.m), 0};
     if (GROUPED && t.expert < 0) return;
