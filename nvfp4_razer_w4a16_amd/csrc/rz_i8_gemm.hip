@@ -7,13 +7,16 @@
 // are stored, 16 bytes of a row a lane; the order of K within a product is free as long
 // as both agree.
 //
-// Out of range: rows are clamped to the last one (their results are not stored); pieces
-// past K read as zeros.
+// Out of range: rows are clamped to the last one (their results are not stored).  Pieces
+// of W past K read as zeros, so that whatever is read of X there adds nothing.
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "rz_groups.h"
 #include "rz_i8.h"
 #include "rz_i8_launch.h"
+#include "rz_i8_plan.h"
 
 namespace rz {
 
@@ -29,64 +32,404 @@ struct Args {
   int experts;
 };
 
-// A 64x64 tile of y per workgroup of four waves, a 32x32 quarter each.
-template <typename OT, bool GROUPED> __device__ void i8_tile(const Args& a, int64_t im, int64_t in) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, l32 = lane & 31;
-  Tile t = {im * 64, min(im * 64 + 64, a.m), 0};
-  if (GROUPED) t = find_tile(a.offsets, a.experts, a.m, 64, im);
-  if (t.expert < 0) return;
-  const int64_t n0 = in * 64 + (wave & 1) * 32, m = t.m0 + (wave >> 1) * 32 + l32;
-  if (n0 >= a.n) return;
-  const int64_t wr = t.expert * a.n + min(n0 + l32, a.n - 1);
-  int64_t xr = min(m, t.m1 - 1);
-  bool none = false;
-  if (GROUPED && a.x_rows) {
-    xr = a.x_rows[xr];
-    none = xr < 0 || xr >= a.x_rows_total;
-    if (none) xr = 0;
-  }
-  const int8_t *pw = a.wc + wr * a.k, *px = a.xc + xr * a.k;
-  i32x16_t acc = {};
-  for (int64_t k = half * 16; k - half * 16 < a.k; k += 32) {
-    i32x4_t fw = {}, fx = {};
-    if (k < a.k) {
-      fw = *(const i32x4_t*)(pw + k);
-      fx = *(const i32x4_t*)(px + k);
+// Memory from p on of which loads past `bytes` read zero.
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kPastW = 0x7FFFFFFFu;  // past every tile of W
+
+// 16 bytes a lane straight to LDS, lane i's at l + 16 i.
+__device__ __forceinline__ void load_lds16(Rsrc r, uint32_t offset, uint8_t* l) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, (int)offset, 0, 0, 0);
+}
+
+// The workgroup's barrier, once all of this wave's loads but the last LEFT have arrived
+// and its LDS accesses are done.  (The wait is the builtin, which the compiler counts
+// with: it would put one of its own, for all loads, ahead of a loop's first LDS read.)
+template <int LEFT> __device__ __forceinline__ void wait_and_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | (LEFT & 48) << 10 | 0x70);  // vmcnt(LEFT) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// f(0), f(1) .. as compile-time constants, until one of them is false.
+template <typename F, int... I> __device__ __forceinline__ bool for_each(F& f, std::integer_sequence<int, I...>) {
+  return (f(std::integral_constant<int, I>{}) && ...);
+}
+
+// Place of tile `pos`: bands of eight row tiles, within a band the row tiles of
+// one column tile side by side, so that what runs at one time shares few rows of
+// W and X.
+__device__ __forceinline__ void tile_place(int pos, int mt, int nt, int& im, int& in) {
+  const int band = pos / (8 * nt), at = pos - band * 8 * nt;
+  const int high = min(8, mt - band * 8);
+  in = at / high;
+  im = band * 8 + at - in * high;
+}
+
+// ---- tile kernel -------------------------------------------------------------
+// A kTileN x BM tile of y (256 rows of W, BM = 256 or 128 of X) per workgroup of four
+// waves (2x2), each wave 128 x (BM/2) in 32x32 accumulators, 128 bytes of K a step.  As
+// many workgroups as CUs; each walks through the tiles.
+//
+// LDS: a ring of two steps of W and of three of X (160 KiB for BM = 256), filled by
+// direct-to-LDS loads of whole 128-byte row pieces.  A piece is eight 16-byte chunks;
+// chunk c of row r lies at place c ^ (r & 7) ^ (r >> 3 & 1), so that 16 lanes of a
+// fragment read (one chunk of 16 rows) cover all banks.  Direct loads write lane-linear,
+// so the loading lane picks its chunk by the same rule.  Lane half h takes chunk 4h + i
+// at product i.
+//
+// Schedule of a step (products 0..3): the fragments of the next product are read under
+// this one's.  Under product 0 the X rows of the step after next are requested, into the
+// place of the step before.  The barrier sits before product 3, whose fragments are then
+// in registers: behind it the next step is complete (each wave has waited for its own
+// loads, but for the X rows just requested) and nobody reads this step any more, so the W
+// rows of the step after next go into its place.  W has a whole step to arrive, X two.
+template <int BM, typename OT, bool GROUPED>
+__global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) {
+  constexpr int BN = kTileN;
+  constexpr int NI = BN / 64, MI = BM / 64;      // 32-row fragments of a wave
+  constexpr int NL = BN / 32, ML = BM / 32;      // direct loads of a wave and step
+  __shared__ __attribute__((aligned(16))) uint8_t w0[BN * kStepB], w1[BN * kStepB];
+  __shared__ __attribute__((aligned(16))) uint8_t x0[BM * kStepB], x1[BM * kStepB], x2[BM * kStepB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
+  const int all_nb = (int)(a.k / 16);            // 16-byte pieces of a row
+  auto w_place = [&](auto p) -> uint8_t* {
+    constexpr int i = decltype(p)::value % 2;
+    return i == 0 ? w0 : w1;
+  };
+  auto x_place = [&](auto p) -> uint8_t* {
+    constexpr int i = decltype(p)::value % 3;
+    return i == 0 ? x0 : i == 1 ? x1 : x2;
+  };
+
+  // ---- the tile at hand
+  int64_t n0;
+  Tile t;
+  int nb, slot;                                  // pieces of its slice of K; slot of `part` or -1
+  Rsrc wc, xc;
+  uint32_t ow[NL], ox[ML];                       // direct load i of this lane: bytes from wc, xc
+  const int mt = GROUPED ? live_tiles(a.offsets, a.experts, a.m, BM) : plan.mt;
+  const int full = GROUPED ? mt * plan.nt : plan.full;
+  const int items = full + plan.rest * plan.split;
+  // Consecutive workgroups go to the eight XCDs in turn: of every round of tiles
+  // each XCD takes adjacent ones.
+  const int grid = gridDim.x, b = blockIdx.x;
+  const int place = (b % 8) * (grid / 8) + min(b % 8, grid % 8) + b / 8;
+  const int chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+  auto set_tile = [&](int item) {
+    int im, in, pos = item, b0 = 0;
+    nb = all_nb;
+    slot = -1;
+    if (!GROUPED && item >= full) {
+      slot = item - full;
+      pos = full + slot / plan.split;
+      const int s = slot % plan.split, steps = (all_nb + 7) / 8;
+      b0 = steps * s / plan.split * 8;
+      nb = min(steps * (s + 1) / plan.split * 8, all_nb) - b0;
     }
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw, fx, acc, 0, 0, 0);
-  }
-  if (m >= t.m1) return;
-  const float sx = a.xs[xr];
-  OT* y = (OT*)a.y + m * a.n;
+    tile_place(pos, mt, plan.nt, im, in);
+    if (GROUPED)
+      t = find_tile(a.offsets, a.experts, a.m, BM, im);
+    else
+      t = Tile{(int64_t)im * BM, min((int64_t)(im + 1) * BM, a.m), 0};
+    n0 = (int64_t)in * BN;
+    const int64_t wr = (int64_t)t.expert * a.n + n0;
+    const int w_rows = (int)min((int64_t)BN, a.n - n0), x_rows = (int)(t.m1 - t.m0);
+    int64_t xr[ML];
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    const int64_t n = n0 + 8 * (i >> 2) + 4 * half + (i & 3);
-    if (n < a.n) y[n] = none ? (OT)0.0f : mx_cvt<OT>(i8_scaled(acc[i], sx, a.ws[t.expert * a.n + n]));
+    for (int i = 0; i < ML; i++) xr[i] = min((4 * i + wave) * 8 + (lane >> 3), x_rows - 1);
+    const bool gather = GROUPED && a.x_rows;
+    if (gather) {
+#pragma unroll
+      for (int i = 0; i < ML; i++) xr[i] = a.x_rows[t.m0 + xr[i]];
+#pragma unroll
+      for (int i = 0; i < ML; i++) xr[i] = min(max(xr[i], (int64_t)0), a.x_rows_total - 1);
+    }
+    const int64_t x_first = gather ? 0 : t.m0, x_span = gather ? a.x_rows_total : x_rows;
+    wc = rsrc_of(a.wc + wr * a.k + b0 * 16, w_rows * a.k - b0 * 16);
+    xc = rsrc_of(a.xc + x_first * a.k + b0 * 16, x_span * a.k - b0 * 16);
+#pragma unroll
+    for (int i = 0; i < NL; i++) ow[i] = (uint32_t)(min((4 * i + wave) * 8 + (lane >> 3), w_rows - 1) * a.k);
+#pragma unroll
+    for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(xr[i] * a.k);
+  };
+  auto load_w = [&](int s, uint8_t* l) {
+    const int piece = s * 8 + chunk;
+#pragma unroll
+    for (int i = 0; i < NL; i++) load_lds16(wc, piece < nb ? ow[i] + piece * 16 : kPastW, l + (4 * i + wave) * 1024);
+  };
+  auto load_x = [&](int s, uint8_t* l) {
+    const uint32_t col = (uint32_t)min(s * 8 + chunk, nb - 1) * 16;
+#pragma unroll
+    for (int i = 0; i < ML; i++) load_lds16(xc, ox[i] + col, l + (4 * i + wave) * 1024);
+  };
+
+  struct Frags {
+    i32x4_t w[NI], x[MI];
+  };
+  auto read_frags = [&](const uint8_t* lw, const uint8_t* lx, int i) {
+    Frags f;
+    const int at = l32 * kStepB + ((4 * half + i) ^ (l32 & 7) ^ ((l32 >> 3) & 1)) * 16;
+#pragma unroll
+    for (int j = 0; j < NI; j++) f.w[j] = *(const i32x4_t*)(lw + (wn + j * 32) * kStepB + at);
+#pragma unroll
+    for (int j = 0; j < MI; j++) f.x[j] = *(const i32x4_t*)(lx + (wm + j * 32) * kStepB + at);
+    return f;
+  };
+  i32x16_t acc[NI][MI];
+  auto products = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+      for (int j = 0; j < MI; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
+  };
+  // Keeps the products before it from moving past the branches behind them, where
+  // their operands would have to wait in registers.
+  auto pin = [&]() {
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+      for (int j = 0; j < MI; j++) asm volatile("" : "+a"(acc[i][j]));
+  };
+  // The instruction order asked for: LDS reads, then memory loads, one at a time
+  // between the products.
+  auto spread = [&](int reads, int loads) {
+#pragma unroll
+    for (int i = 0; i < NI * MI; i++) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  int item = place;
+  if (item >= items) return;
+  set_tile(item);
+  load_x(0, x0);
+  load_w(0, w0);
+  load_x(1, x1);
+  load_w(1, w1);
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+      for (int j = 0; j < MI; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[i][j][e] = 0;
+    const int steps = (nb + 7) / 8;
+    int s = 0;
+    wait_and_meet<NL + ML>();
+    Frags f = read_frags(w0, x0, 0), g;
+    // position P of the rings: products 0 to 2 of step s, and the fragments of product 3
+    auto front = [&](auto which) {
+      constexpr int P = decltype(which)::value;
+      uint8_t *lw = w_place(which), *lx = x_place(which);
+      g = read_frags(lw, lx, 1);
+      load_x(s + 2, x_place(std::integral_constant<int, P + 2>{}));
+      products(f);
+      spread(NI + MI, ML);
+      f = read_frags(lw, lx, 2);
+      products(g);
+      spread(NI + MI, 0);
+      g = read_frags(lw, lx, 3);
+      products(f);
+      spread(NI + MI, 0);
+      pin();
+    };
+    // product 3 of step s behind the barrier, then the next step's front.  The loads run
+    // past the slice's end, where they read nothing of use.
+    auto step = [&](auto which) {
+      constexpr int P = decltype(which)::value;
+      typedef std::integral_constant<int, P + 1> Next;
+      wait_and_meet<ML>();
+      f = read_frags(w_place(Next{}), x_place(Next{}), 0);
+      load_w(s + 2, w_place(which));
+      products(g);
+      spread(NI + MI, NL);
+      pin();
+      if (++s >= steps) return false;
+      front(Next{});
+      return true;
+    };
+    front(std::integral_constant<int, 0>{});
+    while (for_each(step, std::make_integer_sequence<int, 6>{})) {
+    }
+
+    // ---- this tile's results, under which the next one's first steps are loaded
+    const Tile done = t;
+    const int64_t dn0 = n0;
+    const int dslot = slot;
+    item += grid;
+    wait_and_meet<0>();  // nothing of this tile is under way or read any more
+    if (item < items) {
+      set_tile(item);
+      load_x(0, x0);
+      load_w(0, w0);
+      load_x(1, x1);
+      load_w(1, w1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // The accumulators are taken out of their registers where they are written, not
+    // all at once, and the addresses are worked out here, not kept from before the
+    // loop: either would spill.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int half = lane >> 5, l32 = lane & 31;
+    if (!GROUPED && dslot >= 0) {  // a slice's sums, in the order of the registers
+      i32x4_t* p = (i32x4_t*)(plan.part + (int64_t)dslot * BM * BN) + wave * (NI * MI * 4 * 64) + lane;
+#pragma unroll
+      for (int i = 0; i < NI; i++)
+#pragma unroll
+        for (int j = 0; j < MI; j++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            i32x16_t& c = acc[i][j];
+            if (q == 0) asm volatile("" : "+a"(c));
+            p[((i * MI + j) * 4 + q) * 64] = i32x4_t{c[q * 4], c[q * 4 + 1], c[q * 4 + 2], c[q * 4 + 3]};
+          }
+    } else {
+      // Through LDS, in the third place of the ring of X, to be stored in whole 128-byte lines.
+      typedef OT V4 __attribute__((ext_vector_type(4)));
+      constexpr int kCols = 128 / sizeof(OT), kPer = 16 / sizeof(OT), kFr = kCols / 32;  // columns of a pass, a store
+      const int rows = (int)(done.m1 - done.m0), cols = (int)min(a.n - dn0, (int64_t)BN);
+      uint8_t* o = x2 + wave * (32 * 128);
+      const int r0 = lane >> 3, c0 = (lane & 7) * kPer;  // of a store within its 8 rows
+      OT* y = (OT*)a.y + (done.m0 + wm + r0) * a.n + dn0 + wn + c0;
+      const float* sw = a.ws + done.expert * a.n + dn0;
+#pragma unroll
+      for (int j = 0; j < MI; j++) {
+        // the scale of this lane's row
+        bool none = false;
+        int64_t xr = done.m0 + min(wm + j * 32 + l32, rows - 1);
+        if (GROUPED && a.x_rows) {
+          xr = a.x_rows[xr];
+          none = xr < 0 || xr >= a.x_rows_total;
+          if (none) xr = 0;
+        }
+        const float sx = a.xs[xr];
+#pragma unroll
+        for (int p = 0; p < NI / kFr; p++) {
+#pragma unroll
+          for (int i = 0; i < kFr; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              i32x16_t& c = acc[p * kFr + i][j];
+              if (q == 0) asm volatile("" : "+a"(c));
+              const int n = wn + (p * kFr + i) * 32 + q * 8 + half * 4;
+              V4 v;
+#pragma unroll
+              for (int e = 0; e < 4; e++) v[e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], sx, sw[min(n + e, cols - 1)]));
+              if (GROUPED && none) v = V4{};
+              const int byte = (i * 32 + q * 8 + half * 4) * (int)sizeof(OT);
+              *(V4*)(o + l32 * 128 + (((byte >> 4) ^ (l32 & 7)) << 4) + (byte & 15)) = v;
+            }
+          wave_lds_sync();
+          const int n = wn + p * kCols + c0;
+          u32x4_t v[4];
+#pragma unroll
+          for (int s = 0; s < 4; s++) v[s] = *(const u32x4_t*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
+#pragma unroll
+          for (int s = 0; s < 4; s++)
+            if (wm + j * 32 + s * 8 + r0 < rows && n + kPer <= cols)
+              __builtin_memcpy(y + (int64_t)(j * 32 + s * 8) * a.n + p * kCols, &v[s], 16);
+          if (cols % kPer) {  // the columns of a width that ends inside a store
+#pragma unroll 1
+            for (int s = 0; s < 4; s++) {
+              const OT* e = (const OT*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
+              if (wm + j * 32 + s * 8 + r0 < rows && n < cols && n + kPer > cols)
+#pragma unroll 1
+                for (int i = 0; n + i < cols; i++) y[(int64_t)(j * 32 + s * 8) * a.n + p * kCols + i] = e[i];
+            }
+          }
+          wave_lds_sync();
+        }
+      }
+    }
+    if (item >= items) return;
   }
 }
 
-template <typename OT, bool GROUPED> __global__ __launch_bounds__(256) void i8_tile_kernel(Args a, int64_t mt, int64_t nt) {
-  for (int64_t i = blockIdx.x; i < mt * nt; i += gridDim.x) i8_tile<OT, GROUPED>(a, i / nt, i % nt);
+// y of the split tiles: adds the slices' sums.  A thread takes 16 sums of one fragment
+// in register order; the half-waves swap so that each lane stores runs of eight columns.
+template <int BM, typename OT>
+__global__ __launch_bounds__(256) void i8_fold_kernel(Args a, TilePlan plan) {
+  constexpr int BN = kTileN;
+  constexpr int NI = BN / 64, MI = BM / 64;
+  typedef OT V8 __attribute__((ext_vector_type(8)));
+  const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+  const int piece = blockIdx.x * 4 + (threadIdx.x >> 6);  // fragment of a tile
+  const int tile = piece / (4 * NI * MI), frag = piece % (4 * NI * MI);
+  const int wave = frag / (NI * MI), i = frag % (NI * MI) / MI, j = frag % MI;
+  int im, in;
+  tile_place(plan.full + tile, plan.mt, plan.nt, im, in);
+  i32x4_t v[4] = {};
+  const i32x4_t* p = (const i32x4_t*)plan.part + ((int64_t)tile * plan.split * 4 * NI * MI + frag) * 256 + lane;
+  for (int s = 0; s < plan.split; s++, p += 4 * NI * MI * 256)
+#pragma unroll
+    for (int q = 0; q < 4; q++) v[q] += p[q * 64];
+  const int64_t row = (int64_t)im * BM + (wave >> 1) * (BM / 2) + j * 32 + l32;
+  const float sx = a.xs[min(row, a.m - 1)];
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    // of columns 8 q .. 8 q + 15 the lower half-wave stores the first eight, the upper the others
+    i32x4_t other;
+#pragma unroll
+    for (int e = 0; e < 4; e++) other[e] = __shfl_xor(half ? v[q][e] : v[q + 1][e], 32, 64);
+    const i32x4_t lo = half ? other : v[q], hi = half ? v[q + 1] : other;
+    const int64_t n = (int64_t)in * BN + (wave & 1) * (BN / 2) + i * 32 + (q + half) * 8;
+    if (row >= a.m || n >= a.n) continue;
+    OT* y = (OT*)a.y + row * a.n + n;
+    V8 o;
+#pragma unroll
+    for (int e = 0; e < 8; e++) o[e] = mx_cvt<OT>(i8_scaled(e < 4 ? lo[e] : hi[e - 4], sx, a.ws[min(n + e, a.n - 1)]));
+    if (n + 8 <= a.n) {
+      __builtin_memcpy(y, &o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        if (n + e < a.n) y[e] = o[e];
+    }
+  }
 }
 
-template <typename OT> hipError_t run(const Args& a, hipStream_t stream) {
-  const int64_t mt = (a.m + 63) / 64 + (a.offsets ? std::min((int64_t)a.experts, a.m) : 0), nt = (a.n + 63) / 64;
-  const dim3 grid((unsigned)std::min(mt * nt, (int64_t)1 << 20));
-  if (a.offsets) hipLaunchKernelGGL((i8_tile_kernel<OT, true>), grid, dim3(256), 0, stream, a, mt, nt);
-  else hipLaunchKernelGGL((i8_tile_kernel<OT, false>), grid, dim3(256), 0, stream, a, mt, nt);
+template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
+  const int grid = std::min(p.full + p.rest * p.split, device_cu_count());
+  hipLaunchKernelGGL((i8_tile_kernel<BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !p.rest) return e;
+  hipLaunchKernelGGL((i8_fold_kernel<BM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (BM / 64))), dim3(256), 0,
+                     stream, a, p);
   return hipGetLastError();
+}
+
+template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t stream) {
+  double us;
+  TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0, us);
+  p.part = (int32_t*)ws;
+  if (p.high == 256) return a.offsets ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<256, OT, false>(a, p, stream);
+  return a.offsets ? go_tiles<128, OT, true>(a, p, stream) : go_tiles<128, OT, false>(a, p, stream);
 }
 
 }  // namespace
 
-size_t i8_gemm_ws_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t i8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
+  double us;
+  return tile_ws_bytes(tile_plan(m, n, k, experts, us));
+}
 
-hipError_t launch_i8_gemm(const I8Gemm& g, void*, hipStream_t stream) {
+hipError_t launch_i8_gemm(const I8Gemm& g, void* ws, hipStream_t stream) {
   const Args a = {g.x.codes, g.w.codes, g.x.scales, g.w.scales, g.m, g.n, g.k, g.x.rows, g.y, g.offsets, g.x_rows,
                   g.experts};
-  if (g.y_dtype == kF32) return run<float>(a, stream);
-  if (g.y_dtype == kF16) return run<_Float16>(a, stream);
-  return run<__bf16>(a, stream);
+  if (g.y_dtype == kF32) return run<float>(a, ws, stream);
+  if (g.y_dtype == kF16) return run<_Float16>(a, ws, stream);
+  return run<__bf16>(a, ws, stream);
 }
 
 }  // namespace rz
