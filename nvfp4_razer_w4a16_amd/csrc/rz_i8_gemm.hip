@@ -94,6 +94,11 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
   constexpr int NL = BN / 32, ML = BM / 32;      // direct loads of a wave and step
   __shared__ __attribute__((aligned(16))) uint8_t w0[BN * kStepB], w1[BN * kStepB];
   __shared__ __attribute__((aligned(16))) uint8_t x0[BM * kStepB], x1[BM * kStepB], x2[BM * kStepB];
+  // scales of the tile's columns and rows, and which rows are padding: behind the results' place in x2
+  // where that is large enough (and all other LDS taken)
+  constexpr int kOut = 4 * 32 * 128, kScales = (BN + BM) * 4 + 32;
+  __shared__ __attribute__((aligned(16))) uint8_t own[BM == 256 ? 16 : kScales];
+  static_assert(BM != 256 || kOut + kScales <= BM * kStepB, "x2 holds both");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
@@ -113,6 +118,8 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
   int nb, slot;                                  // pieces of its slice of K; slot of `part` or -1
   Rsrc wc, xc;
   uint32_t ow[NL], ox[ML];                       // direct load i of this lane: bytes from wc, xc
+  float sw, sx;                                  // of the tile's column, and row, tid
+  bool none;                                     // that row is padding
   const int mt = GROUPED ? live_tiles(a.offsets, a.experts, a.m, BM) : plan.mt;
   const int full = GROUPED ? mt * plan.nt : plan.full;
   const int items = full + plan.rest * plan.split;
@@ -157,6 +164,15 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     for (int i = 0; i < NL; i++) ow[i] = (uint32_t)(min((4 * i + wave) * 8 + (lane >> 3), w_rows - 1) * a.k);
 #pragma unroll
     for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(xr[i] * a.k);
+    int64_t row = t.m0 + min(tid % BM, x_rows - 1);
+    none = false;
+    if (gather) {
+      row = a.x_rows[row];
+      none = row < 0 || row >= a.x_rows_total;
+      if (none) row = 0;
+    }
+    sw = a.ws[wr + min(tid, w_rows - 1)];
+    sx = a.xs[row];
   };
   auto load_w = [&](int s, uint8_t* l) {
     const int piece = s * 8 + chunk;
@@ -204,7 +220,7 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     for (int i = 0; i < NI * MI; i++) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (i < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (i % 2 && i / 2 < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -267,7 +283,12 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     const int64_t dn0 = n0;
     const int dslot = slot;
     item += grid;
+    uint8_t* scl = BM == 256 ? x2 + kOut : own;
     wait_and_meet<0>();  // nothing of this tile is under way or read any more
+    *(float*)(scl + tid * 4) = sw;
+    if (BM == 256 || tid < BM) *(float*)(scl + (BN + tid) * 4) = sx;
+    if (GROUPED) *(uint64_t*)(scl + (BN + BM) * 4 + wave * 8) = __ballot(none);
+    wait_and_meet<0>();
     if (item < items) {
       set_tile(item);
       load_x(0, x0);
@@ -302,18 +323,12 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       uint8_t* o = x2 + wave * (32 * 128);
       const int r0 = lane >> 3, c0 = (lane & 7) * kPer;  // of a store within its 8 rows
       OT* y = (OT*)a.y + (done.m0 + wm + r0) * a.n + dn0 + wn + c0;
-      const float* sw = a.ws + done.expert * a.n + dn0;
+      const float* csw = (const float*)scl + wn + half * 4;
 #pragma unroll
       for (int j = 0; j < MI; j++) {
-        // the scale of this lane's row
-        bool none = false;
-        int64_t xr = done.m0 + min(wm + j * 32 + l32, rows - 1);
-        if (GROUPED && a.x_rows) {
-          xr = a.x_rows[xr];
-          none = xr < 0 || xr >= a.x_rows_total;
-          if (none) xr = 0;
-        }
-        const float sx = a.xs[xr];
+        const int m = wm + j * 32 + l32;  // this lane's row
+        const float rsx = *(const float*)(scl + (BN + m) * 4);
+        const bool zero = GROUPED && (scl[(BN + BM) * 4 + (m >> 3)] >> (m & 7) & 1);
 #pragma unroll
         for (int p = 0; p < NI / kFr; p++) {
 #pragma unroll
@@ -322,11 +337,11 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
             for (int q = 0; q < 4; q++) {
               i32x16_t& c = acc[p * kFr + i][j];
               if (q == 0) asm volatile("" : "+a"(c));
-              const int n = wn + (p * kFr + i) * 32 + q * 8 + half * 4;
+              const f32x4_t s4 = *(const f32x4_t*)(csw + (p * kFr + i) * 32 + q * 8);
               V4 v;
 #pragma unroll
-              for (int e = 0; e < 4; e++) v[e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], sx, sw[min(n + e, cols - 1)]));
-              if (GROUPED && none) v = V4{};
+              for (int e = 0; e < 4; e++) v[e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], rsx, s4[e]));
+              if (zero) v = V4{};
               const int byte = (i * 32 + q * 8 + half * 4) * (int)sizeof(OT);
               *(V4*)(o + l32 * 128 + (((byte >> 4) ^ (l32 & 7)) << 4) + (byte & 15)) = v;
             }
