@@ -22,6 +22,8 @@ namespace rz {
 
 namespace {
 
+using namespace i8;
+
 struct Args {
   const int8_t *xc, *wc;
   const float *xs, *ws;
@@ -139,17 +141,22 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       b0 = steps * s / plan.split * 8;
       nb = min(steps * (s + 1) / plan.split * 8, all_nb) - b0;
     }
-    tile_place(pos, mt, plan.nt, im, in);
+    if (!GROUPED && BM == 128 && plan.halves) {  // half `item % 2` of a tile of twice the height
+      tile_place(plan.first + item / 2, mt, plan.nt, im, in);
+      im = 2 * im + item % 2;
+    } else {
+      tile_place(pos, mt, plan.nt, im, in);
+    }
     if (GROUPED)
       t = find_tile(a.offsets, a.experts, a.m, BM, im);
-    else
-      t = Tile{(int64_t)im * BM, min((int64_t)(im + 1) * BM, a.m), 0};
+    else  // a half behind the last row has none: what is read for it is the last one
+      t = Tile{min((int64_t)im * BM, a.m), min((int64_t)(im + 1) * BM, a.m), 0};
     n0 = (int64_t)in * BN;
     const int64_t wr = (int64_t)t.expert * a.n + n0;
-    const int w_rows = (int)min((int64_t)BN, a.n - n0), x_rows = (int)(t.m1 - t.m0);
+    const int w_rows = (int)min((int64_t)BN, a.n - n0), x_rows = (int)(t.m1 - t.m0), x_last = max(x_rows, 1) - 1;
     int64_t xr[ML];
 #pragma unroll
-    for (int i = 0; i < ML; i++) xr[i] = min((4 * i + wave) * 8 + (lane >> 3), x_rows - 1);
+    for (int i = 0; i < ML; i++) xr[i] = min((4 * i + wave) * 8 + (lane >> 3), x_last);
     const bool gather = GROUPED && a.x_rows;
     if (gather) {
 #pragma unroll
@@ -157,14 +164,14 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
 #pragma unroll
       for (int i = 0; i < ML; i++) xr[i] = min(max(xr[i], (int64_t)0), a.x_rows_total - 1);
     }
-    const int64_t x_first = gather ? 0 : t.m0, x_span = gather ? a.x_rows_total : x_rows;
+    const int64_t x_first = gather ? 0 : min(t.m0, a.m - 1), x_span = gather ? a.x_rows_total : x_last + 1;
     wc = rsrc_of(a.wc + wr * a.k + b0 * 16, w_rows * a.k - b0 * 16);
     xc = rsrc_of(a.xc + x_first * a.k + b0 * 16, x_span * a.k - b0 * 16);
 #pragma unroll
     for (int i = 0; i < NL; i++) ow[i] = (uint32_t)(min((4 * i + wave) * 8 + (lane >> 3), w_rows - 1) * a.k);
 #pragma unroll
     for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(xr[i] * a.k);
-    int64_t row = t.m0 + min(tid % BM, x_rows - 1);
+    int64_t row = min(t.m0, a.m - 1) + min(tid % BM, x_last);
     none = false;
     if (gather) {
       row = a.x_rows[row];
@@ -324,47 +331,55 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       const int r0 = lane >> 3, c0 = (lane & 7) * kPer;  // of a store within its 8 rows
       OT* y = (OT*)a.y + (done.m0 + wm + r0) * a.n + dn0 + wn + c0;
       const float* csw = (const float*)scl + wn + half * 4;
-#pragma unroll
-      for (int j = 0; j < MI; j++) {
-        const int m = wm + j * 32 + l32;  // this lane's row
+      constexpr int kPasses = MI * NI / kFr;  // 32 rows and kCols columns each
+      V4 v[kFr * 4];
+      auto convert = [&](int pass) {
+        const int j = pass / (NI / kFr), p = pass % (NI / kFr), m = wm + j * 32 + l32;  // this lane's row
         const float rsx = *(const float*)(scl + (BN + m) * 4);
         const bool zero = GROUPED && (scl[(BN + BM) * 4 + (m >> 3)] >> (m & 7) & 1);
 #pragma unroll
-        for (int p = 0; p < NI / kFr; p++) {
+        for (int i = 0; i < kFr; i++)
 #pragma unroll
-          for (int i = 0; i < kFr; i++)
+          for (int q = 0; q < 4; q++) {
+            i32x16_t& c = acc[p * kFr + i][j];
+            if (q == 0) asm volatile("" : "+a"(c));
+            const f32x4_t s4 = *(const f32x4_t*)(csw + (p * kFr + i) * 32 + q * 8);
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-              i32x16_t& c = acc[p * kFr + i][j];
-              if (q == 0) asm volatile("" : "+a"(c));
-              const f32x4_t s4 = *(const f32x4_t*)(csw + (p * kFr + i) * 32 + q * 8);
-              V4 v;
-#pragma unroll
-              for (int e = 0; e < 4; e++) v[e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], rsx, s4[e]));
-              if (zero) v = V4{};
-              const int byte = (i * 32 + q * 8 + half * 4) * (int)sizeof(OT);
-              *(V4*)(o + l32 * 128 + (((byte >> 4) ^ (l32 & 7)) << 4) + (byte & 15)) = v;
-            }
-          wave_lds_sync();
-          const int n = wn + p * kCols + c0;
-          u32x4_t v[4];
-#pragma unroll
-          for (int s = 0; s < 4; s++) v[s] = *(const u32x4_t*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
-#pragma unroll
-          for (int s = 0; s < 4; s++)
-            if (wm + j * 32 + s * 8 + r0 < rows && n + kPer <= cols)
-              __builtin_memcpy(y + (int64_t)(j * 32 + s * 8) * a.n + p * kCols, &v[s], 16);
-          if (cols % kPer) {  // the columns of a width that ends inside a store
-#pragma unroll 1
-            for (int s = 0; s < 4; s++) {
-              const OT* e = (const OT*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
-              if (wm + j * 32 + s * 8 + r0 < rows && n < cols && n + kPer > cols)
-#pragma unroll 1
-                for (int i = 0; n + i < cols; i++) y[(int64_t)(j * 32 + s * 8) * a.n + p * kCols + i] = e[i];
-            }
+            for (int e = 0; e < 4; e++) v[i * 4 + q][e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], rsx, s4[e]));
+            if (zero) v[i * 4 + q] = V4{};
           }
-          wave_lds_sync();
+      };
+      convert(0);
+#pragma unroll
+      for (int pass = 0; pass < kPasses; pass++) {
+        const int j = pass / (NI / kFr), p = pass % (NI / kFr);
+#pragma unroll
+        for (int i = 0; i < kFr; i++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const int byte = (i * 32 + q * 8 + half * 4) * (int)sizeof(OT);
+            *(V4*)(o + l32 * 128 + (((byte >> 4) ^ (l32 & 7)) << 4) + (byte & 15)) = v[i * 4 + q];
+          }
+        wave_lds_sync();
+        const int n = wn + p * kCols + c0;
+        u32x4_t line[4];
+#pragma unroll
+        for (int s = 0; s < 4; s++) line[s] = *(const u32x4_t*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
+        if (pass + 1 < kPasses) convert(pass + 1);
+#pragma unroll
+        for (int s = 0; s < 4; s++)
+          if (wm + j * 32 + s * 8 + r0 < rows && n + kPer <= cols)
+            __builtin_memcpy(y + (int64_t)(j * 32 + s * 8) * a.n + p * kCols, &line[s], 16);
+        if (cols % kPer) {  // the columns of a width that ends inside a store
+#pragma unroll 1
+          for (int s = 0; s < 4; s++) {
+            const OT* e = (const OT*)(o + (s * 8 + r0) * 128 + ((lane & 7) ^ r0) * 16);
+            if (wm + j * 32 + s * 8 + r0 < rows && n < cols && n + kPer > cols)
+#pragma unroll 1
+              for (int i = 0; n + i < cols; i++) y[(int64_t)(j * 32 + s * 8) * a.n + p * kCols + i] = e[i];
+          }
         }
+        wave_lds_sync();
       }
     }
     if (item >= items) return;
@@ -417,8 +432,10 @@ __global__ __launch_bounds__(256) void i8_fold_kernel(Args a, TilePlan plan) {
 template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
   const int grid = std::min(p.full + p.rest * p.split, device_cu_count());
   hipLaunchKernelGGL((i8_tile_kernel<BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !p.rest) return e;
+  return hipGetLastError();
+}
+
+template <int BM, typename OT> hipError_t go_fold(const Args& a, const TilePlan& p, hipStream_t stream) {
   hipLaunchKernelGGL((i8_fold_kernel<BM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (BM / 64))), dim3(256), 0,
                      stream, a, p);
   return hipGetLastError();
@@ -428,15 +445,27 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
   double us;
   TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0, us);
   p.part = (int32_t*)ws;
-  if (p.high == 256) return a.offsets ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<256, OT, false>(a, p, stream);
-  return a.offsets ? go_tiles<128, OT, true>(a, p, stream) : go_tiles<128, OT, false>(a, p, stream);
+  if (a.offsets) return p.high == 256 ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<128, OT, true>(a, p, stream);
+  TilePlan halves = p;
+  if (p.halves) {  // the tiles of whole rounds, then the rest in halves
+    halves.first = p.full - p.halves;
+    halves.full = 2 * p.halves;
+    p.full -= p.halves;
+    p.halves = 0;
+  }
+  hipError_t e = hipSuccess;
+  if (p.full + p.rest > 0)
+    e = p.high == 256 ? go_tiles<256, OT, false>(a, p, stream) : go_tiles<128, OT, false>(a, p, stream);
+  if (e == hipSuccess && halves.halves) return go_tiles<128, OT, false>(a, halves, stream);
+  if (e != hipSuccess || !p.rest) return e;
+  return p.high == 256 ? go_fold<256, OT>(a, p, stream) : go_fold<128, OT>(a, p, stream);
 }
 
 }  // namespace
 
 size_t i8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
   double us;
-  return tile_ws_bytes(tile_plan(m, n, k, experts, us));
+  return i8::tile_ws_bytes(i8::tile_plan(m, n, k, experts, us));
 }
 
 hipError_t launch_i8_gemm(const I8Gemm& g, void* ws, hipStream_t stream) {

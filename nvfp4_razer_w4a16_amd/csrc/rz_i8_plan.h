@@ -1,5 +1,6 @@
 // rz_i8_plan.h -- which kernel a product of 8-bit integer tensors runs on, and how it is
-// cut: rules on sizes and the device's compute units.  Host code.
+// cut: rules on sizes and the device's compute units.  Host code.  (In a namespace of its
+// own: the MXFP4 products' rules have the same names.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -12,6 +13,7 @@
 #include "rz_i8_launch.h"
 
 namespace rz {
+namespace i8 {
 
 // ---- tile kernel -------------------------------------------------------------
 constexpr int kTileN = 256;   // rows of W of a tile
@@ -23,6 +25,8 @@ struct TilePlan {
   int high;  // rows of X of a tile
   int mt, nt;
   int full, rest, split;
+  int halves;  // of the full tiles, 256 high, the last ones that are done as two of 128 each
+  int first;   // the first of them
   int32_t* part;
 };
 
@@ -54,6 +58,11 @@ inline TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t expe
     const double t = (steps + s - 1) / s * step_us(high, false) + fold_us(rest * s, high);
     if (t < best) best = t, p.split = s;
   }
+  if (high == 256 && rest * 2 <= cus && steps * step_us(128, true) + 6.0 < best) {
+    best = steps * step_us(128, true) + 6.0;
+    p.halves = rest;
+    p.split = 1;
+  }
   us = p.full / cus * step_us(high, true) * steps + best;
   if (p.split > 1) p.rest = rest, p.full -= rest;
   return p;
@@ -67,4 +76,5 @@ inline TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts, doub
 }
 inline size_t tile_ws_bytes(const TilePlan& p) { return (size_t)p.rest * p.split * kTileN * p.high * 4; }
 
+}  // namespace i8
 }  // namespace rz
