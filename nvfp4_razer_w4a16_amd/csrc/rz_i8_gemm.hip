@@ -386,6 +386,321 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
   }
 }
 
+// ---- stream kernel -------------------------------------------------------------
+// For few rows of X the product is a read of W.  A workgroup of eight waves owns 16
+// W rows at a time (a "row tile", one contiguous piece of memory) and all of K,
+// which the waves share in units of 256 bytes; each keeps its share of up to 16 MT
+// rows of X (a "job") in registers for all the row tiles that the workgroup walks
+// through, so that nothing but W is read in the loop.  The row
+// tiles of all jobs stand in one line that is cut between the workgroups, however
+// the rows are spread over the experts; a piece that crosses jobs loads the next
+// one's X on the way.
+//
+// A row tile comes in CK chunks of up to 2048 bytes of K, 32 KiB each, by
+// direct-to-LDS loads into a ring of RING buffers, RING - 1 chunks ahead: memory is
+// read in long runs whatever K is, and what is under way costs no registers.  A chunk's
+// 16-byte pieces lie in LDS as in memory but for an exchange within a row, piece c of
+// row r at c ^ (r & mask), which spreads the rows over the banks where the row's length
+// would not.  Rows of at most 1024 or 512 bytes come RT = two or four row tiles a chunk,
+// each of which has four or two of the waves to share its K.
+//
+// Of a wave's sixteen pieces, lane group g = lane / 16 takes the four from 4 g on, one
+// a product: K is summed in another order, the same for both operands.  Pieces past the
+// row or the chunk are zeros in X, whatever W's fragment holds there.  The scales of a
+// row tile come to LDS the same way as W.  The waves' sums meet in LDS.  Loads past the
+// last row return zero (the buffer descriptor ends there), so no load has a branch
+// around it and a chunk's loads have a fixed number.
+constexpr int kSWaves = 8, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
+
+// Ring places.
+constexpr int stream_ring(int mt) { return mt == 4 ? 3 : 4; }
+
+template <int RT, int CK, int MT, bool GROUPED>
+__global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int y_dtype, StreamPlan plan) {
+  constexpr int kRing = stream_ring(MT);
+  static_assert(RT == 1 || CK == 1, "chunks of several row tiles hold whole rows");
+  // Of the waves of a row tile, kAlong share its K and kX the job's rows; a wave has
+  // kUnits times 256 bytes of K and kMT times 16 rows.
+  constexpr int kX = !GROUPED && CK == 1 && MT > 1 ? 2 : 1, kAlong = kSWaves / RT / kX, kUnits = kX, kMT = MT / kX;
+  constexpr int kRows = kSRows * RT;         // rows of W in a chunk
+  constexpr int kPart = kSRows * 16 * kMT;   // sums of one wave
+  constexpr int kSums = kSRows * 16 * MT;    // results of a row tile
+  constexpr int kOuts = (RT * kSums + 64 * kSWaves - 1) / (64 * kSWaves);  // of a thread in a chunk
+  // A round is whole row tiles and whole turns of the ring, and an even number of tiles
+  // where there are two sets of sums.
+  constexpr int kRound = CK >= 4 ? 2 * CK : kRing % 2 ? 2 * kRing : kRing;
+  static_assert(kRound % kRing == 0 && kRound % CK == 0, "whole turns, whole row tiles");
+  constexpr int kAreas = CK == 1 ? kRing : kRound / CK;  // places of scales, in turn for the round's row tiles
+  // Row tiles that the scales are requested ahead: enough that the loads of kRing - 2
+  // chunks are behind them when they are needed, behind the next row tile's first barrier.
+  constexpr int kScAhead = CK == 1 ? kRing - 2 : 0;
+  static_assert(kAreas > kScAhead + 1, "of four areas one is read, and the others loaded");
+  __shared__ __attribute__((aligned(16))) uint8_t r0[kSRows * kChunkB], r1[kSRows * kChunkB], r2[kSRows * kChunkB],
+      r3[kRing > 3 ? kSRows * kChunkB : 16];
+  __shared__ __attribute__((aligned(16))) float a0[kRows], a1[kRows], a2[kAreas > 2 ? kRows : 4], a3[kAreas > 3 ? kRows : 4];
+  // The waves' sums of a row tile are added behind the next chunk's barrier, where there
+  // is a second set of them or a barrier more before the next tile's are written.
+  constexpr int kParts = CK == 1 && (MT == 1 || kX == 2) ? 2 : 1;
+  constexpr bool kDefer = CK > 1 || kParts == 2;
+  __shared__ __attribute__((aligned(16))) int part[kParts * kSWaves * kPart];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kb = (int)a.k, nb = kb / 16;
+  const int units = (int)((a.n + kSRows - 1) / kSRows);  // what the line is cut into
+  auto ring = [&](auto p) -> uint8_t* {
+    constexpr int i = decltype(p)::value % kRing;
+    return i == 0 ? r0 : i == 1 ? r1 : i == 2 ? r2 : r3;
+  };
+  auto area = [&](auto tile) -> float* {
+    constexpr int i = decltype(tile)::value % kAreas;
+    return i == 0 ? a0 : i == 1 ? a1 : i == 2 ? a2 : a3;
+  };
+  // exchange of a row's pieces: within aligned groups, at most 16, that divide the row
+  auto key = [](int pieces, int r) { return r & (min(pieces & -pieces, 16) - 1); };
+  auto quotient = [](int p, int mul) { return (int)(((uint32_t)p * (uint32_t)mul) >> 20); };
+  // direct load i of this lane: bytes from the chunk's first one, or past every end
+  uint32_t off[kSLoads], off_last[kSLoads];
+#pragma unroll
+  for (int i = 0; i < kSLoads; i++) {
+    const int p = (i * kSWaves + wave) * 64 + lane;
+    auto offset = [&](int pieces, int mul) {
+      const int r = quotient(p, mul), c = p - r * pieces;
+      return r < kRows ? (uint32_t)(r * kb + (c ^ key(pieces, r)) * 16) : 0x7FFFFFFFu;
+    };
+    off_last[i] = offset(plan.last, plan.mul_last);
+    off[i] = CK > 1 ? offset(plan.pieces, plan.mul_pieces) : off_last[i];
+  }
+
+  // this workgroup's piece of the line
+  const uint32_t b = blockIdx.x;
+  Cuts c = plan.cuts;
+  if (GROUPED) c = cuts_of((uint32_t)units, (uint32_t)live_tiles(a.offsets, a.experts, a.m, plan.rows), gridDim.x, RT);
+  int job, unit, left;
+  if (c.per_job) {
+    job = GROUPED ? (int)(b / c.per_job) : quotient((int)b, plan.mul_per_job);
+    const uint32_t cut = b - (uint32_t)job * c.per_job;
+    unit = (int)(c.share * cut + min(cut, c.extra));
+    left = job < (int)c.jobs ? (int)(c.share + (cut < c.extra ? 1 : 0)) : 0;
+  } else {
+    const uint32_t start = c.share * b + min(b, c.extra);
+    job = (int)(start / (uint32_t)units);
+    unit = (int)(start - (uint32_t)job * (uint32_t)units);
+    left = (int)(c.share + (b < c.extra ? 1 : 0));
+  }
+  for (; left > 0; job++, unit = 0) {
+    Tile t;
+    if (GROUPED)
+      t = find_tile(a.offsets, a.experts, a.m, plan.rows, job);
+    else
+      t = Tile{(int64_t)job * plan.rows, min((int64_t)(job + 1) * plan.rows, a.m), 0};
+    if (GROUPED && t.expert < 0) return;
+    // its rows of W in this job: n_rows from n0 on, in `end` chunks or times CK
+    const int taken = min(left, units - unit), n0 = unit * kSRows;
+    const int n_rows = (int)min((int64_t)taken * kSRows, a.n - n0), end = (n_rows + kRows - 1) / kRows;
+    left -= taken;
+    int tile = 0;
+    const int8_t* wc = a.wc + ((int64_t)t.expert * a.n + n0) * kb;
+    const float* wsc = a.ws + (int64_t)t.expert * a.n + n0;
+    auto rows_of = [&](int tile) { return tile < end ? min(n_rows - tile * kRows, kRows) : 0; };
+    auto load_chunk = [&](int tile, int ck, uint8_t* l) {
+      const int col = ck * plan.pieces * 16;
+      const Rsrc r = rsrc_of(wc + (int64_t)tile * kRows * kb + col, max(rows_of(tile) * kb - col, 0));
+#pragma unroll
+      for (int i = 0; i < kSLoads; i++)
+        load_lds16(r, ck == CK - 1 ? off_last[i] : off[i], l + (i * kSWaves + wave) * 1024);
+    };
+    auto load_scales = [&](int tile, float* l) {
+      const Rsrc r = rsrc_of(wsc + (int64_t)tile * kRows, rows_of(tile) * 4);
+      if (tid < kRows)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 4, tid * 4, 0, 0, 0);
+    };
+    __syncthreads();  // the job before still reads the ring
+    if constexpr (kScAhead > 0) load_scales(tile, a0);
+    load_chunk(tile, 0, r0);
+    __builtin_amdgcn_sched_barrier(0);
+    // this wave's share of X
+    i32x4_t fx[kMT][CK][kUnits][4];
+    const int along = wave % kAlong, x_row = wave / kAlong % kX * 16 * kMT;
+#pragma unroll
+    for (int j = 0; j < kMT; j++) {
+      int64_t row = min(t.m0 + x_row + 16 * j + (lane & 15), t.m1 - 1);
+      if (GROUPED && a.x_rows) row = min((int64_t)max(a.x_rows[row], 0), a.x_rows_total - 1);
+      const int8_t* pc = a.xc + row * kb;
+#pragma unroll
+      for (int u = 0; u < CK; u++)
+#pragma unroll
+        for (int v = 0; v < kUnits; v++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int at = 16 * (along + v * kAlong) + 4 * (lane >> 4) + i;  // of the chunk's pieces
+            fx[j][u][v][i] = *(const i32x4_t*)(pc + min(u * plan.pieces + at, nb - 1) * 16);
+          }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kScAhead > 1) load_scales(tile + 1, a1);
+    load_chunk(tile + 1 / CK, 1 % CK, r1);
+    if constexpr (kRing > 3) load_chunk(tile + 2 / CK, 2 % CK, r2);
+    // Where the operands lie: worked out while the first loads are under way, hence
+    // from a lane number that the compiler cannot follow up to the kernel's start.
+    int at_lane = lane;
+    asm volatile("" : "+v"(at_lane));
+    const int g = at_lane >> 4, w_row = wave / (kAlong * kX) * kSRows + (at_lane & 15), mine = 16 * along + 4 * g;
+    // fragment i of W in a chunk; the next unit's lie kAlong * 256
+    // bytes on, as the exchange is within 16 pieces
+    int fo[4], fo_last[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int c = mine + i;
+      auto offset = [&](int pieces) {  // past the row: some other codes
+        return min(w_row * pieces + (c ^ key(pieces, w_row)), kSRows * kChunkB / 16 - 1 - 16 * kAlong * (kUnits - 1)) * 16;
+      };
+      fo_last[i] = offset(plan.last);
+      fo[i] = CK > 1 ? offset(plan.pieces) : fo_last[i];
+    }
+    // pieces that the chunk does not have add nothing
+#pragma unroll
+    for (int j = 0; j < kMT; j++)
+#pragma unroll
+      for (int u = 0; u < CK; u++)
+#pragma unroll
+        for (int v = 0; v < kUnits; v++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (mine + 16 * v * kAlong + i >= (u == CK - 1 ? plan.last : plan.pieces)) fx[j][u][v][i] = i32x4_t{};
+
+    // this thread's results: the scale of their row, and rows that padding leaves zero
+    bool none[kOuts];
+    float sx[kOuts];
+#pragma unroll
+    for (int i = 0; i < kOuts; i++) {
+      none[i] = false;
+      int64_t row = min(t.m0 + ((tid + i * 64 * kSWaves) % kSums >> 4), t.m1 - 1);
+      if (GROUPED && a.x_rows) {
+        row = a.x_rows[row];
+        none[i] = row < 0 || row >= a.x_rows_total;
+        if (none[i]) row = 0;
+      }
+      sx[i] = a.xs[row];
+    }
+    // y of a row tile, from set `set` of the waves' sums
+    auto finish = [&](int tile, int set, const float* sw) {
+#pragma unroll
+      for (int i = 0; i < kOuts; i++) {
+        const int o = tid + i * 64 * kSWaves;
+        const int n = o & 15, m = (RT == 1 ? o : o % kSums) >> 4, at_tile = RT == 1 ? 0 : o / kSums;
+        const int m_x = kX == 1 ? m : m % (16 * kMT);
+        const int64_t row = t.m0 + m;
+        const int col = tile * kRows + at_tile * kSRows + n;
+        if (o >= RT * kSums || row >= t.m1 || col >= n_rows) continue;
+        // lane (n / 4) * 16 + m % 16 of a wave holds it in element n % 4
+        const int* p = part + ((set * RT + at_tile) * kX + (kX == 1 ? 0 : m / (16 * kMT))) * kAlong * kPart + (m_x >> 4) * 256 +
+                       ((n >> 2) * 16 + (m_x & 15)) * 4 + (n & 3);
+        int v[kAlong];
+#pragma unroll
+        for (int w = 0; w < kAlong; w++) v[w] = p[w * kPart];
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kAlong; w++) sum += v[w];
+        float r = i8_scaled(sum, sx[i], sw[at_tile * kSRows + n]);
+        if (none[i]) r = 0.0f;
+        const int64_t at = row * a.n + n0 + col;
+        if (y_dtype == kF32) ((float*)a.y)[at] = r;
+        else if (y_dtype == kF16) ((_Float16*)a.y)[at] = mx_cvt<_Float16>(r);
+        else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(r);
+      }
+    };
+    auto meet = [&]() {  // once this wave's LDS accesses are done
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    i32x4_t acc[kMT];
+    // position P of a round: chunk P % CK of the row tile, ring place P % kRing;
+    // false behind the last row tile
+    auto chunk = [&](auto which) {
+      constexpr int P = decltype(which)::value, ck = P % CK, ahead = ck + kRing - 1;
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kSLoads*(kRing - 2)) : "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if constexpr (ck == 0) {
+        load_scales(tile + kScAhead, area(std::integral_constant<int, P / CK + kScAhead>{}));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kMT; j++) acc[j] = i32x4_t{0, 0, 0, 0};
+      }
+      load_chunk(tile + ahead / CK, ahead % CK, ring(std::integral_constant<int, P + kRing - 1>{}));
+      const uint8_t* l = ring(which);
+      auto unit_of = [&](auto which_unit) {
+        constexpr int v = decltype(which_unit)::value;
+        if (v > 0 && 16 * (along + v * kAlong) >= plan.last) return false;  // the row ends before it
+        i32x4_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = *(const i32x4_t*)(l + (ck == CK - 1 ? fo_last[i] : fo[i]) + v * kAlong * 256);
+#pragma unroll
+        for (int j = 0; j < kMT; j++) {
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[i], fx[j][ck][v][i], acc[j], 0, 0, 0);
+          asm volatile("" : "+v"(acc[j]));  // here, not behind the next barrier with all chunks' operands
+        }
+        return true;
+      };
+      for_each(unit_of, std::make_integer_sequence<int, kUnits>{});
+      if constexpr (kDefer && ck == 0)
+        if (tile > 0)
+          finish(tile - 1, (P / CK + kParts - 1) % kParts, area(std::integral_constant<int, P / CK + kAreas - 1>{}));
+      if constexpr (ck == CK - 1) {
+        int* sums = part + (P / CK % kParts * kSWaves + wave) * kPart;
+#pragma unroll
+        for (int j = 0; j < kMT; j++) *(i32x4_t*)(sums + j * 256 + lane * 4) = acc[j];
+        if constexpr (!kDefer) {
+          meet();
+          finish(tile, 0, area(std::integral_constant<int, P / CK>{}));
+        }
+        return ++tile < end;
+      }
+      return true;
+    };
+    while (for_each(chunk, std::make_integer_sequence<int, kRound>{})) {
+    }
+    if constexpr (kDefer) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      meet();
+      const int last = (end - 1) % kAreas;
+      finish(end - 1, (end - 1) % kParts, last == 0 ? a0 : last == 1 ? a1 : last == 2 ? a2 : a3);
+    }
+  }
+}
+
+template <int RT, int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, StreamPlan p, hipStream_t stream) {
+  const int64_t tiles = (a.n + kSRows - 1) / kSRows, full = (a.m + p.rows - 1) / p.rows;
+  const int64_t jobs = a.offsets ? std::min(full + a.experts, a.m) : full;
+  const int64_t grid = std::min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
+  if (!a.offsets) {
+    p.cuts = cuts_of((uint32_t)tiles, (uint32_t)jobs, (uint32_t)grid, RT);
+    if (p.cuts.per_job) p.mul_per_job = (1 << 20) / (int)p.cuts.per_job + 1;
+  }
+  const dim3 blocks((unsigned)grid), threads(64 * kSWaves);
+  if (a.offsets) hipLaunchKernelGGL((i8_stream_kernel<RT, CK, MT, true>), blocks, threads, 0, stream, a, y_dtype, p);
+  else hipLaunchKernelGGL((i8_stream_kernel<RT, CK, MT, false>), blocks, threads, 0, stream, a, y_dtype, p);
+  return hipGetLastError();
+}
+
+hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream_t s) {
+  if (p.rt == 4) return p.mt == 1 ? go_stream<4, 1, 1>(a, y_dtype, p, s) : go_stream<4, 1, 2>(a, y_dtype, p, s);
+  if (p.rt == 2) return p.mt == 1 ? go_stream<2, 1, 1>(a, y_dtype, p, s) : go_stream<2, 1, 2>(a, y_dtype, p, s);
+  switch (p.mt * 16 + p.ck) {
+    case 17: return go_stream<1, 1, 1>(a, y_dtype, p, s);
+    case 18: return go_stream<1, 2, 1>(a, y_dtype, p, s);
+    case 20: return go_stream<1, 4, 1>(a, y_dtype, p, s);
+    case 24: return go_stream<1, 8, 1>(a, y_dtype, p, s);
+    case 33: return go_stream<1, 1, 2>(a, y_dtype, p, s);
+    case 34: return go_stream<1, 2, 2>(a, y_dtype, p, s);
+    case 36: return go_stream<1, 4, 2>(a, y_dtype, p, s);
+    case 65: return go_stream<1, 1, 4>(a, y_dtype, p, s);
+    default: return go_stream<1, 2, 4>(a, y_dtype, p, s);
+  }
+}
+
 // y of the split tiles: adds the slices' sums.  A thread takes 16 sums of one fragment
 // in register order; the half-waves swap so that each lane stores runs of eight columns.
 template <int BM, typename OT>
@@ -464,13 +779,16 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 }  // namespace
 
 size_t i8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
+  i8::StreamPlan p;
   double us;
-  return i8::tile_ws_bytes(i8::tile_plan(m, n, k, experts, us));
+  return i8::streams(m, n, k, experts, p) ? 0 : i8::tile_ws_bytes(i8::tile_plan(m, n, k, experts, us));
 }
 
 hipError_t launch_i8_gemm(const I8Gemm& g, void* ws, hipStream_t stream) {
   const Args a = {g.x.codes, g.w.codes, g.x.scales, g.w.scales, g.m, g.n, g.k, g.x.rows, g.y, g.offsets, g.x_rows,
                   g.experts};
+  i8::StreamPlan p;
+  if (i8::streams(g.m, g.n, g.k, g.offsets ? g.experts : 0, p)) return run_stream(a, g.y_dtype, p, stream);
   if (g.y_dtype == kF32) return run<float>(a, ws, stream);
   if (g.y_dtype == kF16) return run<_Float16>(a, ws, stream);
   return run<__bf16>(a, ws, stream);
