@@ -14,6 +14,8 @@ Streams as in ``mx``.  No call has a backward.  The package re-exports every nam
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -43,6 +45,11 @@ class razer_combine(ctypes.Structure):
                 ("weights", ctypes.c_void_p), ("add", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
+# The structs as bytes, which cost a fifth of a ctypes instance to make
+_route_bytes = struct.Struct("qqiiiiiiiIf4xPPPPPPP").pack
+_combine_bytes = struct.Struct("qqqqqqi4xPPPPP").pack
+
+
 class MoeRoutes(NamedTuple):
     """experts, weights, slots: [tokens, top]; offsets: [E + 1]; rows: [tokens * top].  All are
     int32 but the weights, float32; offsets, rows and slots are None where no order was asked
@@ -57,8 +64,8 @@ class MoeRoutes(NamedTuple):
 def bind(L: ctypes.CDLL):
     """Argument types of the calls bound here."""
     vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
-    L.razer_moe_route.restype, L.razer_moe_route.argtypes = i32, [ctypes.POINTER(razer_route), vp, sz, vp]
-    L.razer_moe_combine.restype, L.razer_moe_combine.argtypes = i32, [ctypes.POINTER(razer_combine), vp]
+    L.razer_moe_route.restype, L.razer_moe_route.argtypes = i32, [vp, vp, sz, vp]
+    L.razer_moe_combine.restype, L.razer_moe_combine.argtypes = i32, [vp, vp]
     L.razer_moe_workspace_bytes.restype, L.razer_moe_workspace_bytes.argtypes = sz, [i64] * 3
 
 
@@ -66,17 +73,21 @@ def razer_moe_workspace_bytes(tokens: int, experts: int, top: int) -> int:
     return int(lib().razer_moe_workspace_bytes(tokens, experts, top))
 
 
+# a function of the sizes alone
+_workspace_bytes = functools.lru_cache(4096)(razer_moe_workspace_bytes)
+
+
 def _new_routes(tokens: int, experts: int, top: int, order: bool, space: int, device):
-    """(routes, the workspace behind them in the same buffer)"""
+    """(routes, the address of `space` bytes behind them in the same buffer)"""
     n = tokens * top
     head = (4 * n + experts + 1 if order else 2 * n) + 3 & ~3
-    buf = torch.empty(head + space // 4, dtype=torch.int32, device=device)
-    shape = tokens, top
-    chosen, weights = buf[:n].view(shape), buf[n:2 * n].view(torch.float32).view(shape)
+    buf = torch.empty(head + (space + 3 >> 2), dtype=torch.int32, device=device)
+    part, shape, strides = buf.as_strided, (tokens, top), (top, 1)
+    weights = part(shape, strides, n).view(torch.float32)
     if not order:
-        return MoeRoutes(chosen, weights, None, None, None), None
-    routes = MoeRoutes(chosen, weights, buf[4 * n:4 * n + experts + 1], buf[3 * n:4 * n], buf[2 * n:3 * n].view(shape))
-    return routes, buf[head:]
+        return MoeRoutes(part(shape, strides, 0), weights, None, None, None), None
+    return MoeRoutes(part(shape, strides, 0), weights, part((experts + 1,), (1,), 4 * n), part((n,), (1,), 3 * n),
+                     part(shape, strides, 2 * n)), buf.data_ptr() + 4 * head
 
 
 def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
@@ -120,13 +131,15 @@ def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", b
         ld = experts
     bias_at = None
     if bias is not None:
-        _check_buffer(bias, (experts,), dev, "bias", torch.float32)
+        if (not isinstance(bias, _Tensor) or bias.dtype is not torch.float32 or bias.get_device() != dev.index
+                or bias.shape != (experts,) or not bias.is_contiguous()):
+            _check_buffer(bias, (experts,), dev, "bias", torch.float32)
         bias_at = bias.data_ptr()
-    space, given = razer_moe_workspace_bytes(tokens, experts, top) if order else 0, out is not None
+    space, given = _workspace_bytes(tokens, experts, top) if order else 0, out is not None
+    ws = None
     if not given:
-        out, own = _new_routes(tokens, experts, top, order, 0 if workspace is not None else space, dev)
+        out, ws = _new_routes(tokens, experts, top, order, 0 if workspace is not None else space, dev)
     else:
-        own = None
         _check_buffer(out.experts, (tokens, top), dev, "out.experts", torch.int32)
         _check_buffer(out.weights, (tokens, top), dev, "out.weights", torch.float32)
         if order:
@@ -135,16 +148,16 @@ def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", b
             _check_buffer(out.slots, (tokens, top), dev, "out.slots", torch.int32)
     if workspace is not None:
         _check_buffer(workspace, None, dev, "workspace")
-        own = workspace
-    elif own is None and space:
-        own = torch.empty(space, dtype=torch.uint8, device=dev)
-    a = razer_route(tokens, max(ld, experts), experts, top, groups, kept, group_best, kind, dt,
-                    RAZER_ROUTE_RENORM if renormalise else 0, scale, logits.data_ptr(), bias_at,
-                    out.experts.data_ptr(), out.weights.data_ptr())
-    if order:
-        a.offsets, a.rows, a.slots = out.offsets.data_ptr(), out.rows.data_ptr(), out.slots.data_ptr()
-    status = lib().razer_moe_route(a, own.data_ptr() if own is not None else None,
-                                   own.nbytes if own is not None else 0, _stream(dev.index))
+        ws, space = workspace.data_ptr(), workspace.nbytes
+    elif given and space:
+        workspace = torch.empty(space, dtype=torch.uint8, device=dev)  # kept until the launch is enqueued
+        ws = workspace.data_ptr()
+    status = lib().razer_moe_route(
+        _route_bytes(tokens, max(ld, experts), experts, top, groups, kept, group_best, kind, dt,
+                     RAZER_ROUTE_RENORM if renormalise else 0, scale, logits.data_ptr(), bias_at or 0,
+                     out.experts.data_ptr(), out.weights.data_ptr(), out.offsets.data_ptr() if order else 0,
+                     out.rows.data_ptr() if order else 0, out.slots.data_ptr() if order else 0),
+        ws, space, _stream(dev.index))
     if status:
         _check(status, "razer_moe_route")
     if not given and _grad_enabled() and (logits.requires_grad or bias is not None and bias.requires_grad):
@@ -170,13 +183,17 @@ def razer_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
     dt = _dtype(kind)
     rows, cols = y.shape
     tokens, top = slots.shape
-    _check_buffer(slots, (tokens, top), dev, "slots", torch.int32)
-    _check_buffer(weights, (tokens, top), dev, "weights", torch.float32)
+    index = dev.index
+    if slots.dtype is not torch.int32 or slots.get_device() != index or not slots.is_contiguous():
+        _check_buffer(slots, (tokens, top), dev, "slots", torch.int32)
+    if (not isinstance(weights, _Tensor) or weights.dtype is not torch.float32 or weights.get_device() != index
+            or weights.shape != slots.shape or not weights.is_contiguous()):
+        _check_buffer(weights, (tokens, top), dev, "weights", torch.float32)
     if y.stride(1) != 1 or y.stride(0) < cols:
         y = y.contiguous()
     source = add
     if add is not None:
-        if not isinstance(add, _Tensor) or add.device != dev or add.shape != (tokens, cols) or add.dtype is not kind:
+        if not isinstance(add, _Tensor) or add.get_device() != index or add.shape != (tokens, cols) or add.dtype is not kind:
             raise ValueError(f"add must be {tokens}x{cols} of {kind} on {dev}")
         if add.stride(1) != 1 or add.stride(0) < cols:
             add = add.contiguous()
@@ -185,10 +202,10 @@ def razer_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
         out = torch.empty(tokens, cols, dtype=kind, device=dev)
     else:
         _check_buffer(out, (tokens, cols), dev, "out", kind)
-    a = razer_combine(tokens, top, cols, rows, max(y.stride(0), cols), 0 if add is None else max(add.stride(0), cols),
-                      dt, y.data_ptr(), slots.data_ptr(), weights.data_ptr(),
-                      None if add is None else add.data_ptr(), out.data_ptr())
-    status = lib().razer_moe_combine(a, _stream(dev.index))
+    status = lib().razer_moe_combine(
+        _combine_bytes(tokens, top, cols, rows, max(y.stride(0), cols), 0 if add is None else max(add.stride(0), cols), dt,
+                       y.data_ptr(), slots.data_ptr(), weights.data_ptr(), 0 if add is None else add.data_ptr(),
+                       out.data_ptr()), _stream(index))
     if status:
         _check(status, "razer_moe_combine")
     if not given and _grad_enabled() and (y.requires_grad or weights.requires_grad

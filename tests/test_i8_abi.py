@@ -90,8 +90,8 @@ def test_grouped_refuses(want, kw):
     (INVALID, dict(dtype=3)), (INVALID, dict(flags=2)), (INVALID, dict(logits=0)), (INVALID, dict(logits=X + 2)),
     (INVALID, dict(stride=31)), (INVALID, dict(stride=1 << 62)), (INVALID, dict(chosen=0)), (INVALID, dict(weights=0)),
     (INVALID, dict(weights=Y + 2)), (INVALID, dict(bias=Y + 1)), (INVALID, dict(rows=0)), (INVALID, dict(slots=0)),
-    (INVALID, dict(offsets=0)), (INVALID, dict(slots=Y + 3)), (INVALID, dict(space=0)), (INVALID, dict(ws=0)),
-    (INVALID, dict(ws=WS + 4)),
+    (INVALID, dict(offsets=0)), (INVALID, dict(slots=Y + 3)), (INVALID, dict(space=0, tokens=40)), (INVALID, dict(ws=0, tokens=40)),
+    (INVALID, dict(ws=WS + 4, tokens=40)),
     (UNSUPPORTED, dict(experts=1025, groups=1, groups_kept=1, stride=2000)), (UNSUPPORTED, dict(top=33)),
     (UNSUPPORTED, dict(tokens=1 << 29)), (OK, dict(tokens=0, offsets=0, rows=0, slots=0, logits=0, chosen=0, weights=0))])
 def test_route_refuses(want, kw):
@@ -205,7 +205,7 @@ def test_binding_refuses_before_it_writes():
         with pytest.raises(ValueError):
             call()
     for call in (lambda: rz.razer_moe_route(h, 33), lambda: rz.razer_moe_route(h, 2, group_best=3),
-                 lambda: rz.razer_moe_route(h, 2, workspace=off[:1]),
+                 lambda: rz.razer_moe_route(h.repeat(9, 1), 2, workspace=off[:1]),
                  lambda: rz.razer_moe_route(torch.zeros(2, 1025, device="cuda"), 2)):
         with pytest.raises(rz.RazerError):
             call()
