@@ -52,6 +52,21 @@ template <typename T> __device__ __forceinline__ T wave_max(T v) {
   v = max(v, dpp<0x143>(v, v));
   return lane_value(v, 63);
 }
+// The same of whole numbers, 0 where a lane has no source: a step is one instruction.
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
+  v = max(v, (uint32_t)dpp<0x111>(0, (int)v));
+  v = max(v, (uint32_t)dpp<0x112>(0, (int)v));
+  v = max(v, (uint32_t)dpp<0x114>(0, (int)v));
+  v = max(v, (uint32_t)dpp<0x118>(0, (int)v));
+  v = max(v, (uint32_t)dpp<0x142>(0, (int)v));
+  v = max(v, (uint32_t)dpp<0x143>(0, (int)v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// A whole number above 0 for each float but NaN, in the floats' order (zeros as one).
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = f2u(f + 0.0f);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
 __device__ __forceinline__ double wave_sum(double v) {
   v += dpp<0x111>(0.0, v);
   v += dpp<0x112>(0.0, v);
@@ -77,8 +92,8 @@ template <typename T, int V> __device__ __forceinline__ void load_row(const T* r
 // The experts of one token: lane j's place j, -1 and 0 for none (lanes from `top` on too).
 // `keys` is LDS of 64 V.
 //
-// Turns of choice compare the fp32 roundings of c, one DPP operation a step: rounding
-// keeps the order, so only entries of an equal rounding are compared in fp64.
+// Turns of choice compare the fp32 roundings of c, as whole numbers in their order:
+// rounding keeps the order, so only entries of an equal rounding are compared in fp64.
 template <int V>
 __device__ __forceinline__ void route_token(const MoeRoute& a, const float (&l)[V], const float (&bias)[V], double* keys,
                                             int& chosen, float& weight) {
@@ -154,39 +169,39 @@ __device__ __forceinline__ void route_token(const MoeRoute& a, const float (&l)[
     }
     wave_lds_sync();  // the next token writes the keys again
   }
-  float c32[V];
+  uint32_t key[V];  // 0: none
 #pragma unroll
-  for (int v = 0; v < V; v++) c32[v] = (float)c[v];
+  for (int v = 0; v < V; v++) key[v] = c[v] == kNone ? 0 : order_key((float)c[v]);
   for (int j = 0; j < a.top; j++) {
-    float best = c32[0];
+    uint32_t best = key[0];
 #pragma unroll
-    for (int v = 1; v < V; v++) best = fmaxf(best, c32[v]);
-    best = wave_max(best);
-    if (best == kNone32) break;
+    for (int v = 1; v < V; v++) best = max(best, key[v]);
+    best = wave_max_key(best);
+    if (best == 0) break;
     int at = -1, count = 0;
 #pragma unroll
     for (int v = V - 1; v >= 0; v--) {
-      const uint64_t equal = __ballot(c32[v] == best);
+      const uint64_t equal = __ballot(key[v] == best);
       count += __popcll(equal);
       if (equal) at = 64 * v + __builtin_ctzll(equal);
     }
     if (count == 1) {
 #pragma unroll
-      for (int v = 0; v < V; v++) c32[v] = c32[v] == best ? kNone32 : c32[v];
+      for (int v = 0; v < V; v++) key[v] = key[v] == best ? 0 : key[v];
     } else {
       double most = kNone;
 #pragma unroll
       for (int v = 0; v < V; v++)
-        if (c32[v] == best) most = max(most, c[v]);
+        if (key[v] == best) most = max(most, c[v]);
       most = wave_max(most);
 #pragma unroll
       for (int v = V - 1; v >= 0; v--) {
-        const uint64_t equal = __ballot(c32[v] == best && c[v] == most);
+        const uint64_t equal = __ballot(key[v] == best && c[v] == most);
         if (equal) at = 64 * v + __builtin_ctzll(equal);
       }
 #pragma unroll
       for (int v = 0; v < V; v++)
-        if (lane + 64 * v == at) c32[v] = kNone32;
+        if (lane + 64 * v == at) key[v] = 0;
     }
     if (lane == j) chosen = at;
   }
