@@ -61,4 +61,40 @@ __device__ __forceinline__ int live_tiles(const int32_t* offsets, int experts, i
   return __builtin_amdgcn_readfirstlane(cnt);
 }
 
+// The same for a kernel that looks tiles up more than once: what lane l counts for expert l
+// stays in registers, if there are no more than 64.
+struct RowTiles {
+  int lo, hi, cnt, sum;  // lane l: expert l's rows, its tiles, and those of the experts up to it
+  int count;             // of all experts
+};
+__device__ __forceinline__ RowTiles row_tiles(const int32_t* offsets, int experts, int64_t m_rows, int rows) {
+  const int lane = threadIdx.x & 63, m = (int)m_rows;
+  RowTiles r = {};
+  if (experts > 64) {
+    r.count = live_tiles(offsets, experts, m_rows, rows);
+    return r;
+  }
+  if (lane < experts) {
+    r.lo = min(max(offsets[lane], 0), m);
+    r.hi = min(max(offsets[lane + 1], r.lo), m);
+  }
+  r.cnt = r.sum = (r.hi - r.lo + rows - 1) / rows;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(r.sum, o, 64);
+    if (lane >= o) r.sum += up;
+  }
+  r.count = __builtin_amdgcn_readlane(r.sum, 63);
+  return r;
+}
+__device__ __forceinline__ Tile find_tile(const RowTiles& r, const int32_t* offsets, int experts, int64_t m_rows, int rows,
+                                          int64_t t) {
+  if (experts > 64) return find_tile(offsets, experts, m_rows, rows, t);
+  const uint64_t hit = __ballot(r.sum > t);
+  if (!hit) return {0, 0, -1};
+  const int src = __builtin_ctzll(hit);
+  const int m0 = __builtin_amdgcn_readlane(r.lo, src) + (int)(t - __builtin_amdgcn_readlane(r.sum - r.cnt, src)) * rows;
+  return {m0, min(m0 + rows, __builtin_amdgcn_readlane(r.hi, src)), src};
+}
+
 }  // namespace rz

@@ -46,12 +46,14 @@ __device__ __forceinline__ void load_lds16(Rsrc r, uint32_t offset, uint8_t* l) 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, (int)offset, 0, 0, 0);
 }
 
-// The workgroup's barrier, once all of this wave's loads but the last LEFT have arrived
-// and its LDS accesses are done.  (The wait is the builtin, which the compiler counts
-// with: it would put one of its own, for all loads, ahead of a loop's first LDS read.)
-template <int LEFT> __device__ __forceinline__ void wait_and_meet() {
+// The operand of s_waitcnt for at most VM loads and stores, and LGKM LDS accesses, under
+// way.  (The builtin, which the compiler counts with: after waits that it does not know of
+// it puts its own, for all loads, ahead of a loop's first LDS read.)
+constexpr int vm_lgkm(int vm, int lgkm) { return (vm & 15) | (vm & 48) << 10 | 0x70 | lgkm << 8; }
+
+// The workgroup's barrier.
+__device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((LEFT & 15) | (LEFT & 48) << 10 | 0x70);  // vmcnt(LEFT) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -114,15 +116,9 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     return i == 0 ? x0 : i == 1 ? x1 : x2;
   };
 
-  // ---- the tile at hand
-  int64_t n0;
-  Tile t;
-  int nb, slot;                                  // pieces of its slice of K; slot of `part` or -1
-  Rsrc wc, xc;
-  uint32_t ow[NL], ox[ML];                       // direct load i of this lane: bytes from wc, xc
-  float sw, sx;                                  // of the tile's column, and row, tid
-  bool none;                                     // that row is padding
-  const int mt = GROUPED ? live_tiles(a.offsets, a.experts, a.m, BM) : plan.mt;
+  const bool gather = GROUPED && a.x_rows;
+  const RowTiles tiles = GROUPED ? row_tiles(a.offsets, a.experts, a.m, BM) : RowTiles{};
+  const int mt = GROUPED ? tiles.count : plan.mt;
   const int full = GROUPED ? mt * plan.nt : plan.full;
   const int items = full + plan.rest * plan.split;
   // Consecutive workgroups go to the eight XCDs in turn: of every round of tiles
@@ -130,16 +126,26 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
   const int grid = gridDim.x, b = blockIdx.x;
   const int place = (b % 8) * (grid / 8) + min(b % 8, grid % 8) + b / 8;
   const int chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
-  auto set_tile = [&](int item) {
-    int im, in, pos = item, b0 = 0;
-    nb = all_nb;
-    slot = -1;
+
+  // Where a tile is.
+  struct Spot {
+    Tile t;
+    int64_t n0;
+    int b0, nb, slot;  // first piece and pieces of its slice of K; slot of `part` or -1
+    __device__ int x_last() const { return (int)max(t.m1 - t.m0, (int64_t)1) - 1; }
+  };
+  auto locate = [&](int item) {
+    int im, in, pos = item;
+    Spot o;
+    o.b0 = 0;
+    o.nb = all_nb;
+    o.slot = -1;
     if (!GROUPED && item >= full) {
-      slot = item - full;
-      pos = full + slot / plan.split;
-      const int s = slot % plan.split, steps = (all_nb + 7) / 8;
-      b0 = steps * s / plan.split * 8;
-      nb = min(steps * (s + 1) / plan.split * 8, all_nb) - b0;
+      o.slot = item - full;
+      pos = full + o.slot / plan.split;
+      const int s = o.slot % plan.split, steps = (all_nb + 7) / 8;
+      o.b0 = steps * s / plan.split * 8;
+      o.nb = min(steps * (s + 1) / plan.split * 8, all_nb) - o.b0;
     }
     if (!GROUPED && BM == 128 && plan.halves) {  // half `item % 2` of a tile of twice the height
       tile_place(plan.first + item / 2, mt, plan.nt, im, in);
@@ -148,38 +154,51 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       tile_place(pos, mt, plan.nt, im, in);
     }
     if (GROUPED)
-      t = find_tile(a.offsets, a.experts, a.m, BM, im);
+      o.t = find_tile(tiles, a.offsets, a.experts, a.m, BM, im);
     else  // a half behind the last row has none: what is read for it is the last one
-      t = Tile{min((int64_t)im * BM, a.m), min((int64_t)(im + 1) * BM, a.m), 0};
-    n0 = (int64_t)in * BN;
-    const int64_t wr = (int64_t)t.expert * a.n + n0;
-    const int w_rows = (int)min((int64_t)BN, a.n - n0), x_rows = (int)(t.m1 - t.m0), x_last = max(x_rows, 1) - 1;
-    int64_t xr[ML];
+      o.t = Tile{min((int64_t)im * BM, a.m), min((int64_t)(im + 1) * BM, a.m), 0};
+    o.n0 = (int64_t)in * BN;
+    return o;
+  };
+  // The rows of X of this lane's direct loads, from the tile's first or as they are gathered,
+  // and of the scale that it passes on.
+  struct Rows {
+    int x[ML], scale;
+  };
+  auto rows_of = [&](const Spot& o) {
+    Rows r;
+    const int last = o.x_last();
 #pragma unroll
-    for (int i = 0; i < ML; i++) xr[i] = min((4 * i + wave) * 8 + (lane >> 3), x_last);
-    const bool gather = GROUPED && a.x_rows;
+    for (int i = 0; i < ML; i++) r.x[i] = min((4 * i + wave) * 8 + (lane >> 3), last);
+    r.scale = min(tid % BM, last);
     if (gather) {
+      const int32_t* p = a.x_rows + o.t.m0;
 #pragma unroll
-      for (int i = 0; i < ML; i++) xr[i] = a.x_rows[t.m0 + xr[i]];
-#pragma unroll
-      for (int i = 0; i < ML; i++) xr[i] = min(max(xr[i], (int64_t)0), a.x_rows_total - 1);
+      for (int i = 0; i < ML; i++) r.x[i] = p[r.x[i]];
+      r.scale = p[r.scale];
     }
-    const int64_t x_first = gather ? 0 : min(t.m0, a.m - 1), x_span = gather ? a.x_rows_total : x_last + 1;
-    wc = rsrc_of(a.wc + wr * a.k + b0 * 16, w_rows * a.k - b0 * 16);
-    xc = rsrc_of(a.xc + x_first * a.k + b0 * 16, x_span * a.k - b0 * 16);
+    return r;
+  };
+  // What the loads of the tile at hand go by.
+  Rsrc wc, xc;
+  int nb;
+  uint32_t ow[NL], ox[ML];                       // direct load i of this lane: bytes from wc, xc
+  float sw, sx;                                  // of the tile's column, and row, tid
+  bool none;                                     // that row is padding
+  auto aim = [&](const Spot& o, const Rows& r) {
+    const int64_t wr = (int64_t)o.t.expert * a.n + o.n0;
+    const int w_rows = (int)min((int64_t)BN, a.n - o.n0);
+    const int64_t first = gather ? 0 : min(o.t.m0, a.m - 1), span = gather ? a.x_rows_total : o.x_last() + 1;
+    nb = o.nb;
+    wc = rsrc_of(a.wc + wr * a.k + o.b0 * 16, w_rows * a.k - o.b0 * 16);
+    xc = rsrc_of(a.xc + first * a.k + o.b0 * 16, span * a.k - o.b0 * 16);
 #pragma unroll
     for (int i = 0; i < NL; i++) ow[i] = (uint32_t)(min((4 * i + wave) * 8 + (lane >> 3), w_rows - 1) * a.k);
 #pragma unroll
-    for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(xr[i] * a.k);
-    int64_t row = min(t.m0, a.m - 1) + min(tid % BM, x_last);
-    none = false;
-    if (gather) {
-      row = a.x_rows[row];
-      none = row < 0 || row >= a.x_rows_total;
-      if (none) row = 0;
-    }
+    for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(min((int64_t)max(r.x[i], 0), span - 1) * a.k);
+    none = r.scale < 0 || r.scale >= span;
     sw = a.ws[wr + min(tid, w_rows - 1)];
-    sx = a.xs[row];
+    sx = a.xs[first + (none ? 0 : r.scale)];
   };
   auto load_w = [&](int s, uint8_t* l) {
     const int piece = s * 8 + chunk;
@@ -234,7 +253,9 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
 
   int item = place;
   if (item >= items) return;
-  set_tile(item);
+  Spot spot = locate(item);
+  Rows rows_at = rows_of(spot);
+  aim(spot, rows_at);
   load_x(0, x0);
   load_w(0, w0);
   load_x(1, x1);
@@ -248,8 +269,13 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
         for (int e = 0; e < 16; e++) acc[i][j][e] = 0;
     const int steps = (nb + 7) / 8;
     int s = 0;
-    wait_and_meet<NL + ML>();
+    __builtin_amdgcn_s_waitcnt(vm_lgkm(NL + ML, 0));
+    meet();
     Frags f = read_frags(w0, x0, 0), g;
+    // Where the next tile is: its row numbers arrive under this one's steps.
+    item += grid;
+    const Spot next = locate(min(item, items - 1));
+    const Rows next_rows = rows_of(next);
     // position P of the rings: products 0 to 2 of step s, and the fragments of product 3
     auto front = [&](auto which) {
       constexpr int P = decltype(which)::value;
@@ -271,7 +297,8 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     auto step = [&](auto which) {
       constexpr int P = decltype(which)::value;
       typedef std::integral_constant<int, P + 1> Next;
-      wait_and_meet<ML>();
+      __builtin_amdgcn_s_waitcnt(vm_lgkm(ML, 0));
+      meet();
       f = read_frags(w_place(Next{}), x_place(Next{}), 0);
       load_w(s + 2, w_place(which));
       products(g);
@@ -286,23 +313,23 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     }
 
     // ---- this tile's results, under which the next one's first steps are loaded
-    const Tile done = t;
-    const int64_t dn0 = n0;
-    const int dslot = slot;
-    item += grid;
+    const Spot done = spot;
     uint8_t* scl = BM == 256 ? x2 + kOut : own;
-    wait_and_meet<0>();  // nothing of this tile is under way or read any more
+    __builtin_amdgcn_s_waitcnt(vm_lgkm(0, 0));  // nothing of this tile is under way
+    meet();                                     // or read any more
     *(float*)(scl + tid * 4) = sw;
     if (BM == 256 || tid < BM) *(float*)(scl + (BN + tid) * 4) = sx;
     if (GROUPED) *(uint64_t*)(scl + (BN + BM) * 4 + wave * 8) = __ballot(none);
-    wait_and_meet<0>();
     if (item < items) {
-      set_tile(item);
+      spot = next;
+      aim(next, next_rows);
       load_x(0, x0);
       load_w(0, w0);
       load_x(1, x1);
       load_w(1, w1);
     }
+    __builtin_amdgcn_s_waitcnt(vm_lgkm(63, 0));
+    meet();
     __builtin_amdgcn_sched_barrier(0);
     // The accumulators are taken out of their registers where they are written, not
     // all at once, and the addresses are worked out here, not kept from before the
@@ -310,8 +337,8 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int half = lane >> 5, l32 = lane & 31;
-    if (!GROUPED && dslot >= 0) {  // a slice's sums, in the order of the registers
-      i32x4_t* p = (i32x4_t*)(plan.part + (int64_t)dslot * BM * BN) + wave * (NI * MI * 4 * 64) + lane;
+    if (!GROUPED && done.slot >= 0) {  // a slice's sums, in the order of the registers
+      i32x4_t* p = (i32x4_t*)(plan.part + (int64_t)done.slot * BM * BN) + wave * (NI * MI * 4 * 64) + lane;
 #pragma unroll
       for (int i = 0; i < NI; i++)
 #pragma unroll
@@ -326,15 +353,19 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       // Through LDS, in the third place of the ring of X, to be stored in whole 128-byte lines.
       typedef OT V4 __attribute__((ext_vector_type(4)));
       constexpr int kCols = 128 / sizeof(OT), kPer = 16 / sizeof(OT), kFr = kCols / 32;  // columns of a pass, a store
-      const int rows = (int)(done.m1 - done.m0), cols = (int)min(a.n - dn0, (int64_t)BN);
+      const int rows = (int)(done.t.m1 - done.t.m0), cols = (int)min(a.n - done.n0, (int64_t)BN);
       uint8_t* o = x2 + wave * (32 * 128);
       const int r0 = lane >> 3, c0 = (lane & 7) * kPer;  // of a store within its 8 rows
-      OT* y = (OT*)a.y + (done.m0 + wm + r0) * a.n + dn0 + wn + c0;
+      OT* y = (OT*)a.y + (done.t.m0 + wm + r0) * a.n + done.n0 + wn + c0;
       const float* csw = (const float*)scl + wn + half * 4;
       constexpr int kPasses = MI * NI / kFr;  // 32 rows and kCols columns each
       V4 v[kFr * 4];
+      f32x4_t s4[kFr * 4];                    // scales of a pass's columns, the same for the passes of all rows
       auto convert = [&](int pass) {
-        const int j = pass / (NI / kFr), p = pass % (NI / kFr), m = wm + j * 32 + l32;  // this lane's row
+        const int j = pass % MI, p = pass / MI, m = wm + j * 32 + l32;  // this lane's row
+        if (j == 0)
+#pragma unroll
+          for (int i = 0; i < kFr * 4; i++) s4[i] = *(const f32x4_t*)(csw + p * kCols + i * 8);
         const float rsx = *(const float*)(scl + (BN + m) * 4);
         const bool zero = GROUPED && (scl[(BN + BM) * 4 + (m >> 3)] >> (m & 7) & 1);
 #pragma unroll
@@ -343,16 +374,15 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
           for (int q = 0; q < 4; q++) {
             i32x16_t& c = acc[p * kFr + i][j];
             if (q == 0) asm volatile("" : "+a"(c));
-            const f32x4_t s4 = *(const f32x4_t*)(csw + (p * kFr + i) * 32 + q * 8);
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[i * 4 + q][e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], rsx, s4[e]));
+            for (int e = 0; e < 4; e++) v[i * 4 + q][e] = mx_cvt<OT>(i8_scaled(c[q * 4 + e], rsx, s4[i * 4 + q][e]));
             if (zero) v[i * 4 + q] = V4{};
           }
       };
       convert(0);
 #pragma unroll
       for (int pass = 0; pass < kPasses; pass++) {
-        const int j = pass / (NI / kFr), p = pass % (NI / kFr);
+        const int j = pass % MI, p = pass / MI;
 #pragma unroll
         for (int i = 0; i < kFr; i++)
 #pragma unroll
@@ -608,10 +638,9 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
         else ((__bf16*)a.y)[at] = mx_cvt<__bf16>(r);
       }
     };
-    auto meet = [&]() {  // once this wave's LDS accesses are done
+    auto meet_lds = [&]() {  // once this wave's LDS accesses are done
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+      meet();
     };
     i32x4_t acc[kMT];
     // position P of a round: chunk P % CK of the row tile, ring place P % kRing;
@@ -653,7 +682,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
 #pragma unroll
         for (int j = 0; j < kMT; j++) *(i32x4_t*)(sums + j * 256 + lane * 4) = acc[j];
         if constexpr (!kDefer) {
-          meet();
+          meet_lds();
           finish(tile, 0, area(std::integral_constant<int, P / CK>{}));
         }
         return ++tile < end;
@@ -664,7 +693,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
     }
     if constexpr (kDefer) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      meet();
+      meet_lds();
       const int last = (end - 1) % kAreas;
       finish(end - 1, (end - 1) % kParts, last == 0 ? a0 : last == 1 ? a1 : last == 2 ? a2 : a3);
     }
