@@ -30,10 +30,20 @@ struct TilePlan {
   int32_t* part;
 };
 
-// us that a step of a tile of 256 or 128 rows takes in a full round, and in one that
-// leaves CUs (and power) to spare; what slices cost, their sums written and read.
-inline double step_us(int high, bool full) { return high == 256 ? full ? 1.5 : 1.3 : full ? 0.9 : 0.8; }
-inline double fold_us(int slices, int high) { return 4.0 + slices * high * (0.1 / 256); }
+// us that a round of `tiles` tiles takes: a step of 256 or 128 rows, the longer the more of
+// them there are (they share the memory's and the card's power), and a tile's first loads
+// and results; what slices cost, their sums written and read, and another launch.
+// Measured, 256 rows, 128 rows, and as chosen here:
+//   1024 x 14336 x 4096  57.8  72.0  57.8     512 x 28672 x 8192   111  143  111
+//   2048 x 4096 x 4096   43.5  35.8  35.8     1024 x 4096 x 4096  42.0 28.0 28.0
+//   2048 x 28672 x 8192   408   478   393     1024 x 4096 x 14336  119 76.5 76.4
+//   8192 rows, 8 experts of 14336 x 4096  458  540  460
+//   8192 rows, 64 experts of 1536 x 2048 71.2 73.4 73.2, 16384 rows 102 93.1 92.9
+inline double round_us(int high, double tiles, int cus, int steps) {
+  const double f = std::min(tiles / cus, 1.0);
+  return high == 256 ? steps * (0.85 + 0.62 * f) + 10.0 : steps * (0.48 + 0.5 * f) + 6.0;
+}
+inline double fold_us(int slices, int high) { return 3.0 + slices * high * 2.5e-4; }
 inline int steps_of(int64_t k) { return (int)((k + kStepB - 1) / kStepB); }
 
 // The tiles of a product, `high` rows each, and its time in us.  The last, partly
@@ -46,24 +56,26 @@ inline TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t expe
   p.mt = (int)((m + high - 1) / high + std::min(experts, m));
   p.full = (int)std::min((int64_t)p.mt * p.nt, (int64_t)INT32_MAX);  // more have no memory for their results
   p.split = 1;
+  auto rounds_us = [&](double tiles) {
+    const double rounds = std::floor(tiles / cus), rest = tiles - rounds * cus;
+    return rounds * round_us(high, cus, cus, steps) + (rest > 0 ? round_us(high, rest, cus, steps) : 0);
+  };
   if (experts) {  // of about the same number of rows, whose last tile is half full
     const int64_t parts = std::min(experts, m);
-    const double tiles = (double)p.nt * std::max(parts, m / high + parts / 2), rounds = std::floor(tiles / cus);
-    us = (rounds * step_us(high, true) + (tiles > rounds * cus ? step_us(high, false) : 0)) * steps;
+    us = rounds_us((double)p.nt * std::max(parts, m / high + parts / 2));
     return p;
   }
+  us = rounds_us(p.full);
   const int rest = p.full % cus;
-  double best = rest ? steps * step_us(high, false) : 0;
+  const double whole = rounds_us(p.full - rest);
   for (int s = 2; s <= 8 && rest > 0 && rest * s <= cus && s <= steps; s++) {
-    const double t = (steps + s - 1) / s * step_us(high, false) + fold_us(rest * s, high);
-    if (t < best) best = t, p.split = s;
+    const double t = whole + round_us(high, rest * s, cus, (steps + s - 1) / s) + fold_us(rest * s, high);
+    if (t < us) us = t, p.split = s;
   }
-  if (high == 256 && rest * 2 <= cus && steps * step_us(128, true) + 6.0 < best) {
-    best = steps * step_us(128, true) + 6.0;
-    p.halves = rest;
-    p.split = 1;
+  if (high == 256 && rest > 0 && rest * 2 <= cus) {
+    const double t = whole + round_us(128, rest * 2, cus, steps) + 6.0;
+    if (t < us) us = t, p.split = 1, p.halves = rest;
   }
-  us = p.full / cus * step_us(high, true) * steps + best;
   if (p.split > 1) p.rest = rest, p.full -= rest;
   return p;
 }
@@ -142,25 +154,37 @@ inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) 
 }
 
 // Whether a product runs on the stream kernel: the shorter time of two estimates, in us.
-// Both take what the kernel's own work and the read of W come to, one of them half
-// hidden behind the other, and what a launch costs.
+// The stream kernel's work is its row tiles, whose sums meet in LDS, and half of the
+// shorter of this and the read of W shows beside the other; the tile kernel's its rounds,
+// and not quite half of the read shows.  Measured, stream and tile kernel:
+//   27 x 28672 x 8192   51.1 and 65.1    128 x 28672 x 8192   81.9 and 68.1
+//   128 x 14336 x 4096  22.3 and 24.2    256 x 14336 x 4096   31.7 and 28.6
+//   256 x 4096 x 4096   17.7 and 21.1    1024 x 4096 x 4096   34.8 and 28.0
+//   64 x 4096 x 14336   23.8 and 25.0    256 x 4096 x 14336   54.1 and 30.2
+//   128 x 8192 x 1024   11.7 and 12.2    512 x 8192 x 1024    24.3 and 13.7
+//   8 experts of 14336 x 4096, 64 rows each 116 and 106, 128 rows 207 and 143
+//   64 experts of 1536 x 2048, 8 rows each 37.0 and 47.9, 32 rows 54.9 and 54.4
+struct Estimate {
+  double stream, tile;
+};
+inline Estimate estimate(int64_t m, int64_t n, int64_t k, int64_t experts, const StreamPlan& p) {
+  const int cus = device_cu_count();
+  const int64_t parts = experts ? std::min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
+  const double read = (double)parts * n * k / 5e6;
+  const int64_t jobs = (rows + p.rows - 1) / p.rows;  // of each W
+  const double units = (double)parts * jobs * ((n + kSRows * p.rt - 1) / (kSRows * p.rt));
+  const double work = std::ceil(units / cus) * (0.22 * p.mt + 0.4 * p.ck);
+  // an expert's jobs read its W one after the other; those of one product side by side
+  const double streamed = experts ? read * jobs : read;
+  double tile;
+  tile_plan(m, n, k, experts, tile);
+  return {std::max(work, streamed) + std::min(work, streamed) / 2 + 2.5 + 0.3 * p.ck * p.mt, tile + 0.45 * read};
+}
 inline bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
   p = stream_plan(m, n, k, experts);
   if (!p.ck) return false;
-  const int cus = device_cu_count();
-  const int64_t parts = experts ? std::min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
-  auto whole = [](double us) { return (int)std::min(us, 1e9); };
-  const int read = whole((double)parts * n * k / 5e6);
-  auto rounds = [&](int64_t units) { return (double)((units + cus - 1) / cus); };
-  auto total = [&](double us, double fixed) {
-    const int work = whole(us);
-    return std::max(work, read) + std::min(work, read) / 2 + fixed;
-  };
-  const double stream = rounds(parts * ((rows + p.rows - 1) / p.rows) * ((n + kSRows * p.rt - 1) / (kSRows * p.rt))) *
-                        (0.25 * p.mt + 0.3 * p.ck);
-  double tile;
-  tile_plan(m, n, k, experts, tile);
-  return total(stream, 3.0 + 0.4 * p.ck * p.mt) <= total(tile, 4.0);  // X is loaded first
+  const Estimate e = estimate(m, n, k, experts, p);
+  return e.stream <= e.tile;
 }
 
 }  // namespace i8
