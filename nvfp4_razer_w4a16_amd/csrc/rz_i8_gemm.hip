@@ -7,8 +7,8 @@
 // are stored, 16 bytes of a row a lane; the order of K within a product is free as long
 // as both agree.
 //
-// Out of range: rows are clamped to the last one (their results are not stored).  Pieces
-// of W past K read as zeros, so that whatever is read of X there adds nothing.
+// Out of range: rows are clamped to the last one (their results are not stored); pieces
+// past K read as zeros.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -39,7 +39,7 @@ typedef __amdgpu_buffer_rsrc_t Rsrc;
 __device__ __forceinline__ Rsrc rsrc_of(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
 }
-constexpr uint32_t kPastW = 0x7FFFFFFFu;  // past every tile of W
+constexpr uint32_t kPast = 0xFFFFFFF0u;  // past all that a descriptor holds
 
 // 16 bytes a lane straight to LDS, lane i's at l + 16 i.
 __device__ __forceinline__ void load_lds16(Rsrc r, uint32_t offset, uint8_t* l) {
@@ -203,12 +203,12 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
   auto load_w = [&](int s, uint8_t* l) {
     const int piece = s * 8 + chunk;
 #pragma unroll
-    for (int i = 0; i < NL; i++) load_lds16(wc, piece < nb ? ow[i] + piece * 16 : kPastW, l + (4 * i + wave) * 1024);
+    for (int i = 0; i < NL; i++) load_lds16(wc, piece < nb ? ow[i] + piece * 16 : kPast, l + (4 * i + wave) * 1024);
   };
   auto load_x = [&](int s, uint8_t* l) {
-    const uint32_t col = (uint32_t)min(s * 8 + chunk, nb - 1) * 16;
+    const int piece = s * 8 + chunk;
 #pragma unroll
-    for (int i = 0; i < ML; i++) load_lds16(xc, ox[i] + col, l + (4 * i + wave) * 1024);
+    for (int i = 0; i < ML; i++) load_lds16(xc, piece < nb ? ox[i] + piece * 16 : kPast, l + (4 * i + wave) * 1024);
   };
 
   struct Frags {
@@ -224,6 +224,13 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     return f;
   };
   i32x16_t acc[NI][MI];
+  auto first_products = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+      for (int j = 0; j < MI; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], i32x16_t{}, 0, 0, 0);
+  };
   auto products = [&](const Frags& f) {
 #pragma unroll
     for (int i = 0; i < NI; i++)
@@ -261,12 +268,6 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
   load_x(1, x1);
   load_w(1, w1);
   while (true) {
-#pragma unroll
-    for (int i = 0; i < NI; i++)
-#pragma unroll
-      for (int j = 0; j < MI; j++)
-#pragma unroll
-        for (int e = 0; e < 16; e++) acc[i][j][e] = 0;
     const int steps = (nb + 7) / 8;
     int s = 0;
     __builtin_amdgcn_s_waitcnt(vm_lgkm(NL + ML, 0));
@@ -278,11 +279,14 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     const Rows next_rows = rows_of(next);
     // position P of the rings: products 0 to 2 of step s, and the fragments of product 3
     auto front = [&](auto which) {
-      constexpr int P = decltype(which)::value;
+      constexpr int P = decltype(which)::value;  // 0 for the tile's first step alone
       uint8_t *lw = w_place(which), *lx = x_place(which);
       g = read_frags(lw, lx, 1);
       load_x(s + 2, x_place(std::integral_constant<int, P + 2>{}));
-      products(f);
+      if constexpr (P == 0)
+        first_products(f);
+      else
+        products(f);
       spread(NI + MI, ML);
       f = read_frags(lw, lx, 2);
       products(g);
@@ -292,9 +296,9 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       spread(NI + MI, 0);
       pin();
     };
-    // product 3 of step s behind the barrier, then the next step's front.  The loads run
-    // past the slice's end, where they read nothing of use.
-    auto step = [&](auto which) {
+    // product 3 of step s behind the barrier.  The loads run past the slice's end, where
+    // they read nothing of use.
+    auto back = [&](auto which) {
       constexpr int P = decltype(which)::value;
       typedef std::integral_constant<int, P + 1> Next;
       __builtin_amdgcn_s_waitcnt(vm_lgkm(ML, 0));
@@ -304,13 +308,25 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       products(g);
       spread(NI + MI, NL);
       pin();
-      if (++s >= steps) return false;
-      front(Next{});
+      s++;
+    };
+    auto step = [&](auto which) {
+      back(which);
+      front(std::integral_constant<int, decltype(which)::value + 1>{});
+      return true;
+    };
+    auto last_steps = [&](auto which) {
+      back(which);
+      if (s >= steps) return false;
+      front(std::integral_constant<int, decltype(which)::value + 1>{});
       return true;
     };
     front(std::integral_constant<int, 0>{});
-    while (for_each(step, std::make_integer_sequence<int, 6>{})) {
-    }
+    // Whole turns of both rings, then one to six steps.  (With a way out behind every step the
+    // compiler waits for all loads at the loop's start, whose LDS any of the ways may have
+    // loaded last.)
+    for (int turns = (steps - 1) / 6; turns > 0; turns--) for_each(step, std::make_integer_sequence<int, 6>{});
+    for_each(last_steps, std::make_integer_sequence<int, 6>{});
 
     // ---- this tile's results, under which the next one's first steps are loaded
     const Spot done = spot;
