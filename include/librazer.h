@@ -498,7 +498,8 @@ size_t razer_i8_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts
 enum { RAZER_SCORE_SOFTMAX = 0, RAZER_SCORE_SIGMOID = 1 };
 enum { RAZER_ROUTE_RENORM = 1u };
 typedef struct razer_route {
-  int64_t tokens;      /* >= 0; tokens * top < 2^30 */
+  int64_t tokens;      /* >= 0; tokens * top < 2^30, tokens <= 2^26, with an order 2^20 (RAZER_E_UNSUPPORTED above:
+                          longer batches are routed in parts) */
   int64_t stride;      /* elements from row to row of logits, >= experts */
   int32_t experts;     /* 1 .. RAZER_MOE_MAX_EXPERTS (RAZER_E_UNSUPPORTED above) */
   int32_t top;         /* 1 .. RAZER_MOE_MAX_TOP, at most the experts of the groups kept */
@@ -535,7 +536,7 @@ typedef struct razer_combine {
   const int32_t* slots;      /* device [tokens, top] */
   const float* weights;      /* device [tokens, top] */
   const void* add;           /* device [tokens, cols], such as the residual or a shared expert's output; NULL: zeros */
-  void* out;                 /* device [tokens, cols]; may be add (if its rows are contiguous) */
+  void* out;                 /* device [tokens, cols]; may be add (if its rows are contiguous), not in memory that y holds */
 } razer_combine;
 razer_status razer_moe_combine(const razer_combine* a, void* stream);
 

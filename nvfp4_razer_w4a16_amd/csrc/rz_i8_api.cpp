@@ -22,6 +22,8 @@ int64_t dtype_size(int dt) { return dt == RAZER_F32 ? 4 : 2; }
 constexpr int64_t kMaxElems = (int64_t)1 << 34;   // 8 elements a thread, a launch has fewer than 2^32 threads
 constexpr int64_t kMaxGemmRows = (int64_t)1 << 30;
 constexpr int64_t kMaxPairs = (int64_t)1 << 30;   // of a token and a place
+constexpr int64_t kMaxTokens = (int64_t)1 << 26;  // blocks of 1024 threads, 16 or 32 tokens each, in one launch
+constexpr int64_t kMaxOrdered = (int64_t)1 << 20; // every block reads the sums of all groups of blocks
 
 razer_status check_i8(const razer_i8* t) {
   if (!t || t->rows < 0 || t->cols < 0 || t->cols % 16 != 0) return RAZER_E_INVALID;
@@ -144,7 +146,7 @@ razer_status razer_moe_route(const razer_route* a, void* ws, size_t ws_bytes, vo
   const void* words[] = {a->bias, a->chosen, a->weights, a->offsets, a->rows, a->slots};
   for (const void* p : words)
     if (!aligned(p, 4)) return RAZER_E_INVALID;
-  if (a->tokens >= kMaxPairs / a->top) return RAZER_E_UNSUPPORTED;
+  if (a->tokens >= kMaxPairs / a->top || a->tokens > (order ? kMaxOrdered : kMaxTokens)) return RAZER_E_UNSUPPORTED;
   if (a->tokens > 0) {
     if (!a->chosen || !a->weights || !rows_ok(a->logits, a->tokens, a->stride, a->experts, a->dtype))
       return RAZER_E_INVALID;
@@ -177,7 +179,7 @@ razer_status razer_moe_route(const razer_route* a, void* ws, size_t ws_bytes, vo
 
 size_t razer_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top) {
   if (tokens < 0 || experts < 1 || experts > RAZER_MOE_MAX_EXPERTS || top < 1 || top > RAZER_MOE_MAX_TOP) return 0;
-  if (tokens >= kMaxPairs / top) return 0;  // refused
+  if (tokens > kMaxOrdered || tokens >= kMaxPairs / top) return 0;  // refused
   return rz::moe_route_ws_bytes(tokens, experts, top);
 }
 

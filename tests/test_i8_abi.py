@@ -93,7 +93,8 @@ def test_grouped_refuses(want, kw):
     (INVALID, dict(offsets=0)), (INVALID, dict(slots=Y + 3)), (INVALID, dict(space=0, tokens=40)), (INVALID, dict(ws=0, tokens=40)),
     (INVALID, dict(ws=WS + 4, tokens=40)),
     (UNSUPPORTED, dict(experts=1025, groups=1, groups_kept=1, stride=2000)), (UNSUPPORTED, dict(top=33)),
-    (UNSUPPORTED, dict(tokens=1 << 29)), (OK, dict(tokens=0, offsets=0, rows=0, slots=0, logits=0, chosen=0, weights=0))])
+    (UNSUPPORTED, dict(tokens=1 << 29)), (UNSUPPORTED, dict(tokens=(1 << 20) + 1)),
+    (UNSUPPORTED, dict(tokens=(1 << 26) + 1, offsets=0, rows=0, slots=0)), (OK, dict(tokens=0, offsets=0, rows=0, slots=0, logits=0, chosen=0, weights=0))])
 def test_route_refuses(want, kw):
     ws = dict(ws=WS, space=1 << 40)
     ws.update({k: kw[k] for k in kw if k in ws})
@@ -128,11 +129,11 @@ def test_workspace_bytes():
     for a in ((0, 8, 64, 0), (8, 0, 64, 0), (8, 8, 0, 2), (-1, 8, 64, 0), (8, 8, 64, -1), (2 ** 30 + 1, 8, 64, 0),
               (8, 2 ** 62, 64, 0), (8, 8, rz.RAZER_I8_MAX_K + 16, 0), (8, 8, 64, rz.RAZER_MX_MAX_EXPERTS + 1)):
         assert rz.razer_i8_workspace_bytes(*a) == 0
-    for a in ((-1, 8, 2), (8, 0, 2), (8, 8, 0), (8, 1025, 2), (8, 64, 33), (2 ** 30, 8, 1), (2 ** 62, 8, 1)):
+    for a in ((-1, 8, 2), (8, 0, 2), (8, 8, 0), (8, 1025, 2), (8, 64, 33), (2 ** 20 + 1, 8, 1), (2 ** 62, 8, 1)):
         assert rz.razer_moe_workspace_bytes(*a) == 0
     for a in ((2 ** 30, 2 ** 30, 131056, 0), (2 ** 30, 2 ** 30, 131056, 4096), (1, 2 ** 30, 16, 0)):
         assert rz.razer_i8_workspace_bytes(*a) >= 0
-    assert rz.razer_moe_workspace_bytes((1 << 25) - 1, 1024, 32) >= 0
+    assert rz.razer_moe_workspace_bytes(1 << 20, 1024, 32) > 0
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
