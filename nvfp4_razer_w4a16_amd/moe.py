@@ -78,16 +78,25 @@ _workspace_bytes = functools.lru_cache(4096)(razer_moe_workspace_bytes)
 
 
 def _new_routes(tokens: int, experts: int, top: int, order: bool, space: int, device):
-    """(routes, the address of `space` bytes behind them in the same buffer)"""
+    """(routes, their addresses, that of `space` bytes behind them in the same buffer)"""
     n = tokens * top
     head = (4 * n + experts + 1 if order else 2 * n) + 3 & ~3
     buf = torch.empty(head + (space + 3 >> 2), dtype=torch.int32, device=device)
-    part, shape, strides = buf.as_strided, (tokens, top), (top, 1)
-    weights = part(shape, strides, n).view(torch.float32)
+    part, shape, strides, at = buf.as_strided, (tokens, top), (top, 1), buf.data_ptr()
+    chosen, weights = part(shape, strides, 0), part(shape, strides, n).view(torch.float32)
     if not order:
-        return MoeRoutes(part(shape, strides, 0), weights, None, None, None), None
-    return MoeRoutes(part(shape, strides, 0), weights, part((experts + 1,), (1,), 4 * n), part((n,), (1,), 3 * n),
-                     part(shape, strides, 2 * n)), buf.data_ptr() + 4 * head
+        return MoeRoutes(chosen, weights, None, None, None), (at, at + 4 * n, 0, 0, 0), None
+    return (MoeRoutes(chosen, weights, part((experts + 1,), (1,), 4 * n), part((n,), (1,), 3 * n),
+                      part(shape, strides, 2 * n)),
+            (at, at + 4 * n, at + 16 * n, at + 12 * n, at + 8 * n), at + 4 * head)
+
+
+def _packed_rows(t: torch.Tensor, cols: int):
+    """(t, stride) of rows that are not contiguous, or overlap: a copy, but for a lone row,
+    whose stride means nothing."""
+    if t.shape[0] > 1 or t.stride(1) != 1 and cols > 1:
+        t = torch.empty(t.shape, dtype=t.dtype, device=t.device).copy_(t)
+    return t, cols
 
 
 def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
@@ -126,19 +135,19 @@ def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", b
     if not 1 <= kept <= groups or top > experts // groups * kept:
         raise ValueError(f"{kept} of {groups} groups kept for {top} of {experts} experts")
     ld, inner = logits.stride()
-    if inner != 1 and experts > 1 or ld < experts and tokens > 1:
-        logits = logits.contiguous()
-        ld = experts
-    bias_at = None
+    if inner != 1 or ld < experts:
+        logits, ld = _packed_rows(logits, experts)
+    index = dev.index
+    bias_at = 0
     if bias is not None:
-        if (not isinstance(bias, _Tensor) or bias.dtype is not torch.float32 or bias.get_device() != dev.index
+        if (not isinstance(bias, _Tensor) or bias.dtype is not torch.float32 or bias.get_device() != index
                 or bias.shape != (experts,) or not bias.is_contiguous()):
             _check_buffer(bias, (experts,), dev, "bias", torch.float32)
         bias_at = bias.data_ptr()
     space, given = _workspace_bytes(tokens, experts, top) if order else 0, out is not None
     ws = None
     if not given:
-        out, ws = _new_routes(tokens, experts, top, order, 0 if workspace is not None else space, dev)
+        out, places, ws = _new_routes(tokens, experts, top, order, 0 if workspace is not None else space, dev)
     else:
         _check_buffer(out.experts, (tokens, top), dev, "out.experts", torch.int32)
         _check_buffer(out.weights, (tokens, top), dev, "out.weights", torch.float32)
@@ -146,6 +155,7 @@ def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", b
             _check_buffer(out.offsets, (experts + 1,), dev, "out.offsets", torch.int32)
             _check_buffer(out.rows, (tokens * top,), dev, "out.rows", torch.int32)
             _check_buffer(out.slots, (tokens, top), dev, "out.slots", torch.int32)
+        places = [t.data_ptr() for t in out[:5 if order else 2]] + ([] if order else [0, 0, 0])
     if workspace is not None:
         _check_buffer(workspace, None, dev, "workspace")
         ws, space = workspace.data_ptr(), workspace.nbytes
@@ -153,11 +163,10 @@ def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", b
         workspace = torch.empty(space, dtype=torch.uint8, device=dev)  # kept until the launch is enqueued
         ws = workspace.data_ptr()
     status = lib().razer_moe_route(
-        _route_bytes(tokens, max(ld, experts), experts, top, groups, kept, group_best, kind, dt,
-                     RAZER_ROUTE_RENORM if renormalise else 0, scale, logits.data_ptr(), bias_at or 0,
-                     out.experts.data_ptr(), out.weights.data_ptr(), out.offsets.data_ptr() if order else 0,
-                     out.rows.data_ptr() if order else 0, out.slots.data_ptr() if order else 0),
-        ws, space, _stream(dev.index))
+        _route_bytes(tokens, ld, experts, top, groups, kept, group_best, kind, dt,
+                     RAZER_ROUTE_RENORM if renormalise else 0, scale, logits.data_ptr(), bias_at,
+                     *places),
+        ws, space, _stream(index))
     if status:
         _check(status, "razer_moe_route")
     if not given and _grad_enabled() and (logits.requires_grad or bias is not None and bias.requires_grad):
@@ -177,35 +186,38 @@ def razer_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
         with _entered(stream):
             return razer_moe_combine(y, slots, weights, add, out)
     dev = _on_gpu(y, "y")
-    if y.dim() != 2 or not isinstance(slots, _Tensor) or slots.dim() != 2:
-        raise ValueError("y and slots must be 2-D")
-    kind = y.dtype
+    index, kind = dev.index, y.dtype
     dt = _dtype(kind)
+    shape = slots.shape if isinstance(slots, _Tensor) else ()
+    if y.dim() != 2 or len(shape) != 2:
+        raise ValueError("y and slots must be 2-D")
     rows, cols = y.shape
-    tokens, top = slots.shape
-    index = dev.index
+    tokens, top = shape
     if slots.dtype is not torch.int32 or slots.get_device() != index or not slots.is_contiguous():
-        _check_buffer(slots, (tokens, top), dev, "slots", torch.int32)
+        _check_buffer(slots, shape, dev, "slots", torch.int32)
     if (not isinstance(weights, _Tensor) or weights.dtype is not torch.float32 or weights.get_device() != index
-            or weights.shape != slots.shape or not weights.is_contiguous()):
-        _check_buffer(weights, (tokens, top), dev, "weights", torch.float32)
-    if y.stride(1) != 1 or y.stride(0) < cols:
-        y = y.contiguous()
-    source = add
+            or weights.shape != shape or not weights.is_contiguous()):
+        _check_buffer(weights, shape, dev, "weights", torch.float32)
+    y_stride, inner = y.stride()
+    if inner != 1 or y_stride < cols:
+        y, y_stride = _packed_rows(y, cols)
+    source, add_at, add_stride = add, 0, 0
     if add is not None:
-        if not isinstance(add, _Tensor) or add.get_device() != index or add.shape != (tokens, cols) or add.dtype is not kind:
+        if (not isinstance(add, _Tensor) or add.get_device() != index or add.shape != (tokens, cols)
+                or add.dtype is not kind):
             raise ValueError(f"add must be {tokens}x{cols} of {kind} on {dev}")
-        if add.stride(1) != 1 or add.stride(0) < cols:
-            add = add.contiguous()
+        add_stride, inner = add.stride()
+        if inner != 1 or add_stride < cols:
+            add, add_stride = _packed_rows(add, cols)
+        add_at = add.data_ptr()
     given = out is not None
     if not given:
         out = torch.empty(tokens, cols, dtype=kind, device=dev)
     else:
         _check_buffer(out, (tokens, cols), dev, "out", kind)
     status = lib().razer_moe_combine(
-        _combine_bytes(tokens, top, cols, rows, max(y.stride(0), cols), 0 if add is None else max(add.stride(0), cols), dt,
-                       y.data_ptr(), slots.data_ptr(), weights.data_ptr(), 0 if add is None else add.data_ptr(),
-                       out.data_ptr()), _stream(index))
+        _combine_bytes(tokens, top, cols, rows, y_stride, add_stride, dt, y.data_ptr(), slots.data_ptr(),
+                       weights.data_ptr(), add_at, out.data_ptr()), _stream(index))
     if status:
         _check(status, "razer_moe_combine")
     if not given and _grad_enabled() and (y.requires_grad or weights.requires_grad
