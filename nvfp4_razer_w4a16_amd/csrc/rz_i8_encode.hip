@@ -11,7 +11,10 @@
 // stored.
 //
 // Bound by memory: the row lives in the registers of 64 to 1024 lanes between its
-// maximum and its codes, so x is read once; longer rows are read twice.
+// maximum and its codes, so x is read once; rows of more than 32768 are read twice.
+// Measured: the gated form of 2041 x 14336 from bf16 28.6-30.1 us (146 MB, 4.9-5.1 TB/s; a
+// copy of 1 GiB reaches 5.1) and back to bf16 13.5-14.2 us (88 MB, 6.2-6.5 TB/s, the codes
+// still in the cache behind the L2s); one row of 4096 2.2 and 1.8 us, the time of any launch.
 #include <algorithm>
 
 #include "rz_i8.h"

@@ -91,6 +91,16 @@ __device__ __forceinline__ void tile_place(int pos, int mt, int nt, int& im, int
 // in registers: behind it the next step is complete (each wave has waited for its own
 // loads, but for the X rows just requested) and nobody reads this step any more, so the W
 // rows of the step after next go into its place.  W has a whole step to arrive, X two.
+// A load takes the CU's address unit 16 cycles and the four waves come at once, so loads
+// stand behind every other product (one behind each: 2048 x 28672 x 8192 450 us, and 421).
+//
+// Measured: 8192 cubed 403-409 us (2.7 POP/s), 2048 x 28672 x 8192 390-400 us, of which
+// the last half-filled round, in halves, takes 72-77; a loop of products in registers
+// alone runs at 3.47 POP/s on random codes (4.93 on zeros), a library's product of the
+// first size at 2.2.  Bound by power, then by its results: a step takes 1.46 us, 2.95 POP/s
+// (on zeros, which power does not hold down, 0.98 us, 4.4), and between two tiles lie some
+// 10 us, half of them the stores of 256 CUs at once.  The matrix units are busy 72 % of
+// the time.
 template <int BM, typename OT, bool GROUPED>
 __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) {
   constexpr int BN = kTileN;
@@ -456,6 +466,11 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
 // row tile come to LDS the same way as W.  The waves' sums meet in LDS.  Loads past the
 // last row return zero (the buffer descriptor ends there), so no load has a branch
 // around it and a chunk's loads have a fixed number.
+//
+// Bound by the read of W: 1 x 14336 x 4096 13.4-14.2 us (58.8 MB, 4.1-4.4 TB/s, the ramp of a
+// launch in it), 27 x 28672 x 8192 50.7-51.7 us (237 MB, 4.6 TB/s), 8 tokens through 2 of 8
+// experts of 14336 x 4096, seven of them used, 77-78 us (411 MB, 5.3 TB/s; a copy of 1 GiB
+// reaches 5.1).
 constexpr int kSWaves = 8, kSLoads = kSRows * kChunkB / 1024 / kSWaves;
 
 // Ring places.

@@ -7,7 +7,16 @@
 // rounding of each other once in some ten thousand tokens, and the choice would then
 // depend on how exp rounds.
 // Order: the pairs (token, place) sorted by expert, then token.
-// Combine: out[t] = add[t] + sum_j w[t, j] y[slots[t, j]], bound by memory.
+// Combine: out[t] = add[t] + sum_j w[t, j] y[slots[t, j]].
+//
+// Route and order are bound by instructions and by launches: 8192 tokens of 256 experts,
+// 8 of them out of 4 of 8 groups by sigmoid, 17.6-18.6 us of route (some 700 vector
+// instructions a token: a quarter of them the fp64 scores, a quarter the groups, 25 for each
+// choice) and 6.8 us of order; 333 tokens of 64 experts 4.3 and 5.2 us; one token, in one
+// launch, 6.2 us of latency.  (Comparing fp64 scores across the wave took 33-43 us.)
+// Combine is bound by memory: 8192 tokens of 8 rows of 4096 in bf16 131-134 us (671 MB, 5.0-5.1
+// TB/s; a copy of 1 GiB reaches 5.1).  A thread takes 16 bytes of a row and adds up its
+// token's rows in registers, so that every row is read once and nothing meets elsewhere.
 #include <algorithm>
 
 #include "rz_mx.h"
