@@ -477,7 +477,7 @@ size_t razer_i8_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t experts
  *   groups > 1: the experts are `groups` equal runs; a group's score is the sum of its
  *               group_best largest c; the groups_kept best groups stay
  *   chosen: the `top` largest c of what stays, the best first
- *   weights = scale * s (RAZER_ROUTE_RENORM: s / sum of the chosen s)
+ *   weights = scale * s (RAZER_ROUTE_RENORM: s / sum of the chosen s, 0 where that is 0)
  *
  * Equal values go to the lowest index, of groups too.  Scores and choices are worked
  * out in fp64 (experts' scores lie close together: fp32 would now and then choose

@@ -225,7 +225,7 @@ __device__ __forceinline__ void route_token(const MoeRoute& a, const float (&l)[
     const double sum = wave_sum(mine);
     mine = sum > 0.0 ? mine / sum : 0.0;
   }
-  weight = (float)(mine * (double)a.scale);
+  weight = chosen < 0 ? 0.0f : (float)(mine * (double)a.scale);
 }
 
 // ---- order ---------------------------------------------------------------------

@@ -10,7 +10,9 @@ a product are I8Tensors::
     y = razer_i8_gemm(razer_i8_quantize_gated(gu), down)
 
 Streams as in ``mx``: calls run on the current stream, or on ``stream``.  No call has a
-backward.  The package re-exports every name here.
+backward: where an operand's scales require a gradient, one that reaches the result
+raises (what is written to ``out`` stands outside any graph).  The package re-exports
+every name here.
 """
 from __future__ import annotations
 
@@ -20,7 +22,8 @@ import functools
 import torch
 
 from . import _check_buffer, lib
-from .mx import _check, _dtype, _entered, _on_gpu, _rows_of, _space, _stream
+from .mx import (_check, _dtype, _entered, _grad_enabled, _on_gpu, _rows_of, _space, _stream,
+                 _without_backward)
 
 I8_UNIT = 16
 RAZER_I8_MAX_K = 131056
@@ -187,6 +190,12 @@ def _operands(x, w):
     return xs, ws
 
 
+def _result(call: str, out, x, w=None):
+    """out, in the graph of the operands' scales that require a gradient."""
+    scales = [t._scales for t in (x, w) if t is not None and t._scales is not None and t._scales.requires_grad]
+    return _without_backward(call, (out,), scales)[0] if scales and _grad_enabled() else out
+
+
 def _encode(call, x, parts: int, out, stream) -> I8Tensor:
     if stream is not None:
         with _entered(stream):
@@ -230,8 +239,8 @@ def razer_i8_dequant(t: I8Tensor, dtype: torch.dtype = torch.float32, out=None, 
     if stream is not None:
         with _entered(stream):
             return razer_i8_dequant(t, dtype, out)
-    struct, dev = _operand(t, "t"), t._device
-    if out is None:
+    struct, dev, given = _operand(t, "t"), t._device, out is not None
+    if not given:
         out = torch.empty(t._rows, t._cols, dtype=dtype, device=dev)
     else:
         _check_buffer(out, t.shape, dev, "out")
@@ -239,7 +248,7 @@ def razer_i8_dequant(t: I8Tensor, dtype: torch.dtype = torch.float32, out=None, 
     st = lib().razer_i8_dequant(struct, out.data_ptr(), _dtype(dtype), _stream(t._index))
     if st:
         _check(st, "razer_i8_dequant")
-    return out
+    return out if given else _result("razer_i8_dequant", out, t)
 
 
 def razer_i8_workspace_bytes(m: int, n: int, k: int, experts: int = 0) -> int:
@@ -260,8 +269,8 @@ def razer_i8_gemm(x: I8Tensor, w: I8Tensor, out_dtype: torch.dtype = torch.bfloa
             return razer_i8_gemm(x, w, out_dtype, out, workspace)
     xs, ws = _operands(x, w)
     m, n, dev, index, space, space_bytes = x._rows, w._rows, x._device, x._index, None, 0
-    current = _stream(index)
-    if out is None:
+    current, given = _stream(index), out is not None
+    if not given:
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _check_buffer(out, (m, n), dev, "out")
@@ -271,7 +280,7 @@ def razer_i8_gemm(x: I8Tensor, w: I8Tensor, out_dtype: torch.dtype = torch.bfloa
     status = lib().razer_i8_gemm(xs, ws, out.data_ptr(), _dtype(out.dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_i8_gemm")
-    return out
+    return out if given else _result("razer_i8_gemm", out, x, w)
 
 
 def razer_i8_gemm_grouped(x: I8Tensor, w: I8Tensor, offsets: torch.Tensor, x_rows: torch.Tensor | None = None,
@@ -286,7 +295,7 @@ def razer_i8_gemm_grouped(x: I8Tensor, w: I8Tensor, offsets: torch.Tensor, x_row
         with _entered(stream):
             return razer_i8_gemm_grouped(x, w, offsets, x_rows, out_dtype, out, workspace)
     xs, ws = _operands(x, w)
-    dev, index = x._device, x._index
+    dev, index, given = x._device, x._index, out is not None
     current = _stream(index)
     if offsets.dim() != 1:
         raise ValueError("offsets must be 1-D")
@@ -301,7 +310,7 @@ def razer_i8_gemm_grouped(x: I8Tensor, w: I8Tensor, offsets: torch.Tensor, x_row
         _check_buffer(x_rows, x_rows.shape, dev, "x_rows", torch.int32)
         m, rows = x_rows.numel(), x_rows.data_ptr()
     n = w._rows // experts
-    if out is None:
+    if not given:
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _check_buffer(out, (m, n), dev, "out")
@@ -313,4 +322,4 @@ def razer_i8_gemm_grouped(x: I8Tensor, w: I8Tensor, offsets: torch.Tensor, x_row
                                          _dtype(out.dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_i8_gemm_grouped")
-    return out
+    return out if given else _result("razer_i8_gemm_grouped", out, x, w)

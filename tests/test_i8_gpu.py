@@ -209,3 +209,20 @@ def test_scales_of_the_first_token_do_not_reach_padding():
         y = rz.razer_i8_gemm_grouped(ref.device(x, sx), ref.device(w, sw),
                                      torch.tensor([0, copies], dtype=torch.int32).cuda(), rows)
         assert (y == 0).all()
+
+
+def test_scales_that_require_a_gradient():
+    """There is no backward: results are in the graph of such scales, and raise there."""
+    x, w = rz.razer_i8_quantize(torch.randn(6, 64, device="cuda")), rz.razer_i8_quantize(torch.randn(48, 64, device="cuda"))
+    offsets = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    leaf = rz.I8Tensor.of(w.codes, w.scales.clone().requires_grad_())
+    for result, want in ((rz.razer_i8_gemm(x, leaf), rz.razer_i8_gemm(x, w)),
+                         (rz.razer_i8_gemm_grouped(x, leaf, offsets), rz.razer_i8_gemm_grouped(x, w, offsets)),
+                         (rz.razer_i8_dequant(leaf), rz.razer_i8_dequant(w))):
+        assert torch.equal(result, want) and result.requires_grad and not want.requires_grad
+        with pytest.raises(RuntimeError, match="no backward"):
+            result.sum().backward()
+    out = torch.empty(6, 48, dtype=torch.bfloat16, device="cuda")
+    assert not rz.razer_i8_gemm(x, leaf, out=out).requires_grad
+    with torch.no_grad():
+        assert not rz.razer_i8_gemm(x, leaf).requires_grad

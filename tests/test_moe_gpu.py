@@ -185,3 +185,17 @@ def test_combine_special():
     assert torch.equal(rz.razer_moe_combine(y.t().contiguous().t(), slots[1:], w[1:], h[1:]), want)
     assert rz.razer_moe_combine(y, slots[:0], w[:0]).shape == (0, 64)
     assert (rz.razer_moe_combine(y[:0], slots[2:], w[2:]) == 0).all()
+
+
+def test_places_that_no_expert_takes_weigh_nothing():
+    """... whatever the scale is, and whether or not there are scores to divide by."""
+    logits = torch.full((3, 8), float("-inf"), device="cuda")
+    logits[0, 5] = 1.0
+    logits[1, 2] = -900.0  # a sigmoid that is 0 in 64 bits: a sum of nothing
+    for scale in (float("inf"), -2.0):
+        for renormalise in (False, True):
+            for copies in (1, 7):
+                r = rz.razer_moe_route(logits.repeat(copies, 1), 2, score="sigmoid", renormalise=renormalise, scale=scale)
+                assert r.experts[:3].tolist() == [[5, -1], [2, -1], [-1, -1]]
+                assert (r.weights[:, 1] == 0).all() and (r.weights[2::3] == 0).all()
+    assert r.weights[1, 0] == 0 and r.weights[0, 0] == -2.0
