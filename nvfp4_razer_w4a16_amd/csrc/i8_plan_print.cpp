@@ -5,20 +5,16 @@
 
 #include "rz_i8_plan.h"
 
-namespace rz {
-int device_cu_count() { return 256; }
-}  // namespace rz
-
 int main(int argc, char** argv) {
   for (int i = 1; i < argc; i++) {
     long long m, n, k, experts;
     if (sscanf(argv[i], "%lld,%lld,%lld,%lld", &m, &n, &k, &experts) != 4) return 1;
     rz::i8::StreamPlan s;
-    if (rz::i8::streams(m, n, k, experts, s)) {
+    if (rz::i8::streams(m, n, k, experts, 256, s)) {
       printf("stream %d %d %d %d\n", s.rt, s.ck, s.mt, s.rows);
     } else {
       double us;
-      const rz::i8::TilePlan t = rz::i8::tile_plan(m, n, k, experts, us);
+      const rz::i8::TilePlan t = rz::i8::tile_plan(m, n, k, experts, 256, us);
       printf("tile %d %d %d %d %d\n", t.high, t.full, t.rest, t.split, t.halves);
     }
   }

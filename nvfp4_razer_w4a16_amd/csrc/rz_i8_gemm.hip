@@ -734,7 +734,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
 template <int RT, int CK, int MT> hipError_t go_stream(const Args& a, int y_dtype, StreamPlan p, hipStream_t stream) {
   const int64_t tiles = (a.n + kSRows - 1) / kSRows, full = (a.m + p.rows - 1) / p.rows;
   const int64_t jobs = a.offsets ? std::min(full + a.experts, a.m) : full;
-  const int64_t grid = std::min(tiles * jobs, (int64_t)device_cu_count());  // the ring fills a CU
+  const int64_t grid = std::min(tiles * jobs, (int64_t)p.cus);  // the ring fills a CU
   if (!a.offsets) {
     p.cuts = cuts_of((uint32_t)tiles, (uint32_t)jobs, (uint32_t)grid, RT);
     if (p.cuts.per_job) p.mul_per_job = (1 << 20) / (int)p.cuts.per_job + 1;
@@ -805,7 +805,7 @@ __global__ __launch_bounds__(256) void i8_fold_kernel(Args a, TilePlan plan) {
 }
 
 template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
-  const int grid = std::min(p.full + p.rest * p.split, device_cu_count());
+  const int grid = std::min(p.full + p.rest * p.split, p.cus);
   hipLaunchKernelGGL((i8_tile_kernel<BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
   return hipGetLastError();
 }
@@ -816,9 +816,9 @@ template <int BM, typename OT> hipError_t go_fold(const Args& a, const TilePlan&
   return hipGetLastError();
 }
 
-template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t stream) {
+template <typename OT> hipError_t run(const Args& a, int cus, void* ws, hipStream_t stream) {
   double us;
-  TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0, us);
+  TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0, cus, us);
   p.part = (int32_t*)ws;
   if (a.offsets) return p.high == 256 ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<128, OT, true>(a, p, stream);
   TilePlan halves = p;
@@ -839,19 +839,21 @@ template <typename OT> hipError_t run(const Args& a, void* ws, hipStream_t strea
 }  // namespace
 
 size_t i8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int64_t experts) {
+  const int cus = device_cu_count();
   i8::StreamPlan p;
   double us;
-  return i8::streams(m, n, k, experts, p) ? 0 : i8::tile_ws_bytes(i8::tile_plan(m, n, k, experts, us));
+  return i8::streams(m, n, k, experts, cus, p) ? 0 : i8::tile_ws_bytes(i8::tile_plan(m, n, k, experts, cus, us));
 }
 
 hipError_t launch_i8_gemm(const I8Gemm& g, void* ws, hipStream_t stream) {
   const Args a = {g.x.codes, g.w.codes, g.x.scales, g.w.scales, g.m, g.n, g.k, g.x.rows, g.y, g.offsets, g.x_rows,
                   g.experts};
+  const int cus = device_cu_count();
   i8::StreamPlan p;
-  if (i8::streams(g.m, g.n, g.k, g.offsets ? g.experts : 0, p)) return run_stream(a, g.y_dtype, p, stream);
-  if (g.y_dtype == kF32) return run<float>(a, ws, stream);
-  if (g.y_dtype == kF16) return run<_Float16>(a, ws, stream);
-  return run<__bf16>(a, ws, stream);
+  if (i8::streams(g.m, g.n, g.k, g.offsets ? g.experts : 0, cus, p)) return run_stream(a, g.y_dtype, p, stream);
+  if (g.y_dtype == kF32) return run<float>(a, cus, ws, stream);
+  if (g.y_dtype == kF16) return run<_Float16>(a, cus, ws, stream);
+  return run<__bf16>(a, cus, ws, stream);
 }
 
 }  // namespace rz

@@ -1,5 +1,5 @@
 // rz_i8_plan.h -- which kernel a product of 8-bit integer tensors runs on, and how it is
-// cut: rules on sizes and the device's compute units.  Host code.  (In a namespace of its
+// cut: rules on sizes and the device's compute units (`cus`).  Host code.  (In a namespace of its
 // own: the MXFP4 products' rules have the same names.)
 #pragma once
 
@@ -9,8 +9,6 @@
 
 #include <algorithm>
 #include <cmath>
-
-#include "rz_i8_launch.h"
 
 namespace rz {
 namespace i8 {
@@ -22,6 +20,7 @@ constexpr int kStepB = 128;   // bytes of a row and step
 // How a product is cut: mt x nt tiles (grouped: as many row tiles as there are),
 // the last `rest` of them each in `split` slices of K whose sums go to slots of `part`.
 struct TilePlan {
+  int cus;
   int high;  // rows of X of a tile
   int mt, nt;
   int full, rest, split;
@@ -48,9 +47,10 @@ inline int steps_of(int64_t k) { return (int)((k + kStepB - 1) / kStepB); }
 
 // The tiles of a product, `high` rows each, and its time in us.  The last, partly
 // filled round of tiles is cut along K where that is quicker.
-inline TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t experts, double& us) {
+inline TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t experts, int cus, double& us) {
   TilePlan p = {};
-  const int cus = device_cu_count(), steps = steps_of(k);
+  const int steps = steps_of(k);
+  p.cus = cus;
   p.high = high;
   p.nt = (int)((n + kTileN - 1) / kTileN);
   p.mt = (int)((m + high - 1) / high + std::min(experts, m));
@@ -79,9 +79,9 @@ inline TilePlan tiles_of(int high, int64_t m, int64_t n, int64_t k, int64_t expe
   if (p.split > 1) p.rest = rest, p.full -= rest;
   return p;
 }
-inline TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts, double& us) {
+inline TilePlan tile_plan(int64_t m, int64_t n, int64_t k, int64_t experts, int cus, double& us) {
   double low_us;
-  const TilePlan p = tiles_of(256, m, n, k, experts, us), low = tiles_of(128, m, n, k, experts, low_us);
+  const TilePlan p = tiles_of(256, m, n, k, experts, cus, us), low = tiles_of(128, m, n, k, experts, cus, low_us);
   if (low_us >= us + 1.0) return p;  // the larger tile's results take longer to store
   us = low_us;
   return low;
@@ -114,6 +114,7 @@ __host__ __device__ __forceinline__ Cuts cuts_of(uint32_t tiles, uint32_t jobs, 
 
 // The chunks of a row: `ck` of them, each `pieces` 16-byte pieces, the last `last`.
 struct StreamPlan {
+  int cus;
   int ck, mt;  // ck = 0: not covered
   int rt;      // row tiles of a chunk
   int rows;    // of a job, at most 16 mt
@@ -124,8 +125,9 @@ struct StreamPlan {
 };
 
 // The stream kernel's shape for `m` rows, of each of `experts` on average if that is not 0.
-inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
+inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts, int cus) {
   StreamPlan p = {};
+  p.cus = cus;
   int ck = 1;
   while ((int64_t)ck * kChunkB < k) ck *= 2;
   if (ck > 8) return p;  // X would not fit the registers
@@ -145,7 +147,7 @@ inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts) 
   // Short rows: several row tiles a chunk, if there is a chunk for every CU.
   const int64_t jobs = experts ? std::min(experts, m) : (m + p.rows - 1) / p.rows;
   p.rt = p.mt == 4 ? 1 : k <= kChunkB / 4 ? 4 : k <= kChunkB / 2 ? 2 : 1;
-  while (p.rt > 1 && jobs * ((n + kSRows * p.rt - 1) / (kSRows * p.rt)) < device_cu_count()) p.rt /= 2;
+  while (p.rt > 1 && jobs * ((n + kSRows * p.rt - 1) / (kSRows * p.rt)) < cus) p.rt /= 2;
   p.pieces = (int)(((k + ck - 1) / ck + 63) / 64 * 4);  // whole products' pieces
   p.last = (int)(k / 16) - p.pieces * (ck - 1);
   p.mul_pieces = (1 << 20) / p.pieces + 1;
@@ -168,7 +170,7 @@ struct Estimate {
   double stream, tile;
 };
 inline Estimate estimate(int64_t m, int64_t n, int64_t k, int64_t experts, const StreamPlan& p) {
-  const int cus = device_cu_count();
+  const int cus = p.cus;
   const int64_t parts = experts ? std::min(experts, m) : 1, rows = (m + parts - 1) / parts;  // W's used, rows each
   const double read = (double)parts * n * k / 5e6;
   const int64_t jobs = (rows + p.rows - 1) / p.rows;  // of each W
@@ -177,11 +179,11 @@ inline Estimate estimate(int64_t m, int64_t n, int64_t k, int64_t experts, const
   // an expert's jobs read its W one after the other; those of one product side by side
   const double streamed = experts ? read * jobs : read;
   double tile;
-  tile_plan(m, n, k, experts, tile);
+  tile_plan(m, n, k, experts, cus, tile);
   return {std::max(work, streamed) + std::min(work, streamed) / 2 + 2.5 + 0.3 * p.ck * p.mt, tile + 0.45 * read};
 }
-inline bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, StreamPlan& p) {
-  p = stream_plan(m, n, k, experts);
+inline bool streams(int64_t m, int64_t n, int64_t k, int64_t experts, int cus, StreamPlan& p) {
+  p = stream_plan(m, n, k, experts, cus);
   if (!p.ck) return false;
   const Estimate e = estimate(m, n, k, experts, p);
   return e.stream <= e.tile;

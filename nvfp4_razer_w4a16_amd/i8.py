@@ -18,11 +18,12 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 import torch
 
 from . import _check_buffer, lib
-from .mx import (_check, _dtype, _entered, _grad_enabled, _on_gpu, _rows_of, _space, _stream,
+from .mx import (_check, _dtype, _entered, _grad_enabled, _on_gpu, _rows_of, _space, _stream, _Tensor,
                  _without_backward)
 
 I8_UNIT = 16
@@ -34,14 +35,18 @@ class razer_i8(ctypes.Structure):
                 ("scales", ctypes.c_void_p)]
 
 
+# The struct as bytes, which cost a quarter of a ctypes instance to make
+_struct_bytes = struct.Struct("qqPP").pack
+
+
 def bind(L: ctypes.CDLL):
     """Argument types of the calls bound here."""
-    vp, sz, i32, i64, P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, ctypes.POINTER(razer_i8)
-    for name, args in (("razer_i8_quantize", [vp, i32, i64, P, vp]),
-                       ("razer_i8_quantize_gated", [vp, i32, i64, P, vp]),
-                       ("razer_i8_dequant", [P, vp, i32, vp]),
-                       ("razer_i8_gemm", [P, P, vp, i32, vp, sz, vp]),
-                       ("razer_i8_gemm_grouped", [P, P, vp, i64, vp, i64, vp, i32, vp, sz, vp])):
+    vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
+    for name, args in (("razer_i8_quantize", [vp, i32, i64, vp, vp]),
+                       ("razer_i8_quantize_gated", [vp, i32, i64, vp, vp]),
+                       ("razer_i8_dequant", [vp, vp, i32, vp]),
+                       ("razer_i8_gemm", [vp, vp, vp, i32, vp, sz, vp]),
+                       ("razer_i8_gemm_grouped", [vp, vp, vp, i64, vp, i64, vp, i32, vp, sz, vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = i32, args
     L.razer_i8_workspace_bytes.restype, L.razer_i8_workspace_bytes.argtypes = sz, [i64] * 4
@@ -54,8 +59,8 @@ class I8Tensor:
     replaced; a call refuses a tensor whose buffers do not match its shape."""
 
     # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers it was
-    # given, when their shapes were last looked at
-    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at")
+    # given, when their shapes were last looked at; _struct: the razer_i8 as of then
+    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at", "_struct")
 
     def __init__(self, rows: int, cols: int, device):
         if rows < 0 or cols < 0 or cols % I8_UNIT:
@@ -63,21 +68,20 @@ class I8Tensor:
         self._rows, self._cols = rows, cols
         # one buffer for both: codes, then scales; their views are made when asked for
         self._buf = buf = torch.empty(rows * (cols + 4), dtype=torch.int8, device=device)
-        self._device, self._index = buf.device, buf.get_device()
+        self._device, self._index, at = buf.device, buf.get_device(), buf.data_ptr()
         self._codes = self._scales = None
+        self._struct = _struct_bytes(rows, cols, at, at + rows * cols)
 
     @classmethod
     def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "I8Tensor":
         """The tensor that these buffers hold (shared, not copied); leading
         dimensions, such as a stack of experts, are rows."""
         t = cls.__new__(cls)
-        shape = codes.shape
-        if len(shape) != 2:
-            codes = codes.view(-1, shape[-1])
-            shape = codes.shape
+        if codes.dim() != 2:
+            codes = codes.view(-1, codes.shape[-1])
         if scales.dim() != 1:
             scales = scales.view(-1)
-        t._rows, t._cols = shape
+        t._rows, t._cols = codes.shape
         t._buf, t._codes, t._scales = None, codes, scales
         t._check_buffers("I8Tensor")
         return t
@@ -142,31 +146,30 @@ class I8Tensor:
         self._checked(name)
         return self._device
 
-    def _checked(self, name: str) -> razer_i8:
-        """The struct of buffers that match the shape.  The owner of buffers that it
+    def _checked(self, name: str) -> bytes:
+        """The razer_i8 of buffers that match the shape.  The owner of buffers that it
         was given may have changed them since: every call looks where they are and
         how long, and at the rest if they have moved."""
-        rows, cols = self._rows, self._cols
-        if self._buf is not None:
-            at = self._buf.data_ptr()
-            return razer_i8(rows, cols, at, at + rows * cols)
-        c, s = self._codes, self._scales
-        at, scales_at = c.data_ptr(), s.data_ptr()
-        if at != self._at or scales_at != self._scales_at or c.nbytes != rows * cols or s.nbytes != 4 * rows:
-            self._check_buffers(name)
-        return razer_i8(rows, cols, at, scales_at)
+        if self._buf is None:
+            c, s, rows = self._codes, self._scales, self._rows
+            if (c.data_ptr() != self._at or s.data_ptr() != self._scales_at or c.nbytes != rows * self._cols
+                    or s.nbytes != 4 * rows):
+                self._check_buffers(name)
+        return self._struct
 
     def _check_buffers(self, name: str):
         c, s, rows, cols = self._codes, self._scales, self._rows, self._cols
         index = c.get_device()
         if (c.dtype is not torch.int8 or s.dtype is not torch.float32 or cols % I8_UNIT or s.get_device() != index
-                or c.shape != (rows, cols) or s.shape != (rows,) or not c.is_contiguous() or not s.is_contiguous()):
+                or c.shape != (rows, cols) or s.dim() != 1 or s.nbytes != 4 * rows or not c.is_contiguous()
+                or not s.is_contiguous()):
             raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
                              f"{s.dtype} on {s.device} are no contiguous 8-bit tensor of {rows}x{cols}")
         self._device, self._index, self._at, self._scales_at = c.device, index, c.data_ptr(), s.data_ptr()
+        self._struct = _struct_bytes(rows, cols, self._at, self._scales_at)
 
 
-def _operand(t, name: str) -> razer_i8:
+def _operand(t, name: str) -> bytes:
     """The struct of an operand on a GPU."""
     if not isinstance(t, I8Tensor):
         raise TypeError(f"{name} must be an I8Tensor")
@@ -190,10 +193,12 @@ def _operands(x, w):
     return xs, ws
 
 
-def _result(call: str, out, x, w=None):
-    """out, in the graph of the operands' scales that require a gradient."""
-    scales = [t._scales for t in (x, w) if t is not None and t._scales is not None and t._scales.requires_grad]
-    return _without_backward(call, (out,), scales)[0] if scales and _grad_enabled() else out
+def _outside_graph(call: str, out, x, w):
+    """out, in the graph of the scales of x and w where they require a gradient."""
+    xs, ws = x._scales, w._scales  # None: nobody has seen them
+    if (xs is not None and xs.requires_grad or ws is not None and ws.requires_grad) and _grad_enabled():
+        return _without_backward(call, (out,), (xs, ws))[0]
+    return out
 
 
 def _encode(call, x, parts: int, out, stream) -> I8Tensor:
@@ -205,20 +210,21 @@ def _encode(call, x, parts: int, out, stream) -> I8Tensor:
     if x.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     rows, width = x.shape
-    cols = width // parts
-    if width % parts or cols % I8_UNIT:
+    cols = width if parts == 1 else width // parts
+    if cols * parts != width or cols % I8_UNIT:
         raise ValueError(f"columns must be a multiple of {parts * I8_UNIT}")
+    current = _stream(dev.index)
     if out is None:
         out = I8Tensor(rows, cols, dev)
-        struct = out._checked("out")
+        packed = out._struct
     else:
-        struct = _operand(out, "out")
+        packed = _operand(out, "out")
         if out._device != dev:
             raise ValueError(f"out must be on {dev}, not {out._device}")
         if out.shape != (rows, cols):
             raise ValueError(f"out is {out.rows}x{out.cols}, expected {rows}x{cols}")
     x, ptr, ld = _rows_of(x, width)
-    st = call(ptr, dt, ld, struct, _stream(dev.index))
+    st = call(ptr, dt, ld, packed, current)
     if st:
         _check(st, call.__name__)
     return out
@@ -239,16 +245,17 @@ def razer_i8_dequant(t: I8Tensor, dtype: torch.dtype = torch.float32, out=None, 
     if stream is not None:
         with _entered(stream):
             return razer_i8_dequant(t, dtype, out)
-    struct, dev, given = _operand(t, "t"), t._device, out is not None
+    packed, dev, index, given = _operand(t, "t"), t._device, t._index, out is not None
+    current = _stream(index)
     if not given:
         out = torch.empty(t._rows, t._cols, dtype=dtype, device=dev)
     else:
         _check_buffer(out, t.shape, dev, "out")
         dtype = out.dtype
-    st = lib().razer_i8_dequant(struct, out.data_ptr(), _dtype(dtype), _stream(t._index))
+    st = lib().razer_i8_dequant(packed, out.data_ptr(), _dtype(dtype), current)
     if st:
         _check(st, "razer_i8_dequant")
-    return out if given else _result("razer_i8_dequant", out, t)
+    return out if given else _outside_graph("razer_i8_dequant", out, t, t)
 
 
 def razer_i8_workspace_bytes(m: int, n: int, k: int, experts: int = 0) -> int:
@@ -274,13 +281,14 @@ def razer_i8_gemm(x: I8Tensor, w: I8Tensor, out_dtype: torch.dtype = torch.bfloa
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _check_buffer(out, (m, n), dev, "out")
+        out_dtype = out.dtype
     need = _workspace_bytes(m, n, x._cols, 0, index)
     if need or workspace is not None:
         workspace, space, space_bytes = _space(need, workspace, dev)
-    status = lib().razer_i8_gemm(xs, ws, out.data_ptr(), _dtype(out.dtype), space, space_bytes, current)
+    status = lib().razer_i8_gemm(xs, ws, out.data_ptr(), _dtype(out_dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_i8_gemm")
-    return out if given else _result("razer_i8_gemm", out, x, w)
+    return out if given else _outside_graph("razer_i8_gemm", out, x, w)
 
 
 def razer_i8_gemm_grouped(x: I8Tensor, w: I8Tensor, offsets: torch.Tensor, x_rows: torch.Tensor | None = None,
@@ -297,29 +305,35 @@ def razer_i8_gemm_grouped(x: I8Tensor, w: I8Tensor, offsets: torch.Tensor, x_row
     xs, ws = _operands(x, w)
     dev, index, given = x._device, x._index, out is not None
     current = _stream(index)
-    if offsets.dim() != 1:
-        raise ValueError("offsets must be 1-D")
-    _check_buffer(offsets, offsets.shape, dev, "offsets", torch.int32)
+    # (the checks in line cost a third of the call that names what is wrong)
+    if not (isinstance(offsets, _Tensor) and offsets.dtype is torch.int32 and offsets.get_device() == index
+            and offsets.dim() == 1 and offsets.is_contiguous()):
+        if offsets.dim() != 1:
+            raise ValueError("offsets must be 1-D")
+        _check_buffer(offsets, offsets.shape, dev, "offsets", torch.int32)
     experts, m = offsets.numel() - 1, x._rows
     if experts < 1 or w._rows % experts:
         raise ValueError(f"w has {w._rows} rows for {experts} experts")
     rows = None
     if x_rows is not None:
-        if x_rows.dim() != 1:
-            raise ValueError("x_rows must be 1-D")
-        _check_buffer(x_rows, x_rows.shape, dev, "x_rows", torch.int32)
+        if not (isinstance(x_rows, _Tensor) and x_rows.dtype is torch.int32 and x_rows.get_device() == index
+                and x_rows.dim() == 1 and x_rows.is_contiguous()):
+            if x_rows.dim() != 1:
+                raise ValueError("x_rows must be 1-D")
+            _check_buffer(x_rows, x_rows.shape, dev, "x_rows", torch.int32)
         m, rows = x_rows.numel(), x_rows.data_ptr()
     n = w._rows // experts
     if not given:
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _check_buffer(out, (m, n), dev, "out")
+        out_dtype = out.dtype
     space, space_bytes = None, 0
     need = _workspace_bytes(m, n, x._cols, experts, index)
     if need or workspace is not None:
         workspace, space, space_bytes = _space(need, workspace, dev)
     status = lib().razer_i8_gemm_grouped(xs, ws, offsets.data_ptr(), experts, rows, m, out.data_ptr(),
-                                         _dtype(out.dtype), space, space_bytes, current)
+                                         _dtype(out_dtype), space, space_bytes, current)
     if status:
         _check(status, "razer_i8_gemm_grouped")
-    return out if given else _result("razer_i8_gemm_grouped", out, x, w)
+    return out if given else _outside_graph("razer_i8_gemm_grouped", out, x, w)
