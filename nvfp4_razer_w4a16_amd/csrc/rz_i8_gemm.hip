@@ -460,8 +460,8 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
 // would not.  Rows of at most 1024 or 512 bytes come RT = two or four row tiles a chunk,
 // each of which has four or two of the waves to share its K.
 //
-// Of a wave's sixteen pieces, lane group g = lane / 16 takes the four from 4 g on, one
-// a product: K is summed in another order, the same for both operands.  Pieces past the
+// Of a wave's sixteen pieces, lane group g = lane / 16 takes piece 4 i + g at product i, so
+// that a load of X covers 64 bytes of each of 16 rows.  Pieces past the
 // row or the chunk are zeros in X, whatever W's fragment holds there.  The scales of a
 // row tile come to LDS the same way as W.  The waves' sums meet in LDS.  Loads past the
 // last row return zero (the buffer descriptor ends there), so no load has a branch
@@ -592,7 +592,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
         for (int v = 0; v < kUnits; v++)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const int at = 16 * (along + v * kAlong) + 4 * (lane >> 4) + i;  // of the chunk's pieces
+            const int at = 16 * (along + v * kAlong) + 4 * i + (lane >> 4);  // of the chunk's pieces
             fx[j][u][v][i] = *(const i32x4_t*)(pc + min(u * plan.pieces + at, nb - 1) * 16);
           }
     }
@@ -604,13 +604,13 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
     // from a lane number that the compiler cannot follow up to the kernel's start.
     int at_lane = lane;
     asm volatile("" : "+v"(at_lane));
-    const int g = at_lane >> 4, w_row = wave / (kAlong * kX) * kSRows + (at_lane & 15), mine = 16 * along + 4 * g;
+    const int g = at_lane >> 4, w_row = wave / (kAlong * kX) * kSRows + (at_lane & 15), mine = 16 * along + g;
     // fragment i of W in a chunk; the next unit's lie kAlong * 256
     // bytes on, as the exchange is within 16 pieces
     int fo[4], fo_last[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const int c = mine + i;
+      const int c = mine + 4 * i;
       auto offset = [&](int pieces) {  // past the row: some other codes
         return min(w_row * pieces + (c ^ key(pieces, w_row)), kSRows * kChunkB / 16 - 1 - 16 * kAlong * (kUnits - 1)) * 16;
       };
@@ -626,7 +626,7 @@ __global__ __launch_bounds__(64 * kSWaves, 2) void i8_stream_kernel(Args a, int 
         for (int v = 0; v < kUnits; v++)
 #pragma unroll
           for (int i = 0; i < 4; i++)
-            if (mine + 16 * v * kAlong + i >= (u == CK - 1 ? plan.last : plan.pieces)) fx[j][u][v][i] = i32x4_t{};
+            if (mine + 16 * v * kAlong + 4 * i >= (u == CK - 1 ? plan.last : plan.pieces)) fx[j][u][v][i] = i32x4_t{};
 
     // this thread's results: the scale of their row, and rows that padding leaves zero
     bool none[kOuts];

@@ -238,7 +238,12 @@ __device__ __forceinline__ void route_token(const MoeRoute& a, const float (&l)[
 constexpr int kPairs = 512;          // most pairs of a block
 constexpr int kDirect = 256;         // blocks whose counts every block adds up for itself
 constexpr int kGroup = 64;           // otherwise: blocks of a group
-constexpr int kOneTokens = 8;        // tokens that one workgroup routes and orders
+// Tokens that one workgroup of eight or 16 waves routes and orders.  Two a wave are as quick
+// as two launches for up to 64 experts alone; 16 waves of more than 256 do not fit the
+// registers.  One workgroup and two launches, us captured and called one by one: 32 tokens of
+// 64 experts 8.4, 10.4 and 8.8, 14.7; 16 of 256 (of groups) 10.8, 11.3 and 11.3, 15.2; 32 of
+// 256 16.9, 15.8 and 11.6, 15.1.
+constexpr int most_alone(int experts) { return experts <= 64 ? 32 : experts <= 256 ? 16 : 8; }
 
 struct OrderPlan {
   int per;              // tokens of a block
@@ -246,9 +251,11 @@ struct OrderPlan {
   int row;              // bytes of a block's counts, whole dwords
   size_t counts, sums;  // bytes of the counts and of the groups' sums
 };
-OrderPlan order_plan(int64_t tokens, int64_t experts, int64_t top) {
+// blocks 0: one workgroup for all.  (Without an order nothing asks for one, and the second of
+// two tokens would wait.)
+OrderPlan order_plan(int64_t tokens, int64_t experts, int64_t top, bool order) {
   OrderPlan p = {};
-  if (tokens <= kOneTokens) return p;
+  if (tokens <= (order ? most_alone((int)experts) : 8)) return p;
   p.per = (int)std::min(std::max((tokens + 255) / 256, (int64_t)4), std::min((int64_t)32, kPairs / top));
   p.blocks = (int)((tokens + p.per - 1) / p.per);
   p.groups = p.blocks > kDirect ? (p.blocks + kGroup - 1) / kGroup : 0;
@@ -311,19 +318,20 @@ __device__ __forceinline__ void place(const MoeRoute& a, const int* list, int n,
   }
 }
 
-// All of a few tokens' routing and order, a wave a token.
-template <typename T, int V> __global__ __launch_bounds__(64 * kOneTokens) void route_one_kernel(MoeRoute a) {
-  constexpr int N = 64 * kOneTokens;
-  __shared__ double keys[kOneTokens][64 * V];
-  __shared__ __attribute__((aligned(16))) int list[kOneTokens * 32], start[1024], part[kOneTokens];
+// All of a few tokens' routing and order.
+template <typename T, int V, int WAVES> __global__ __launch_bounds__(64 * WAVES) void route_one_kernel(MoeRoute a) {
+  constexpr int N = 64 * WAVES, kTokens = most_alone(64 * V);
+  __shared__ double keys[WAVES][64 * V];
+  __shared__ __attribute__((aligned(16))) int list[kTokens * 32], start[1024], part[WAVES];
   __shared__ uint32_t bits[1024];
-  const int tid = threadIdx.x, lane = tid & 63, t = tid >> 6, n = (int)a.tokens * a.top;
-  if (t < a.tokens) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = (int)a.tokens * a.top;
+  float bias[V];
+  if (wave < a.tokens) load_row(a.bias, a.experts, 0.0f, bias);
+  for (int t = wave; t < a.tokens; t += WAVES) {
     int chosen;
-    float w, l[V], bias[V];
-    load_row(a.bias, a.experts, 0.0f, bias);
+    float w, l[V];
     load_row((const T*)a.logits + t * a.stride, a.experts, kNone32, l);
-    route_token(a, l, bias, keys[t], chosen, w);
+    route_token(a, l, bias, keys[wave], chosen, w);
     if (lane < a.top) {
       a.chosen[t * a.top + lane] = chosen;
       a.weights[t * a.top + lane] = w;
@@ -333,12 +341,14 @@ template <typename T, int V> __global__ __launch_bounds__(64 * kOneTokens) void 
   if (!a.offsets) return;
   for (int e = tid; e < a.experts; e += N) start[e] = 0;
   __syncthreads();
-  if (tid < n && list[tid] >= 0) atomicAdd(&start[list[tid]], 1);
+  for (int i = tid; i < n; i += N)
+    if (list[i] >= 0) atomicAdd(&start[list[i]], 1);
   __syncthreads();
   const int total = prefix<N>(start, a.experts, part);
   for (int e = tid; e < a.experts; e += N) a.offsets[e] = start[e];
   if (tid == 0) a.offsets[a.experts] = total;
-  if (tid >= total && tid < n) a.rows[tid] = -1;
+  for (int i = tid; i < n; i += N)
+    if (i >= total) a.rows[i] = -1;
   place<N>(a, list, n, 0, start, bits);
 }
 
@@ -487,8 +497,14 @@ __global__ __launch_bounds__(256) void empty_kernel(MoeRoute a) {
 }
 
 template <typename T, int V> hipError_t go_route(const MoeRoute& a, const OrderPlan& p, uint8_t* counts, hipStream_t s) {
-  if (!p.blocks) hipLaunchKernelGGL((route_one_kernel<T, V>), dim3(1), dim3(64 * kOneTokens), 0, s, a);
-  else
+  if (!p.blocks) {
+    if constexpr (V <= 4)
+      if (a.tokens > 8) {
+        hipLaunchKernelGGL((route_one_kernel<T, V, 16>), dim3(1), dim3(64 * 16), 0, s, a);
+        return hipGetLastError();
+      }
+    hipLaunchKernelGGL((route_one_kernel<T, V, 8>), dim3(1), dim3(64 * 8), 0, s, a);
+  } else
     hipLaunchKernelGGL((route_kernel<T, V>), dim3((unsigned)p.blocks), dim3(64 * std::min(p.per, most_waves(V))), 0, s, a,
                        p, counts);
   return hipGetLastError();
@@ -546,7 +562,7 @@ template <typename T> hipError_t run_combine(const MoeCombine& a, hipStream_t st
 }  // namespace
 
 size_t moe_route_ws_bytes(int64_t tokens, int64_t experts, int64_t top) {
-  const OrderPlan p = order_plan(tokens, experts, top);
+  const OrderPlan p = order_plan(tokens, experts, top, true);
   return p.counts + p.sums;
 }
 
@@ -555,7 +571,7 @@ hipError_t launch_moe_route(const MoeRoute& a, void* ws, hipStream_t stream) {
     if (a.offsets) hipLaunchKernelGGL(empty_kernel, dim3(1), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  const OrderPlan p = order_plan(a.tokens, a.experts, a.top);
+  const OrderPlan p = order_plan(a.tokens, a.experts, a.top, a.offsets != nullptr);
   uint8_t* counts = a.offsets ? (uint8_t*)ws : nullptr;
   const hipError_t e = a.dtype == kF32   ? run_route<float>(a, p, counts, stream)
                        : a.dtype == kF16 ? run_route<_Float16>(a, p, counts, stream)

@@ -83,7 +83,7 @@ class I8Tensor:
             scales = scales.view(-1)
         t._rows, t._cols = codes.shape
         t._buf, t._codes, t._scales = None, codes, scales
-        t._check_buffers("I8Tensor")
+        t._check_buffers("I8Tensor", True)
         return t
 
     def _detach(self):
@@ -157,12 +157,12 @@ class I8Tensor:
                 self._check_buffers(name)
         return self._struct
 
-    def _check_buffers(self, name: str):
+    def _check_buffers(self, name: str, shaped: bool = False):
         c, s, rows, cols = self._codes, self._scales, self._rows, self._cols
         index = c.get_device()
         if (c.dtype is not torch.int8 or s.dtype is not torch.float32 or cols % I8_UNIT or s.get_device() != index
-                or c.shape != (rows, cols) or s.dim() != 1 or s.nbytes != 4 * rows or not c.is_contiguous()
-                or not s.is_contiguous()):
+                or not shaped and c.shape != (rows, cols) or s.dim() != 1 or s.nbytes != 4 * rows
+                or not c.is_contiguous() or not s.is_contiguous()):
             raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
                              f"{s.dtype} on {s.device} are no contiguous 8-bit tensor of {rows}x{cols}")
         self._device, self._index, self._at, self._scales_at = c.device, index, c.data_ptr(), s.data_ptr()

@@ -78,16 +78,20 @@ _workspace_bytes = functools.lru_cache(4096)(razer_moe_workspace_bytes)
 
 
 def _new_routes(tokens: int, experts: int, top: int, order: bool, space: int, device):
-    """(routes, their addresses, that of `space` bytes behind them in the same buffer)"""
+    """(routes, their addresses, that of `space` bytes behind them in the same buffer).  The
+    buffer has rows of `top`, so that one split makes most of the views."""
     n = tokens * top
-    head = (4 * n + experts + 1 if order else 2 * n) + 3 & ~3
-    buf = torch.empty(head + (space + 3 >> 2), dtype=torch.int32, device=device)
-    part, shape, strides, at = buf.as_strided, (tokens, top), (top, 1), buf.data_ptr()
-    chosen, weights = part(shape, strides, 0), part(shape, strides, n).view(torch.float32)
     if not order:
-        return MoeRoutes(chosen, weights, None, None, None), (at, at + 4 * n, 0, 0, 0), None
-    return (MoeRoutes(chosen, weights, part((experts + 1,), (1,), 4 * n), part((n,), (1,), 3 * n),
-                      part(shape, strides, 2 * n)),
+        buf = torch.empty(2 * tokens, top, dtype=torch.int32, device=device)
+        chosen, weights = buf.split_with_sizes((tokens, tokens))
+        at = buf.data_ptr()
+        return MoeRoutes(chosen, weights.view(torch.float32), None, None, None), (at, at + 4 * n, 0, 0, 0), None
+    head = 4 * n + experts + 4 & ~3  # the space begins at a multiple of 16 bytes
+    lines = (head + (space + 3 >> 2) + top - 1) // top
+    buf = torch.empty(lines, top, dtype=torch.int32, device=device)
+    chosen, weights, slots, rows, rest = buf.split_with_sizes((tokens, tokens, tokens, tokens, lines - 4 * tokens))
+    at = buf.data_ptr()
+    return (MoeRoutes(chosen, weights.view(torch.float32), rest.as_strided((experts + 1,), (1,)), rows.view(n), slots),
             (at, at + 4 * n, at + 16 * n, at + 12 * n, at + 8 * n), at + 4 * head)
 
 

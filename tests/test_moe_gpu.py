@@ -199,3 +199,17 @@ def test_places_that_no_expert_takes_weigh_nothing():
                 assert r.experts[:3].tolist() == [[5, -1], [2, -1], [-1, -1]]
                 assert (r.weights[:, 1] == 0).all() and (r.weights[2::3] == 0).all()
     assert r.weights[1, 0] == 0 and r.weights[0, 0] == -2.0
+
+
+@pytest.mark.parametrize("experts", [40, 100, 256, 257, 600])
+@pytest.mark.parametrize("tokens", [7, 8, 9, 15, 16, 17, 31, 32, 33])
+def test_where_one_workgroup_ends(tokens, experts):
+    """Up to 32 tokens (16 of more than 64 experts, 8 of more than 256) are routed by one workgroup."""
+    for top in (1, 32):
+        logits = _logits(tokens, experts, tokens * experts).cuda()
+        logits[tokens // 2] = float("-inf")
+        logits[-1, 3] = float("nan")
+        r = _check(logits, top, score="sigmoid")
+        bare = rz.razer_moe_route(logits, top, score="sigmoid", order=False)
+        assert torch.equal(bare.experts, r.experts) and bare.rows is None
+        assert torch.equal(bare.weights.nan_to_num(-1.0), r.weights.nan_to_num(-1.0))
