@@ -15,7 +15,7 @@ int main(int argc, char** argv) {
     } else {
       double us;
       const rz::i8::TilePlan t = rz::i8::tile_plan(m, n, k, experts, 256, us);
-      printf("tile %d %d %d %d %d\n", t.high, t.full, t.rest, t.split, t.halves);
+      printf("tile %d %d %d %d %d %d\n", t.wide, t.high, t.full, t.rest, t.split, t.halves);
     }
   }
 }

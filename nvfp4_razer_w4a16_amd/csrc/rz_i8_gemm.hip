@@ -74,11 +74,13 @@ __device__ __forceinline__ void tile_place(int pos, int mt, int nt, int& im, int
 }
 
 // ---- tile kernel -------------------------------------------------------------
-// A kTileN x BM tile of y (256 rows of W, BM = 256 or 128 of X) per workgroup of four
-// waves (2x2), each wave 128 x (BM/2) in 32x32 accumulators, 128 bytes of K a step.  As
-// many workgroups as CUs; each walks through the tiles.
+// A BN x BM tile of y (256 rows of W by 256 or 128 of X, or 128 by 128) per workgroup of
+// four waves (2x2), each wave (BN/2) x (BM/2) in 32x32 accumulators, 128 bytes of K a step.
+// As many workgroups as CUs, or twice as many of 128 x 128; each walks through the tiles.
+// The larger a tile, the less of what LDS delivers a product takes; the smaller, the fewer
+// products it takes to fill the card, and two workgroups hide each other's results.
 //
-// LDS: a ring of two steps of W and of three of X (160 KiB for BM = 256), filled by
+// LDS: a ring of two steps of W and of three of X (160 KiB for 256 x 256), filled by
 // direct-to-LDS loads of whole 128-byte row pieces.  A piece is eight 16-byte chunks;
 // chunk c of row r lies at place c ^ (r & 7) ^ (r >> 3 & 1), so that 16 lanes of a
 // fragment read (one chunk of 16 rows) cover all banks.  Direct loads write lane-linear,
@@ -100,18 +102,20 @@ __device__ __forceinline__ void tile_place(int pos, int mt, int nt, int& im, int
 // first size at 2.2.  Bound by power, then by its results: a step takes 1.46 us, 2.95 POP/s
 // (on zeros, which power does not hold down, 0.98 us, 4.4), and between two tiles lie some
 // 10 us, half of them the stores of 256 CUs at once.  The matrix units are busy 72 % of
-// the time.
-template <int BM, typename OT, bool GROUPED>
-__global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) {
-  constexpr int BN = kTileN;
+// the time.  Tiles of 128 x 128: 1024 x 4096 x 4096 22 us (256 x 128: 27), 256 x 8192 x 1024
+// 9.6 us (12.9); with two on a CU its LDS is busy all the time, 1.05 us a step.
+template <int BN, int BM, typename OT, bool GROUPED>
+__global__ __launch_bounds__(256, BN == 256 ? 1 : 2) void i8_tile_kernel(Args a, TilePlan plan) {
   constexpr int NI = BN / 64, MI = BM / 64;      // 32-row fragments of a wave
   constexpr int NL = BN / 32, ML = BM / 32;      // direct loads of a wave and step
   __shared__ __attribute__((aligned(16))) uint8_t w0[BN * kStepB], w1[BN * kStepB];
   __shared__ __attribute__((aligned(16))) uint8_t x0[BM * kStepB], x1[BM * kStepB], x2[BM * kStepB];
   // scales of the tile's columns and rows, and which rows are padding: behind the results' place in x2
-  // where that is large enough (and all other LDS taken)
+  // where that is large enough (and all other LDS taken); in w1, which is then loaded behind the
+  // results, where two workgroups share the LDS
   constexpr int kOut = 4 * 32 * 128, kScales = (BN + BM) * 4 + 32;
-  __shared__ __attribute__((aligned(16))) uint8_t own[BM == 256 ? 16 : kScales];
+  constexpr bool kInW1 = BN == 128;
+  __shared__ __attribute__((aligned(16))) uint8_t own[BM == 256 || kInW1 ? 16 : kScales];
   static_assert(BM != 256 || kOut + kScales <= BM * kStepB, "x2 holds both");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
@@ -207,7 +211,7 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
 #pragma unroll
     for (int i = 0; i < ML; i++) ox[i] = (uint32_t)(min((int64_t)max(r.x[i], 0), span - 1) * a.k);
     none = r.scale < 0 || r.scale >= span;
-    sw = a.ws[wr + min(tid, w_rows - 1)];
+    sw = a.ws[wr + min(tid % BN, w_rows - 1)];
     sx = a.xs[first + (none ? 0 : r.scale)];
   };
   auto load_w = [&](int s, uint8_t* l) {
@@ -263,7 +267,7 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
     for (int i = 0; i < NI * MI; i++) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (i % 2 && i / 2 < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (BN == 128 ? i < loads : i % 2 && i / 2 < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -340,10 +344,10 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
 
     // ---- this tile's results, under which the next one's first steps are loaded
     const Spot done = spot;
-    uint8_t* scl = BM == 256 ? x2 + kOut : own;
+    uint8_t* scl = BM == 256 ? x2 + kOut : kInW1 ? w1 : own;
     __builtin_amdgcn_s_waitcnt(vm_lgkm(0, 0));  // nothing of this tile is under way
     meet();                                     // or read any more
-    *(float*)(scl + tid * 4) = sw;
+    if (BN == 256 || tid < BN) *(float*)(scl + tid * 4) = sw;
     if (BM == 256 || tid < BM) *(float*)(scl + (BN + tid) * 4) = sx;
     if (GROUPED) *(uint64_t*)(scl + (BN + BM) * 4 + wave * 8) = __ballot(none);
     if (item < items) {
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       load_x(0, x0);
       load_w(0, w0);
       load_x(1, x1);
-      load_w(1, w1);
+      if (!kInW1) load_w(1, w1);
     }
     __builtin_amdgcn_s_waitcnt(vm_lgkm(63, 0));
     meet();
@@ -439,6 +443,10 @@ __global__ __launch_bounds__(256, 1) void i8_tile_kernel(Args a, TilePlan plan) 
       }
     }
     if (item >= items) return;
+    if (kInW1) {
+      meet();  // nobody reads the scales any more
+      load_w(1, w1);
+    }
   }
 }
 
@@ -763,9 +771,8 @@ hipError_t run_stream(const Args& a, int y_dtype, const StreamPlan& p, hipStream
 
 // y of the split tiles: adds the slices' sums.  A thread takes 16 sums of one fragment
 // in register order; the half-waves swap so that each lane stores runs of eight columns.
-template <int BM, typename OT>
+template <int BN, int BM, typename OT>
 __global__ __launch_bounds__(256) void i8_fold_kernel(Args a, TilePlan plan) {
-  constexpr int BN = kTileN;
   constexpr int NI = BN / 64, MI = BM / 64;
   typedef OT V8 __attribute__((ext_vector_type(8)));
   const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
@@ -804,15 +811,19 @@ __global__ __launch_bounds__(256) void i8_fold_kernel(Args a, TilePlan plan) {
   }
 }
 
-template <int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
-  const int grid = std::min(p.full + p.rest * p.split, p.cus);
-  hipLaunchKernelGGL((i8_tile_kernel<BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
+template <int BN, int BM, typename OT, bool GROUPED> hipError_t go_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
+  const int grid = std::min(p.full + p.rest * p.split, p.cus * wgs_of(BN));
+  hipLaunchKernelGGL((i8_tile_kernel<BN, BM, OT, GROUPED>), dim3((unsigned)grid), dim3(256), 0, stream, a, p);
   return hipGetLastError();
 }
+template <typename OT, bool GROUPED> hipError_t any_tiles(const Args& a, const TilePlan& p, hipStream_t stream) {
+  if (p.wide == 128) return go_tiles<128, 128, OT, GROUPED>(a, p, stream);
+  return p.high == 256 ? go_tiles<256, 256, OT, GROUPED>(a, p, stream) : go_tiles<256, 128, OT, GROUPED>(a, p, stream);
+}
 
-template <int BM, typename OT> hipError_t go_fold(const Args& a, const TilePlan& p, hipStream_t stream) {
-  hipLaunchKernelGGL((i8_fold_kernel<BM, OT>), dim3((unsigned)(p.rest * (kTileN / 64) * (BM / 64))), dim3(256), 0,
-                     stream, a, p);
+template <int BN, int BM, typename OT> hipError_t go_fold(const Args& a, const TilePlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((i8_fold_kernel<BN, BM, OT>), dim3((unsigned)(p.rest * (BN / 64) * (BM / 64))), dim3(256), 0, stream,
+                     a, p);
   return hipGetLastError();
 }
 
@@ -820,7 +831,7 @@ template <typename OT> hipError_t run(const Args& a, int cus, void* ws, hipStrea
   double us;
   TilePlan p = tile_plan(a.m, a.n, a.k, a.offsets ? a.experts : 0, cus, us);
   p.part = (int32_t*)ws;
-  if (a.offsets) return p.high == 256 ? go_tiles<256, OT, true>(a, p, stream) : go_tiles<128, OT, true>(a, p, stream);
+  if (a.offsets) return any_tiles<OT, true>(a, p, stream);
   TilePlan halves = p;
   if (p.halves) {  // the tiles of whole rounds, then the rest in halves
     halves.first = p.full - p.halves;
@@ -829,11 +840,11 @@ template <typename OT> hipError_t run(const Args& a, int cus, void* ws, hipStrea
     p.halves = 0;
   }
   hipError_t e = hipSuccess;
-  if (p.full + p.rest > 0)
-    e = p.high == 256 ? go_tiles<256, OT, false>(a, p, stream) : go_tiles<128, OT, false>(a, p, stream);
-  if (e == hipSuccess && halves.halves) return go_tiles<128, OT, false>(a, halves, stream);
+  if (p.full + p.rest > 0) e = any_tiles<OT, false>(a, p, stream);
+  if (e == hipSuccess && halves.halves) return go_tiles<256, 128, OT, false>(a, halves, stream);
   if (e != hipSuccess || !p.rest) return e;
-  return p.high == 256 ? go_fold<256, OT>(a, p, stream) : go_fold<128, OT>(a, p, stream);
+  if (p.wide == 128) return go_fold<128, 128, OT>(a, p, stream);
+  return p.high == 256 ? go_fold<256, 256, OT>(a, p, stream) : go_fold<256, 128, OT>(a, p, stream);
 }
 
 }  // namespace

@@ -18,7 +18,7 @@ CLANG = "/opt/rocm/llvm/bin/clang++"
 @pytest.fixture(scope="module")
 def plan(tmp_path_factory):
     """plan(m, n, k, experts) -> ("stream", row tiles a chunk, chunks a row, X tiles of 16 rows, rows a job)
-    or ("tile", rows, whole tiles, split tiles, slices, tiles done in halves)."""
+    or ("tile", rows of W, rows of X, whole tiles, split tiles, slices, tiles done in halves)."""
     if not os.path.exists(CLANG):
         pytest.skip("ROCm clang missing")
     exe = str(tmp_path_factory.mktemp("plan") / "i8_plan")
@@ -43,18 +43,27 @@ def test_every_form_of_the_stream_kernel(plan):
     assert {p[1:4] for p in (plan(*s) for s in shapes.GROUPS) if p[0] == "stream"} == FORMS
 
 
+SHAPES = {(256, 256), (256, 128), (128, 128)}  # rows of W and of X of a tile
+
+
 def test_tiles(plan):
-    """Both heights, more tiles than compute units, halves with and without rows, K cut or not."""
+    """Every shape with more tiles than workgroups and with fewer, with K cut (of all tiles, and of the
+    last ones alone) and with experts; halves with and without rows."""
+    def slots(p):
+        return 512 if p[1] == 128 else 256
+
     got = [plan(*s) for s in shapes.TILES]
-    assert {p[:2] for p in got} == {("tile", 128), ("tile", 256)}
-    assert {p[1] for p in got if p[2] > 256} == {128, 256}
+    assert {p[0] for p in got} == {"tile"} and {p[1:3] for p in got if p[3] > slots(p)} == SHAPES
+    got = [plan(*s) for s in shapes.TILES + shapes.SLICES]
+    assert {p[1:3] for p in got if 0 < p[3] <= slots(p) and p[4] == 0} == SHAPES
     got = [plan(*s) for s in shapes.HALVES]
-    assert all(p[:2] == ("tile", 256) and p[5] > 0 for p in got)
+    assert all(p[:3] == ("tile", 256, 256) and p[6] > 0 for p in got)
     assert any(m % 256 in range(1, 129) for m, _, _ in shapes.HALVES)  # a half without rows
     got = [plan(*s) for s in shapes.SLICES]
-    assert {p[:2] for p in got if p[4] > 1} == {("tile", 128), ("tile", 256)}
-    assert {plan(*s)[:2] for s in shapes.GROUPS if plan(*s)[0] == "tile"} == {("tile", 128), ("tile", 256)}
-    assert any(plan(*s)[2] > 256 for s in shapes.GROUPS if plan(*s)[0] == "tile")
+    assert {p[1:3] for p in got if p[5] > 1} == SHAPES
+    assert {p[3] > 0 for p in got if p[5] > 1} == {False, True}
+    got = [p for p in (plan(*s) for s in shapes.GROUPS) if p[0] == "tile"]
+    assert {p[1:3] for p in got} == SHAPES and {p[1:3] for p in got if p[3] > slots(p)} == SHAPES
 
 
 def test_both_kernels_in_the_tests_of_values(plan):
@@ -63,8 +72,9 @@ def test_both_kernels_in_the_tests_of_values(plan):
 
 @pytest.mark.parametrize("m,n,k,experts,want", [
     (1, 14336, 4096, 0, ("stream", 1, 2, 1)), (27, 28672, 8192, 0, ("stream", 1, 4, 2)), (1, 4096, 14336, 0, ("stream", 1, 8, 1)),
-    (2048, 28672, 8192, 0, ("tile", 256)), (16, 14336, 4096, 8, ("stream", 1, 2, 1)), (8192, 14336, 4096, 8, ("tile", 256)),
-    (999, 1503, 2080, 64, ("stream", 1, 2, 2)), (1, 8192, 16384, 0, ("stream", 1, 8, 1)), (1, 8192, 16400, 0, ("tile", 128)),
+    (2048, 28672, 8192, 0, ("tile", 256, 256)), (16, 14336, 4096, 8, ("stream", 1, 2, 1)), (8192, 14336, 4096, 8, ("tile", 256, 256)),
+    (999, 1503, 2080, 64, ("stream", 1, 2, 2)), (1, 8192, 16384, 0, ("stream", 1, 8, 1)), (1, 8192, 16400, 0, ("tile", 256, 128)),
+    (1024, 4096, 4096, 0, ("tile", 128, 128)), (2048, 4096, 4096, 0, ("tile", 256, 128)), (512, 14336, 4096, 0, ("tile", 256, 128)),
 ])
 def test_forms_of_ordinary_sizes(plan, m, n, k, experts, want):
     assert plan(m, n, k, experts)[:len(want)] == want

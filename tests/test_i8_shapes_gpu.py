@@ -41,9 +41,11 @@ def test_few_rows(m, n, k):
     _check(m, n, k)
 
 
-TILES = [(4096, 4096, 1040), (8192, 4111, 528), (4100, 4099, 528), (3000, 8000, 144), (2300, 8000, 16), (1500, 9000, 128)]
-HALVES = [(6200, 3500, 1296), (5700, 4000, 2000), (2600, 7168, 2048)]
-SLICES = [(1024, 4096, 14336), (1000, 4090, 14336), (900, 2040, 16400), (1030, 3000, 9008), (100, 260, 16400)]
+TILES = [(4096, 4096, 1040), (8192, 4111, 528), (4100, 4099, 528), (3000, 8000, 144), (2300, 8000, 16), (1500, 9000, 128),
+         (6200, 3500, 1296), (5537, 8530, 1040), (2112, 7887, 1168), (1259, 5439, 5008), (600, 2000, 1008)]
+HALVES = [(5700, 4000, 2000), (2600, 7168, 2048), (4907, 7097, 1296)]
+SLICES = [(1024, 4096, 14336), (1000, 4090, 14336), (900, 2040, 16400), (1030, 3000, 9008), (100, 260, 16400),
+          (299, 7026, 9360), (1361, 5987, 7376), (4161, 4018, 5664), (1450, 866, 8592)]
 
 
 @pytest.mark.parametrize("m,n,k", TILES + HALVES + SLICES)
@@ -62,7 +64,8 @@ def sizes_of(total, experts, seed):
 GROUPS = [(40, 2000, 512, 8), (40, 2000, 480, 8), (100, 3000, 512, 8), (40, 2000, 1024, 8), (90, 2000, 1008, 5),
           (40, 2000, 2048, 8), (90, 2000, 2048, 5), (200, 2000, 2048, 8), (40, 900, 4096, 8), (90, 900, 4096, 5),
           (700, 300, 4096, 20), (40, 900, 8192, 8), (200, 900, 8192, 8), (40, 900, 16384, 8), (1000, 24, 64, 500),
-          (9000, 3000, 656, 8), (9000, 3001, 656, 100), (3000, 2000, 528, 4), (12000, 1100, 528, 5), (700, 900, 16400, 4)]
+          (9000, 3000, 656, 8), (9000, 3001, 656, 100), (3000, 2000, 528, 4), (12000, 1100, 528, 5), (700, 900, 16400, 4),
+          (2304, 1323, 1232, 50), (2689, 3565, 1040, 4)]
 
 
 @pytest.mark.parametrize("gather", [False, True])
