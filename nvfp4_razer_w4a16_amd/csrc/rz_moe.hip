@@ -15,7 +15,8 @@
 // choice) and 6.8 us of order; 333 tokens of 64 experts 4.3 and 5.2 us; one token, in one
 // launch, 6.2 us of latency.  (Comparing fp64 scores across the wave took 33-43 us.)
 // Combine is bound by memory: 8192 tokens of 8 rows of 4096 in bf16 131-134 us (671 MB, 5.0-5.1
-// TB/s; a copy of 1 GiB reaches 5.1).  A thread takes 16 bytes of a row and adds up its
+// TB/s; a copy of 1 GiB reaches 5.1), 4124 of 3 rows of 746 in f32 11.7 us (4.2 TB/s; an element
+// a thread took 18.7).  A thread takes 16 bytes of a row and adds up its
 // token's rows in registers, so that every row is read once and nothing meets elsewhere.
 #include <algorithm>
 
@@ -518,15 +519,37 @@ template <typename T> hipError_t run_route(const MoeRoute& a, const OrderPlan& p
   return go_route<T, 16>(a, p, counts, s);
 }
 
-// N elements of a row a thread, at once where N > 1.
-template <typename T, int N> __global__ __launch_bounds__(256) void combine_kernel(MoeCombine a) {
+// N elements of a row a thread, 2^shift threads a row (or a piece of it).  ALIGNED: rows at
+// multiples of 16 bytes, of whole pieces; otherwise loads and stores cross lines, and where
+// a row's last piece is shorter its thread takes the row's last N elements and stores what
+// is its own (the others may be another thread's result already).  WAVE: a wave has one row, whose slots and weights then take
+// scalar loads.
+template <typename T, int N, bool ALIGNED, bool WAVE> __global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int shift) {
   typedef T V __attribute__((ext_vector_type(N)));
-  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;
-  if (c >= a.cols) return;
-  for (int64_t t = blockIdx.y; t < a.tokens; t += gridDim.y) {
+  const int64_t own = (((int64_t)blockIdx.x << shift) + (threadIdx.x & ((1u << shift) - 1))) * N;
+  if (own >= a.cols) return;
+  const int64_t c = ALIGNED ? own : min(own, max(a.cols - N, (int64_t)0));
+  const int skip = (int)(own - c), end = (int)min(a.cols - c, (int64_t)N);
+  auto load = [&](const void* rows, int64_t at) {
+    const T* p = (const T*)rows + at;
+    V v = {};
+    if (ALIGNED) {
+      v = *(const V*)p;
+    } else if (end == N) {
+      __builtin_memcpy(&v, p, sizeof(V));
+    } else {  // rows shorter than a piece
+#pragma unroll
+      for (int i = 0; i < N - 1; i++)
+        if (i < end) v[i] = p[i];
+    }
+    return v;
+  };
+  const int64_t step = (int64_t)gridDim.y * (256 >> shift);
+  const int row = WAVE ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> shift) : (int)threadIdx.x >> shift;
+  for (int64_t t = (int64_t)blockIdx.y * (256 >> shift) + row; t < a.tokens; t += step) {
     float v[N];
     if (a.add) {
-      const V add = *(const V*)((const T*)a.add + t * a.add_stride + c);
+      const V add = load(a.add, t * a.add_stride + c);
 #pragma unroll
       for (int i = 0; i < N; i++) v[i] = (float)add[i];
     } else {
@@ -537,25 +560,40 @@ template <typename T, int N> __global__ __launch_bounds__(256) void combine_kern
       const int64_t s = a.slots[t * a.top + j];
       const float w = a.weights[t * a.top + j];
       V y = {};
-      if (s >= 0 && s < a.y_rows) y = *(const V*)((const T*)a.y + s * a.y_stride + c);
+      if (s >= 0 && s < a.y_rows) y = load(a.y, s * a.y_stride + c);
 #pragma unroll
       for (int i = 0; i < N; i++) v[i] += w * (float)y[i];
     }
     V o;
 #pragma unroll
     for (int i = 0; i < N; i++) o[i] = mx_cvt<T>(v[i]);
-    *(V*)((T*)a.out + t * a.cols + c) = o;
+    T* out = (T*)a.out + t * a.cols + c;
+    if (ALIGNED) {
+      *(V*)out = o;
+    } else if (skip == 0 && end == N) {
+      __builtin_memcpy(out, &o, sizeof(V));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i++)
+        if (i >= skip && i < end) out[i] = o[i];
+    }
   }
 }
 
 template <typename T> hipError_t run_combine(const MoeCombine& a, hipStream_t stream) {
-  constexpr int kAll = 16 / sizeof(T);
+  constexpr int N = 16 / sizeof(T);
   const uintptr_t any = (uintptr_t)a.y | (uintptr_t)a.add | (uintptr_t)a.out | (uintptr_t)(a.cols * sizeof(T)) |
                         (uintptr_t)(a.y_stride * sizeof(T)) | (uintptr_t)(a.add ? a.add_stride * sizeof(T) : 0);
-  const int n = any & 15 ? 1 : kAll;
-  const dim3 grid((unsigned)((a.cols + 256 * n - 1) / (256 * n)), (unsigned)std::min(a.tokens, (int64_t)65535));
-  if (n == 1) hipLaunchKernelGGL((combine_kernel<T, 1>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((combine_kernel<T, kAll>), grid, dim3(256), 0, stream, a);
+  const int64_t pieces = (a.cols + N - 1) / N;
+  int shift = 0;
+  while (shift < 8 && 1 << shift < pieces) shift++;
+  const int64_t rows = 256 >> shift;
+  const dim3 grid((unsigned)((pieces + (1 << shift) - 1) >> shift), (unsigned)std::min((a.tokens + rows - 1) / rows, (int64_t)65535));
+  const bool aligned = !(any & 15), wave = shift >= 6;
+  if (aligned && wave) hipLaunchKernelGGL((combine_kernel<T, N, true, true>), grid, dim3(256), 0, stream, a, shift);
+  else if (aligned) hipLaunchKernelGGL((combine_kernel<T, N, true, false>), grid, dim3(256), 0, stream, a, shift);
+  else if (wave) hipLaunchKernelGGL((combine_kernel<T, N, false, true>), grid, dim3(256), 0, stream, a, shift);
+  else hipLaunchKernelGGL((combine_kernel<T, N, false, false>), grid, dim3(256), 0, stream, a, shift);
   return hipGetLastError();
 }
 

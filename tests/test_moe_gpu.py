@@ -213,3 +213,32 @@ def test_where_one_workgroup_ends(tokens, experts):
         bare = rz.razer_moe_route(logits, top, score="sigmoid", order=False)
         assert torch.equal(bare.experts, r.experts) and bare.rows is None
         assert torch.equal(bare.weights.nan_to_num(-1.0), r.weights.nan_to_num(-1.0))
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("cols", [1, 2, 7, 8, 9, 24, 63, 100, 127, 129, 520, 2047, 2051, 4097])
+def test_combine_widths(cols, dtype):
+    """Rows shorter and longer than a workgroup's, that end inside 16 bytes, at every offset: nothing
+    beside the result is written, nothing behind a row is read (it is NaN)."""
+    dt, tokens, top = DT[dtype], 37, 3
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    wide = torch.full((50, cols + 5), float("nan"), dtype=dt, device="cuda")
+    buffer = torch.full((tokens * cols + 17,), 7.0, dtype=dt, device="cuda")
+    slots = torch.randint(-1, 51, (tokens, top), generator=g, device="cuda").int()
+    weights = torch.rand(tokens, top, generator=g, device="cuda")
+    base = torch.randn(tokens, cols, generator=g, device="cuda").to(dt)
+    for at in (0, 1, 4):
+        y = wide[:, at:at + cols]
+        wide.fill_(float("nan"))
+        y.copy_(torch.randn(50, cols, generator=g, device="cuda"))
+        out = buffer[at:at + tokens * cols].view(tokens, cols)
+        buffer.fill_(7.0)
+        rz.razer_moe_combine(y, slots, weights, base, out=out)
+        want, size = ref.combine(y.double().cpu().numpy(), slots.cpu().numpy(), weights.double().cpu().numpy(),
+                                 base.double().cpu().numpy())
+        bound = (2 * top + 1) * 2.0 ** -24 * size + torch.finfo(dt).eps / 2 * np.abs(want) * 1.01
+        bound += 2.0 ** -25 if dt is torch.float16 else 0  # half a step of its subnormals
+        assert (np.abs(out.double().cpu().numpy() - want) <= bound).all()
+        assert (buffer[:at] == 7.0).all() and (buffer[at + tokens * cols:] == 7.0).all()
+        place = base.clone()
+        assert torch.equal(rz.razer_moe_combine(y, slots, weights, place, out=place), out)
