@@ -58,8 +58,8 @@ class I8Tensor:
     codes: int8 [rows, cols], scales: float32 [rows].  rows, cols and buffers can be
     replaced; a call refuses a tensor whose buffers do not match its shape."""
 
-    # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers it was
-    # given, when their shapes were last looked at; _struct: the razer_i8 as of then
+    # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers (of its own:
+    # the one) when they were last looked at; _struct: the razer_i8 as of then
     __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at", "_struct")
 
     def __init__(self, rows: int, cols: int, device):
@@ -67,10 +67,15 @@ class I8Tensor:
             raise ValueError(f"cols must be a multiple of {I8_UNIT}")
         self._rows, self._cols = rows, cols
         # one buffer for both: codes, then scales; their views are made when asked for
-        self._buf = buf = torch.empty(rows * (cols + 4), dtype=torch.int8, device=device)
-        self._device, self._index, at = buf.device, buf.get_device(), buf.data_ptr()
+        self._buf = torch.empty(rows * (cols + 4), dtype=torch.int8, device=device)
         self._codes = self._scales = None
-        self._struct = _struct_bytes(rows, cols, at, at + rows * cols)
+        self._place()
+
+    def _place(self):
+        """Where its own buffer is."""
+        buf, rows, cols = self._buf, self._rows, self._cols
+        self._device, self._index, self._at = buf.device, buf.get_device(), buf.data_ptr()
+        self._struct = _struct_bytes(rows, cols, self._at, self._at + rows * cols)
 
     @classmethod
     def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "I8Tensor":
@@ -149,8 +154,13 @@ class I8Tensor:
     def _checked(self, name: str) -> bytes:
         """The razer_i8 of buffers that match the shape.  The owner of buffers that it
         was given may have changed them since: every call looks where they are and
-        how long, and at the rest if they have moved."""
-        if self._buf is None:
+        how long, and at the rest if they have moved.  (The one of its own moves with a
+        copy of the whole, or a load from a file.)"""
+        if self._buf is not None:
+            if self._buf.data_ptr() != self._at:
+                self._codes = self._scales = None
+                self._place()
+        else:
             c, s, rows = self._codes, self._scales, self._rows
             if (c.data_ptr() != self._at or s.data_ptr() != self._scales_at or c.nbytes != rows * self._cols
                     or s.nbytes != 4 * rows):

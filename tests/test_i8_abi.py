@@ -239,3 +239,27 @@ def test_backward_raises():
             got.sum().backward()
         with torch.no_grad():
             assert not rz.razer_moe_combine(t[0], want.slots, t[1], t[2]).requires_grad
+
+
+@pytest.mark.parametrize("owned", [True, False])
+def test_a_copy_is_where_its_buffers_are(owned):
+    """A tensor copied whole, or saved and loaded, is taken from its own buffers."""
+    import copy
+    import pickle
+
+    t = rz.I8Tensor(3, 32, "cpu")
+    t.codes.copy_(torch.arange(96).view(3, 32))
+    t.scales.fill_(2.0)
+    if not owned:
+        t = rz.I8Tensor.of(t.codes.clone(), t.scales.clone())
+    for other in (copy.deepcopy(t), pickle.loads(pickle.dumps(t))):
+        packed = razer_i8.from_buffer_copy(other._checked("t"))
+        assert (packed.rows, packed.cols) == (3, 32)
+        assert packed.codes == other.codes.data_ptr() != t.codes.data_ptr()
+        assert packed.scales == other.scales.data_ptr() != t.scales.data_ptr()
+        assert torch.equal(other.codes, t.codes) and torch.equal(other.scales, t.scales)
+        other.codes[0, 0] = 9
+        other.scales[1] = 3.0
+        assert ctypes.string_at(packed.codes, 1) == b"\x09" and t.codes[0, 0] == 0
+        assert ctypes.c_float.from_address(packed.scales + 4).value == 3.0 and t.scales[1] == 2.0
+    assert razer_i8.from_buffer_copy(t._checked("t")).codes == t.codes.data_ptr()
