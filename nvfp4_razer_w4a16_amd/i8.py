@@ -67,15 +67,12 @@ class I8Tensor:
             raise ValueError(f"cols must be a multiple of {I8_UNIT}")
         self._rows, self._cols = rows, cols
         # one buffer for both: codes, then scales; their views are made when asked for
-        self._buf = torch.empty(rows * (cols + 4), dtype=torch.int8, device=device)
-        self._codes = self._scales = None
-        self._place()
+        self._own(torch.empty(rows * (cols + 4), dtype=torch.int8, device=device))
 
-    def _place(self):
-        """Where its own buffer is."""
-        buf, rows, cols = self._buf, self._rows, self._cols
+    def _own(self, buf: torch.Tensor):
+        self._buf, self._codes, self._scales = buf, None, None
         self._device, self._index, self._at = buf.device, buf.get_device(), buf.data_ptr()
-        self._struct = _struct_bytes(rows, cols, self._at, self._at + rows * cols)
+        self._struct = _struct_bytes(self._rows, self._cols, self._at, self._at + self._rows * self._cols)
 
     @classmethod
     def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "I8Tensor":
@@ -158,8 +155,7 @@ class I8Tensor:
         copy of the whole, or a load from a file.)"""
         if self._buf is not None:
             if self._buf.data_ptr() != self._at:
-                self._codes = self._scales = None
-                self._place()
+                self._own(self._buf)
         else:
             c, s, rows = self._codes, self._scales, self._rows
             if (c.data_ptr() != self._at or s.data_ptr() != self._scales_at or c.nbytes != rows * self._cols
