@@ -10,9 +10,9 @@
 // Combine: out[t] = add[t] + sum_j w[t, j] y[slots[t, j]].
 //
 // Route and order are bound by instructions and by launches: 8192 tokens of 256 experts,
-// 8 of them out of 4 of 8 groups by sigmoid, 17.6-18.6 us of route (some 700 vector
-// instructions a token: a quarter of them the fp64 scores, a quarter the groups, 25 for each
-// choice) and 6.8 us of order; 333 tokens of 64 experts 4.3 and 5.2 us; one token, in one
+// 8 of them out of 4 of 8 groups by sigmoid, 17.3-17.7 us of route (690 vector
+// instructions a token: 300 for logits and fp64 scores, 165 for the groups, 25 for each
+// choice) and 6.6 us of order; 333 tokens of 64 experts 4.3 and 5.2 us; one token, in one
 // launch, 6.2 us of latency.  (Comparing fp64 scores across the wave took 33-43 us.)
 // Combine is bound by memory: 8192 tokens of 8 rows of 4096 in bf16 131-134 us (671 MB, 5.0-5.1
 // TB/s; a copy of 1 GiB reaches 5.1), 4124 of 3 rows of 746 in f32 11.7 us (4.2 TB/s; an element
@@ -165,10 +165,17 @@ __device__ __forceinline__ void route_token(const MoeRoute& a, const float (&l)[
       first = max(first, f);
     }
     const double score = a.best == 2 && second > kNone ? first + second : first;
-    int before = 0;
-    for (int g = 0; g < a.groups; g++) {
-      const double other = lane_value(score, g * per);
-      before += other > score || (other == score && g < group);
+    int before = 0;  // groups that are better
+    if (a.groups <= per) {  // a lane compares its group with one other
+      const int g = lane % per;
+      const double other = __shfl(score, min(g, a.groups - 1) * per, 64);
+      const uint64_t better = __ballot(g < a.groups && (other > score || (other == score && g < group)));
+      before = __popc((uint32_t)(better >> (group * per & 63)) & (uint32_t)((1ull << per) - 1));
+    } else {
+      for (int g = 0; g < a.groups; g++) {
+        const double other = lane_value(score, g * per);
+        before += other > score || (other == score && g < group);
+      }
     }
     const uint64_t kept = __ballot(before < a.kept);
     const uint32_t mul = (1u << 20) / (uint32_t)size + 1;  // e / size for e < 1024
