@@ -28,6 +28,7 @@ from .mx import (_check, _dtype, _entered, _grad_enabled, _on_gpu, _rows_of, _sp
 
 I8_UNIT = 16
 RAZER_I8_MAX_K = 131056
+_i8, _f32 = torch.int8, torch.float32
 
 
 class razer_i8(ctypes.Structure):
@@ -56,11 +57,13 @@ class I8Tensor:
     """An 8-bit integer tensor in device memory.
 
     codes: int8 [rows, cols], scales: float32 [rows].  rows, cols and buffers can be
-    replaced; a call refuses a tensor whose buffers do not match its shape."""
+    replaced, or changed in place; a call takes what codes and scales show, and refuses a
+    tensor whose buffers do not match its shape."""
 
-    # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers (of its own:
-    # the one) when they were last looked at; _struct: the razer_i8 as of then
-    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at", "_struct")
+    # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers when they were
+    # last looked at, and what shapes they had; _struct: the razer_i8 as of then
+    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at",
+                 "_codes_shape", "_scales_shape", "_struct")
 
     def __init__(self, rows: int, cols: int, device):
         if rows < 0 or cols < 0 or cols % I8_UNIT:
@@ -72,20 +75,23 @@ class I8Tensor:
     def _own(self, buf: torch.Tensor):
         self._buf, self._codes, self._scales = buf, None, None
         self._device, self._index, self._at = buf.device, buf.get_device(), buf.data_ptr()
-        self._struct = _struct_bytes(self._rows, self._cols, self._at, self._at + self._rows * self._cols)
+        self._scales_at = self._at + self._rows * self._cols
+        self._struct = _struct_bytes(self._rows, self._cols, self._at, self._scales_at)
 
     @classmethod
     def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "I8Tensor":
         """The tensor that these buffers hold (shared, not copied); leading
         dimensions, such as a stack of experts, are rows."""
         t = cls.__new__(cls)
-        if codes.dim() != 2:
-            codes = codes.view(-1, codes.shape[-1])
+        shape = codes.shape
+        if len(shape) != 2:
+            codes = codes.view(-1, shape[-1])
+            shape = codes.shape
         if scales.dim() != 1:
             scales = scales.view(-1)
-        t._rows, t._cols = codes.shape
+        t._rows, t._cols = shape
         t._buf, t._codes, t._scales = None, codes, scales
-        t._check_buffers("I8Tensor", True)
+        t._check_buffers("I8Tensor", shape)
         return t
 
     def _detach(self):
@@ -149,29 +155,35 @@ class I8Tensor:
         return self._device
 
     def _checked(self, name: str) -> bytes:
-        """The razer_i8 of buffers that match the shape.  The owner of buffers that it
-        was given may have changed them since: every call looks where they are and
-        how long, and at the rest if they have moved.  (The one of its own moves with a
-        copy of the whole, or a load from a file.)"""
+        """The razer_i8 of buffers that match the shape.  Whoever holds the codes or scales
+        may have changed them in place since (`.data =`, `t_`, `resize_`): every call looks at
+        those that anybody has seen, and at the rest if they are not as they were.  (The one
+        buffer of its own moves with a copy of the whole, or a load from a file.)"""
+        c, s = self._codes, self._scales
         if self._buf is not None:
-            if self._buf.data_ptr() != self._at:
-                self._own(self._buf)
-        else:
-            c, s, rows = self._codes, self._scales, self._rows
-            if (c.data_ptr() != self._at or s.data_ptr() != self._scales_at or c.nbytes != rows * self._cols
-                    or s.nbytes != 4 * rows):
-                self._check_buffers(name)
+            if c is None and s is None:
+                if self._buf.data_ptr() != self._at:
+                    self._own(self._buf)
+                return self._struct
+            # from here on what is seen counts, not the buffer behind it
+            self._detach()
+            c, s = self._codes, self._scales
+        if (c.data_ptr() != self._at or s.data_ptr() != self._scales_at or c.shape != self._codes_shape
+                or s.shape != self._scales_shape or c.dtype is not _i8 or s.dtype is not _f32
+                or not c.is_contiguous() or not s.is_contiguous()):
+            self._check_buffers(name)
         return self._struct
 
-    def _check_buffers(self, name: str, shaped: bool = False):
+    def _check_buffers(self, name: str, codes_shape=None):
         c, s, rows, cols = self._codes, self._scales, self._rows, self._cols
-        index = c.get_device()
-        if (c.dtype is not torch.int8 or s.dtype is not torch.float32 or cols % I8_UNIT or s.get_device() != index
-                or not shaped and c.shape != (rows, cols) or s.dim() != 1 or s.nbytes != 4 * rows
+        index, codes_shape, scales_shape = c.get_device(), codes_shape or c.shape, s.shape
+        if (c.dtype is not _i8 or s.dtype is not _f32 or cols % I8_UNIT or s.get_device() != index
+                or codes_shape != (rows, cols) or scales_shape != (rows,)
                 or not c.is_contiguous() or not s.is_contiguous()):
             raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
                              f"{s.dtype} on {s.device} are no contiguous 8-bit tensor of {rows}x{cols}")
         self._device, self._index, self._at, self._scales_at = c.device, index, c.data_ptr(), s.data_ptr()
+        self._codes_shape, self._scales_shape = codes_shape, scales_shape
         self._struct = _struct_bytes(rows, cols, self._at, self._scales_at)
 
 
