@@ -103,11 +103,14 @@ class MxTensor:
 
     codes: uint8 [rows, cols // 2], the even column in the low half of a byte;
     scales: uint8 [rows, cols // 32].  rows, cols and buffers can be replaced; a call
-    refuses a tensor whose buffers do not match its shape."""
+    refuses a tensor whose buffers do not match its shape, also where buffers that it was
+    given were changed in place.  (One that made its own buffer keeps to that, whatever is
+    done in place to the shapes or memory of the codes and scales it shows.)"""
 
     # _index: the GPU, -1 without one; _at, _scales_at: addresses of the buffers it was
-    # given, when their shapes were last looked at
-    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at")
+    # given, when they were last looked at, and what shapes they had
+    __slots__ = ("_rows", "_cols", "_buf", "_codes", "_scales", "_device", "_index", "_at", "_scales_at",
+                 "_codes_shape", "_scales_shape")
 
     def __init__(self, rows: int, cols: int, device):
         if rows < 0 or cols < 0 or cols % MX_BLOCK:
@@ -195,28 +198,30 @@ class MxTensor:
 
     def _checked(self, name: str) -> razer_mx:
         """The struct of buffers that match the shape.  The owner of buffers that it
-        was given may have changed them since: every call looks where they are and
-        how long, and at the rest if they have moved."""
+        was given may have changed them in place since (`.data =`, `t_`, `resize_`):
+        every call looks at them, and at the rest if they are not as they were."""
         rows, cols = self._rows, self._cols
-        n = rows * cols >> 1
         if self._buf is not None:
             at = self._buf.data_ptr()
-            return razer_mx(rows, cols, at, at + n)
+            return razer_mx(rows, cols, at, at + (rows * cols >> 1))
         c, s = self._codes, self._scales
         at, scales_at = c.data_ptr(), s.data_ptr()
-        if at != self._at or scales_at != self._scales_at or c.nbytes != n or s.nbytes << 4 != n:
+        if (at != self._at or scales_at != self._scales_at or c.shape != self._codes_shape
+                or s.shape != self._scales_shape or c.dtype is not _u8 or s.dtype is not _u8
+                or not c.is_contiguous() or not s.is_contiguous()):
             self._check_buffers(name)
         return razer_mx(rows, cols, at, scales_at)
 
     def _check_buffers(self, name: str, codes_shape=None):
         c, s, rows, cols = self._codes, self._scales, self._rows, self._cols
-        index = c.get_device()
+        index, codes_shape, scales_shape = c.get_device(), codes_shape or c.shape, s.shape
         if (c.dtype is not _u8 or s.dtype is not _u8 or cols & 31 or s.get_device() != index
-                or (codes_shape or c.shape) != (rows, cols >> 1) or s.shape != (rows, cols >> 5)
+                or codes_shape != (rows, cols >> 1) or scales_shape != (rows, cols >> 5)
                 or not c.is_contiguous() or not s.is_contiguous()):
             raise ValueError(f"{name}: codes {tuple(c.shape)} {c.dtype} on {c.device} and scales {tuple(s.shape)} "
                              f"{s.dtype} on {s.device} are no contiguous uint8 MXFP4 tensor of {rows}x{cols}")
         self._device, self._index, self._at, self._scales_at = c.device, index, c.data_ptr(), s.data_ptr()
+        self._codes_shape, self._scales_shape = codes_shape, scales_shape
 
     def struct(self) -> razer_mx:
         if self._buf is not None:
