@@ -10,9 +10,10 @@ a product are I8Tensors::
     y = razer_i8_gemm(razer_i8_quantize_gated(gu), down)
 
 Streams as in ``mx``: calls run on the current stream, or on ``stream``.  No call has a
-backward: where an operand's scales require a gradient, one that reaches the result
-raises (what is written to ``out`` stands outside any graph).  The package re-exports
-every name here.
+backward: where an input requires a gradient, or an operand's scales do, one that reaches
+the result raises; the scales of an encoded tensor stand in its input's graph for that
+(what is written to ``out`` stands outside any graph).  The package re-exports every name
+here.
 """
 from __future__ import annotations
 
@@ -231,8 +232,8 @@ def _encode(call, x, parts: int, out, stream) -> I8Tensor:
     cols = width if parts == 1 else width // parts
     if cols * parts != width or cols % I8_UNIT:
         raise ValueError(f"columns must be a multiple of {parts * I8_UNIT}")
-    current = _stream(dev.index)
-    if out is None:
+    current, source, given = _stream(dev.index), x, out is not None
+    if not given:
         out = I8Tensor(rows, cols, dev)
         packed = out._struct
     else:
@@ -245,16 +246,22 @@ def _encode(call, x, parts: int, out, stream) -> I8Tensor:
     st = call(ptr, dt, ld, packed, current)
     if st:
         _check(st, call.__name__)
+    if not given and source.requires_grad and _grad_enabled():
+        # from the scales it reaches what the tensor is used in: whole numbers have no gradient
+        _without_backward(call.__name__, (out.scales,), (source,))
     return out
 
 
 def razer_i8_quantize(x: torch.Tensor, out: I8Tensor | None = None, stream=None) -> I8Tensor:
-    """8-bit encoding of x [rows, cols] (f32, f16 or bf16; cols % 16 == 0), a scale a row."""
+    """8-bit encoding of x [rows, cols] (f32, f16 or bf16; cols % 16 == 0), a scale a row.
+    There is no backward: where x requires a gradient, one that reaches the scales, or what
+    the tensor is used in, raises; what is written to out stands outside any graph."""
     return _encode(lib().razer_i8_quantize, x, 1, out, stream)
 
 
 def razer_i8_quantize_gated(gu: torch.Tensor, out: I8Tensor | None = None, stream=None) -> I8Tensor:
-    """8-bit encoding of silu(g) * u for gu [rows, 2 * cols] = [g | u]."""
+    """8-bit encoding of silu(g) * u for gu [rows, 2 * cols] = [g | u]; gradients as in
+    razer_i8_quantize."""
     return _encode(lib().razer_i8_quantize_gated, gu, 2, out, stream)
 
 
