@@ -12,8 +12,8 @@ a product are I8Tensors::
 Streams as in ``mx``: calls run on the current stream, or on ``stream``.  No call has a
 backward: where an input requires a gradient, or an operand's scales do, one that reaches
 the result raises; the scales of an encoded tensor stand in its input's graph for that
-(what is written to ``out`` stands outside any graph).  The package re-exports every name
-here.
+(what is written to ``out`` stands outside any graph).  A tangent of forward mode raises in
+the call.  The package re-exports every name here.
 """
 from __future__ import annotations
 
@@ -24,8 +24,8 @@ import struct
 import torch
 
 from . import _check_buffer, lib
-from .mx import (_check, _dtype, _entered, _grad_enabled, _on_gpu, _rows_of, _space, _stream, _Tensor,
-                 _without_backward)
+from .mx import (_check, _dtype, _entered, _forward, _grad_enabled, _no_tangents, _on_gpu, _rows_of, _space, _stream,
+                 _Tensor, _without_backward)
 
 I8_UNIT = 16
 RAZER_I8_MAX_K = 131056
@@ -215,6 +215,8 @@ def _operands(x, w):
 def _outside_graph(call: str, out, x, w):
     """out, in the graph of the scales of x and w where they require a gradient."""
     xs, ws = x._scales, w._scales  # None: nobody has seen them
+    if _forward._current_level >= 0:
+        _no_tangents(call, (xs, ws))
     if (xs is not None and xs.requires_grad or ws is not None and ws.requires_grad) and _grad_enabled():
         return _without_backward(call, (out,), (xs, ws))[0]
     return out
@@ -246,6 +248,8 @@ def _encode(call, x, parts: int, out, stream) -> I8Tensor:
     st = call(ptr, dt, ld, packed, current)
     if st:
         _check(st, call.__name__)
+    if _forward._current_level >= 0 and not given:
+        _no_tangents(call.__name__, (source,))
     if not given and source.requires_grad and _grad_enabled():
         # from the scales it reaches what the tensor is used in: whole numbers have no gradient
         _without_backward(call.__name__, (out.scales,), (source,))

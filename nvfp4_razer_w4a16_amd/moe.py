@@ -9,7 +9,7 @@ What stands before and behind the grouped products::
     y = razer_moe_combine(rows, r.slots, r.weights, add=h)
 
 Nothing here waits for the GPU, so a layer of experts can be captured in a graph.
-Streams as in ``mx``.  No call has a backward.  The package re-exports every name here.
+Streams as in ``mx``.  No call has a backward, or takes tangents of forward mode.  The package re-exports every name here.
 """
 from __future__ import annotations
 
@@ -21,7 +21,8 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _check_buffer, lib
-from .mx import _check, _dtype, _entered, _grad_enabled, _on_gpu, _stream, _Tensor, _without_backward
+from .mx import (_check, _dtype, _entered, _forward, _grad_enabled, _no_tangents, _on_gpu, _stream, _Tensor,
+                 _without_backward)
 
 RAZER_MOE_MAX_EXPERTS, RAZER_MOE_MAX_TOP, RAZER_MOE_MAX_GROUPS = 1024, 32, 64
 RAZER_SCORE_SOFTMAX, RAZER_SCORE_SIGMOID = 0, 1
@@ -173,6 +174,8 @@ def razer_moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", b
         ws, space, _stream(index))
     if status:
         _check(status, "razer_moe_route")
+    if _forward._current_level >= 0 and not given:
+        _no_tangents("razer_moe_route", (logits, bias))
     if not given and _grad_enabled() and (logits.requires_grad or bias is not None and bias.requires_grad):
         out = out._replace(weights=_without_backward("razer_moe_route", (out.weights.clone(),), (logits, bias))[0])
     return out
@@ -224,6 +227,8 @@ def razer_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
                        weights.data_ptr(), add_at, out.data_ptr()), _stream(index))
     if status:
         _check(status, "razer_moe_combine")
+    if _forward._current_level >= 0 and not given:
+        _no_tangents("razer_moe_combine", (y, weights, source))
     if not given and _grad_enabled() and (y.requires_grad or weights.requires_grad
                                           or source is not None and source.requires_grad):
         out, = _without_backward("razer_moe_combine", (out,), (y, weights, source))

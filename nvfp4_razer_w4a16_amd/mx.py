@@ -18,6 +18,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from . import _DT, RAZER_OK, RazerError, _check_buffer, lib
 
@@ -432,6 +433,14 @@ def _without_backward(call: str, results, inputs):
     return _NoBackward.apply(call, len(results), *results, *(t for t in inputs if t is not None))
 
 
+def _no_tangents(call: str, inputs):
+    """In forward mode a result would lose its inputs' tangents, so one among them raises,
+    whether or not gradients are recorded.  (_forward._current_level: -1 outside that mode.)"""
+    for t in inputs:
+        if t is not None and _forward.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{call} has no derivative in forward mode: detach its inputs")
+
+
 def _vector(t, cols: int, dtype, device, index: int, name: str) -> int:
     """Address of a weight [cols] on GPU `index`."""
     if (not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != index or t.shape != (cols,)
@@ -450,8 +459,9 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     true (by default, where post_weight is given).  gate: [cols] or
     [gate_rows, cols], gate_rows a divisor of rows.  packed: x is an MxTensor, else
     a tensor of h's dtype.  h_out (h itself, if contiguous) and x_out take the
-    results.  There is no backward: one that reaches the results raises.  What is
-    written to h_out and x_out, and a packed x, stands outside any graph."""
+    results.  There is no backward: one that reaches the results raises, as does a
+    tangent of forward mode.  What is written to h_out and x_out, and a packed x, stands
+    outside any graph."""
     if stream is not None:
         with _entered(stream):
             return razer_block_norm(y, h, post_weight=post_weight, post_norm=post_norm, gate=gate,
@@ -505,6 +515,8 @@ def razer_block_norm(y: torch.Tensor | None, h: torch.Tensor, *, post_weight=Non
     status = lib().razer_block_norm(a, _stream(index))
     if status:
         _check(status, "razer_block_norm")
+    if _forward._current_level >= 0 and (new_h or new_x):
+        _no_tangents("razer_block_norm", (y, h, post_weight, pre_weight, gate))
     if _grad_enabled() and (h.requires_grad or y is not None and y.requires_grad
                             or post_weight is not None and post_weight.requires_grad
                             or pre_weight is not None and pre_weight.requires_grad
