@@ -499,7 +499,7 @@ enum { RAZER_SCORE_SOFTMAX = 0, RAZER_SCORE_SIGMOID = 1 };
 enum { RAZER_ROUTE_RENORM = 1u };
 typedef struct razer_route {
   int64_t tokens;      /* >= 0; tokens * top < 2^30, tokens <= 2^26, with an order 2^20 (RAZER_E_UNSUPPORTED above:
-                          longer batches are routed in parts) */
+                          longer batches are routed in parts; an order's time grows with the square of the tokens) */
   int64_t stride;      /* elements from row to row of logits, >= experts */
   int32_t experts;     /* 1 .. RAZER_MOE_MAX_EXPERTS (RAZER_E_UNSUPPORTED above) */
   int32_t top;         /* 1 .. RAZER_MOE_MAX_TOP, at most the experts of the groups kept */

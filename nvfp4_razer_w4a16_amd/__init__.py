@@ -12,6 +12,9 @@ Functions carry the C names: ``razer_quantize_weight``, ``razer_quantize_act``,
 operators and the block norm, ``razer_mx_*`` and ``razer_block_norm``, are in ``mx``,
 the 8-bit integer operators, ``razer_i8_*``, in ``i8``, the routing to experts and the
 combination of their rows, ``razer_moe_*``, in ``moe``; all are re-exported here.
+
+No call has a backward.  Results of the calls here stand outside any graph; ``mx``,
+``i8`` and ``moe`` say which of theirs raise in a backward pass.
 """
 from __future__ import annotations
 

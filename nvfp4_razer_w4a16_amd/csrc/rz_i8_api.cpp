@@ -20,10 +20,13 @@ bool dtype_ok(int dt) { return dt == RAZER_F32 || dt == RAZER_F16 || dt == RAZER
 int64_t dtype_size(int dt) { return dt == RAZER_F32 ? 4 : 2; }
 
 constexpr int64_t kMaxElems = (int64_t)1 << 34;   // 8 elements a thread, a launch has fewer than 2^32 threads
+                                                  // (in each dimension: the combination, of 4 or 8, has two)
 constexpr int64_t kMaxGemmRows = (int64_t)1 << 30;
 constexpr int64_t kMaxPairs = (int64_t)1 << 30;   // of a token and a place
 constexpr int64_t kMaxTokens = (int64_t)1 << 26;  // blocks of 1024 threads, 16 or 32 tokens each, in one launch
-constexpr int64_t kMaxOrdered = (int64_t)1 << 20; // every block reads the sums of all groups of blocks
+// Every block reads the sums of all groups of blocks, which grows with the square of the
+// tokens: 8 of 256 experts of 65536 tokens 44 of the 127 us of a call, of 2^20 1.5 of 2.5 ms.
+constexpr int64_t kMaxOrdered = (int64_t)1 << 20;
 
 razer_status check_i8(const razer_i8* t) {
   if (!t || t->rows < 0 || t->cols < 0 || t->cols % 16 != 0) return RAZER_E_INVALID;

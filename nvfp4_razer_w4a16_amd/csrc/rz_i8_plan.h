@@ -175,6 +175,8 @@ inline StreamPlan stream_plan(int64_t m, int64_t n, int64_t k, int64_t experts, 
 //   100 x 2000 x 2000   7.3 and 10.7     64 x 2048 x 8192    14.5 and 17.4
 //   8 experts of 14336 x 4096, 16 rows each 96 and 116, 64 rows 116 and 123, 128 rows 204 and 146
 //   64 experts of 1536 x 2048, 8 rows each 37.0 and 47.9, 32 rows 53.6 and 52.6
+// Few rows above K = 16384, which have the tile kernel alone, were not measured: how those
+// are cut follows from the fits above.
 struct Estimate {
   double stream, tile;
 };

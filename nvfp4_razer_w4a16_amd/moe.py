@@ -54,7 +54,9 @@ _combine_bytes = struct.Struct("qqqqqqi4xPPPPP").pack
 class MoeRoutes(NamedTuple):
     """experts, weights, slots: [tokens, top]; offsets: [E + 1]; rows: [tokens * top].  All are
     int32 but the weights, float32; offsets, rows and slots are None where no order was asked
-    for.  Expert and slot -1: a place that no expert takes (weight 0)."""
+    for.  Expert and slot -1: a place that no expert takes (weight 0).  The results of a call
+    that was given none are views of one buffer, which its workspace is a part of: to keep
+    one of them alone, copy it."""
     experts: torch.Tensor
     weights: torch.Tensor
     offsets: Optional[torch.Tensor]

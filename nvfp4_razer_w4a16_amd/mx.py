@@ -10,7 +10,8 @@ scale byte each.  Both operands of a product are MxTensors::
 
 Calls run on the current stream; with ``stream`` they run as inside
 ``torch.cuda.stream(stream)``, and what they return belongs to that stream.  No
-call has a backward.  The package re-exports every name here.
+call has a backward: the block norm's plain results raise in one, packed tensors and
+what they are used in stand outside any graph.  The package re-exports every name here.
 """
 from __future__ import annotations
 
